@@ -49,7 +49,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
     if not (force or needs_build()):
         return LIB
     tmp = LIB + f".tmp{os.getpid()}"
-    cmd = [_nvcc(), "-O3", "-std=c++17", *ARCH, "-lineinfo", "--shared", "-Xcompiler", "-fPIC",
+    cmd = [_nvcc(), "-O3", "-std=c++17", "--threads", "0", *ARCH, "-lineinfo", "--shared", "-Xcompiler", "-fPIC",
            "-Xcompiler", "-fvisibility=hidden", "-I", INCLUDE, "-I", CSRC,
            "-o", tmp, *_sources()]
     if verbose:

@@ -16,6 +16,7 @@
 #include <vector>
 
 #include "b200gemm.h"
+#include "host.h"
 #include "gemm_bf16_sm100.cuh"
 #include "gemm_bf16_skinny_sm100.cuh"
 #include "gemm_bf16_small_sm100.cuh"
@@ -67,7 +68,7 @@ using CfgSk128B16 = b200::GemmSkinnyCfg<128, 6, 1>;
 using CfgSk256F32 = b200::GemmSkinnyCfg<256, 4, 0>;
 using CfgSk256B16 = b200::GemmSkinnyCfg<256, 4, 1>;
 
-constexpr int kMaxDevices = 64;
+using b200::host::kMaxDevices;
 // internal configuration slot of the CLC pair kernel with further copies of C
 constexpr gemm_config_t kCfgAllgather = static_cast<gemm_config_t>(GEMM_CFG_COUNT_);
 
@@ -261,7 +262,7 @@ bool overlaps(const void *p, int64_t rows, int64_t cols, int64_t ld, int64_t esi
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
-constexpr int64_t kMaxDim = 0x7FFFFFFF;
+using b200::host::kMaxDim;
 
 // Checks shared by every entry point.  elem sizes in bytes; a_mn / b_mn:
 // A stored K x M, B stored K x N (else M x K and N x K).
@@ -1082,6 +1083,29 @@ gemm_status_t launch_mxf8(DeviceState *st, int attr_slot, const void *A, const u
 }
 
 }  // namespace
+
+// The helpers of host.h, for the entry points in other source files.
+namespace b200 {
+namespace host {
+
+gemm_status_t cuda_fail(cudaError_t e) { return ::cuda_fail(e); }
+
+gemm_status_t device(int &dev, int &sm_count, cudaStream_t stream) {
+    DeviceState *st = nullptr;
+    const gemm_status_t s = current_device(dev, st, stream);
+    if (s == GEMM_OK) sm_count = st->sm_count;
+    return s;
+}
+
+bool capturing(cudaStream_t stream) { return ::capturing(stream); }
+
+bool overlaps(const void *p, int64_t rows, int64_t cols, int64_t ld, int64_t esize, const void *q, int64_t qrows,
+              int64_t qcols, int64_t qld, int64_t qesize) {
+    return ::overlaps(p, rows, cols, ld, esize, q, qrows, qcols, qld, qesize);
+}
+
+}  // namespace host
+}  // namespace b200
 
 extern "C" {
 

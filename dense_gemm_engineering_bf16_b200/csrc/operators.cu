@@ -1,0 +1,408 @@
+// Host side of the operators around the products (include/b200gemm.h): the
+// RMS norm, the MXFP8 quantiser and the product with 4-bit weights.  Argument
+// checks first, then one launch (two where a sum over rows needs its own).
+// None of them keeps state, allocates or synchronises.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cstdint>
+
+#include "b200gemm.h"
+#include "gemm_w4_sm100.cuh"
+#include "host.h"
+#include "mxfp8_quantize_sm100.cuh"
+#include "rmsnorm_sm100.cuh"
+
+namespace {
+
+using b200::kBF16;
+using b200::kF32;
+using b200::kNone;
+using b200::host::aligned16;
+using b200::host::kMaxDim;
+using b200::host::overlaps;
+
+bool valid_type(gemm_out_t t) { return t == GEMM_OUT_F32 || t == GEMM_OUT_BF16; }
+int64_t size_of(gemm_out_t t) { return t == GEMM_OUT_F32 ? 4 : 2; }
+
+// One matrix of a call: rows x cols elements of `esize` bytes, pitch ld.
+struct Mat {
+    const void *p;
+    int64_t rows, cols, ld, esize;
+};
+
+// Pointer, pitch and alignment of a matrix that the call touches.
+gemm_status_t check_mat(const Mat &m) {
+    if (!m.p || m.ld < m.cols) return GEMM_ERR_INVALID_VALUE;
+    if (!aligned16(m.p) || (m.ld * m.esize) % 16) return GEMM_ERR_MISALIGNED;
+    if (m.ld * m.esize >= (int64_t(1) << 40)) return GEMM_ERR_TOO_LARGE;
+    return GEMM_OK;
+}
+
+bool overlap(const Mat &a, const Mat &b) {
+    return overlaps(a.p, a.rows, a.cols, a.ld, a.esize, b.p, b.rows, b.cols, b.ld, b.esize);
+}
+
+// The same matrix in the same place: element (i, j) of one is (i, j) of the other.
+bool same(const Mat &a, const Mat &b) { return a.p == b.p && a.ld == b.ld && a.esize == b.esize; }
+
+// A matrix that is written may overlap nothing else of the call.
+template <size_t N>
+bool any_overlap(const Mat &out, const Mat (&others)[N]) {
+    for (const Mat &o : others)
+        if (overlap(out, o)) return true;
+    return false;
+}
+
+gemm_status_t launched() {
+    const cudaError_t e = cudaGetLastError();
+    return e == cudaSuccess ? GEMM_OK : b200::host::cuda_fail(e);
+}
+
+int round_up(int64_t n, int m) { return static_cast<int>((n + m - 1) / m * m); }
+
+// ---------------------------------------------------------------- RMS norm --
+
+// Threads and vectors of eight per thread for a row of K elements.  Up to
+// 1024 elements a warp holds the row, and eight rows share a block.  Longer
+// rows take a block each: with fewer rows than would fill the SMs, one vector
+// per thread (the shortest chain of loads); else four, which leaves room for
+// several blocks per SM.  VPT 0: the row does not fit into registers.
+struct RowShape {
+    int vpt;
+    dim3 block;
+};
+
+RowShape row_shape(int64_t K, bool few_rows) {
+    const int64_t vecs = (K + 7) / 8;
+    if (vecs <= 128) return {vecs <= 32 ? 1 : vecs <= 64 ? 2 : 4, dim3(32, 8)};
+    if (vecs <= 1024 && few_rows) return {1, dim3(static_cast<unsigned>(round_up(vecs, 32)))};
+    if (vecs <= 4 * 512) return {4, dim3(static_cast<unsigned>(round_up((vecs + 3) / 4, 32)))};
+    return {0, dim3(1024)};
+}
+
+template <int XT, int HT, int VPT>
+gemm_status_t launch_norm(int dev, const b200::RmsnormArgs &a, dim3 block, cudaStream_t stream) {
+    const int64_t blocks = (a.M + block.y - 1) / block.y;
+    gemm_status_t s;
+    if constexpr (VPT == 0) {
+        if ((s = b200::host::prepare<b200::rmsnorm_long_kernel<XT, HT>>(dev, 0, stream)) != GEMM_OK) return s;
+        b200::rmsnorm_long_kernel<XT, HT><<<static_cast<unsigned>(blocks), block, 0, stream>>>(a);
+    } else {
+        if ((s = b200::host::prepare<b200::rmsnorm_kernel<XT, HT, VPT>>(dev, 0, stream)) != GEMM_OK) return s;
+        b200::rmsnorm_kernel<XT, HT, VPT><<<static_cast<unsigned>(blocks), block, 0, stream>>>(a);
+    }
+    return launched();
+}
+
+template <int XT, int HT>
+gemm_status_t dispatch_norm(int dev, int sm_count, const b200::RmsnormArgs &a, cudaStream_t stream) {
+    const RowShape r = row_shape(a.K, a.M <= 2 * sm_count);
+    switch (r.vpt) {
+        case 1: return launch_norm<XT, HT, 1>(dev, a, r.block, stream);
+        case 2: return launch_norm<XT, HT, 2>(dev, a, r.block, stream);
+        case 4: return launch_norm<XT, HT, 4>(dev, a, r.block, stream);
+        default: return launch_norm<XT, HT, 0>(dev, a, r.block, stream);
+    }
+}
+
+template <int XT>
+gemm_status_t dispatch_norm_h(int dev, int sm_count, const b200::RmsnormArgs &a, int ht, cudaStream_t stream) {
+    if (ht == kNone) return dispatch_norm<XT, kNone>(dev, sm_count, a, stream);
+    return ht == kF32 ? dispatch_norm<XT, kF32>(dev, sm_count, a, stream)
+                      : dispatch_norm<XT, kBF16>(dev, sm_count, a, stream);
+}
+
+// Blocks of the backward pass, at most: the rows of its workspace.
+constexpr int64_t kPartialRows = 296;
+
+template <int YT, int HT, int DT, int VPT>
+gemm_status_t launch_back(int dev, int sm_count, b200::RmsnormBackArgs a, dim3 block, float *dw, float *ws,
+                          cudaStream_t stream) {
+    constexpr int kAccBytes = VPT * 8 * 32 * 4;
+    const int64_t per_sm = block.x * block.y <= 512 ? 2 : 1;
+    const int64_t rows = (a.M + block.y - 1) / block.y;
+    const int64_t blocks = std::min({rows, per_sm * sm_count, kPartialRows});
+    // one block's share of dw is dw itself
+    if (dw) a.partial = blocks == 1 ? dw : ws;
+    gemm_status_t s;
+    if (dw && blocks > 1 && (s = b200::host::prepare<b200::rmsnorm_dw_kernel>(dev, 0, stream)) != GEMM_OK) return s;
+    if constexpr (VPT == 0) {
+        if ((s = b200::host::prepare<b200::rmsnorm_back_long_kernel<YT, HT, DT>>(dev, 0, stream)) != GEMM_OK) return s;
+        b200::rmsnorm_back_long_kernel<YT, HT, DT><<<static_cast<unsigned>(blocks), block, 0, stream>>>(a);
+    } else {
+        if ((s = b200::host::prepare<b200::rmsnorm_back_kernel<YT, HT, DT, VPT>>(dev, 0, stream)) != GEMM_OK) return s;
+        b200::rmsnorm_back_kernel<YT, HT, DT, VPT>
+            <<<static_cast<unsigned>(blocks), block, block.y > 1 ? kAccBytes : 0, stream>>>(a);
+    }
+    if ((s = launched()) != GEMM_OK || !dw || blocks == 1) return s;
+    cudaLaunchConfig_t lc = {};
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    lc.gridDim = dim3(static_cast<unsigned>((a.K + 31) / 32));
+    lc.blockDim = dim3(256);
+    lc.stream = stream;
+    lc.attrs = &attr;
+    lc.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&lc, b200::rmsnorm_dw_kernel, static_cast<const float *>(ws), dw, blocks, a.K);
+    return e == cudaSuccess ? GEMM_OK : b200::host::cuda_fail(e);
+}
+
+template <int YT, int HT, int DT>
+gemm_status_t dispatch_back(int dev, int sm_count, const b200::RmsnormBackArgs &a, float *dw, float *ws,
+                            cudaStream_t stream) {
+    const RowShape r = row_shape(a.K, a.M <= 2 * sm_count);
+    switch (r.vpt) {
+        case 1: return launch_back<YT, HT, DT, 1>(dev, sm_count, a, r.block, dw, ws, stream);
+        case 2: return launch_back<YT, HT, DT, 2>(dev, sm_count, a, r.block, dw, ws, stream);
+        case 4: return launch_back<YT, HT, DT, 4>(dev, sm_count, a, r.block, dw, ws, stream);
+        default: return launch_back<YT, HT, DT, 0>(dev, sm_count, a, r.block, dw, ws, stream);
+    }
+}
+
+// --------------------------------------------------------- MXFP8 quantiser --
+
+template <int XT>
+gemm_status_t launch_quantize(int dev, const void *X, uint8_t *Q, uint8_t *sf, int64_t M, int64_t K, int64_t ldx,
+                              int64_t ldq, gemm_layout_t layout, cudaStream_t stream) {
+    gemm_status_t s;
+    if (layout == GEMM_LAYOUT_MNMAJOR) {
+        const int64_t k_tiles = (K + 127) / 128, blocks = k_tiles * ((M + 63) / 64);
+        if (blocks > kMaxDim) return GEMM_ERR_TOO_LARGE;
+        if ((s = b200::host::prepare<b200::mx_quantize_mn_kernel<XT>>(dev, 0, stream)) != GEMM_OK) return s;
+        b200::mx_quantize_mn_kernel<XT><<<static_cast<unsigned>(blocks), 128, 0, stream>>>(X, Q, sf, M, K, ldx, ldq,
+                                                                                         k_tiles);
+        return launched();
+    }
+    constexpr int VPT = 4;
+    const int64_t vecs = K / 8;
+    const dim3 block = vecs <= 32 * VPT ? dim3(32, 8) : dim3(static_cast<unsigned>(std::min(256, round_up((vecs + VPT - 1) / VPT, 32))));
+    const int64_t parts = (vecs + VPT * block.x - 1) / (VPT * block.x);
+    if (parts > 65535) return GEMM_ERR_TOO_LARGE;
+    if ((s = b200::host::prepare<b200::mx_quantize_kernel<XT, VPT>>(dev, 0, stream)) != GEMM_OK) return s;
+    b200::mx_quantize_kernel<XT, VPT>
+        <<<dim3(static_cast<unsigned>((M + block.y - 1) / block.y), static_cast<unsigned>(parts)), block, 0, stream>>>(
+            X, Q, sf, M, K, ldx, ldq);
+    return launched();
+}
+
+// ------------------------------------------------------- 4-bit weights --
+
+template <int NT, int MT, int U>
+gemm_status_t launch_w4(int dev, int sm_count, b200::W4Args a, cudaStream_t stream) {
+    constexpr int S = 4;
+    constexpr int kXBytes = 32 * 1024;
+    constexpr int kRing = S * b200::kW4StageBytes;
+    constexpr int kMaxSmem = kRing + std::max(kXBytes, 8 * NT * (2 * b200::kW4K + 64)) + 8 * NT * 64;
+    auto kernel = b200::gemm_w4_kernel<NT, MT, U, S>;
+    gemm_status_t s;
+    if ((s = b200::host::prepare<b200::gemm_w4_kernel<NT, MT, U, S>>(dev, kMaxSmem, stream)) != GEMM_OK) return s;
+    const int64_t tiles = (a.N + b200::kW4Rows - 1) / b200::kW4Rows;
+    const int64_t token_blocks = (a.M + 8 * NT - 1) / (8 * NT);
+    const int64_t stages = (a.K + b200::kW4K - 1) / b200::kW4K;
+    int64_t split = 1;
+    while (split < 8 && tiles * token_blocks * split < 2 * sm_count && 2 * split <= stages) split *= 2;
+    if (token_blocks > kMaxDim / 8 || tiles * token_blocks > kMaxDim / split) return GEMM_ERR_TOO_LARGE;
+    a.token_blocks = static_cast<int>(token_blocks);
+    const int tokens = static_cast<int>(std::min<int64_t>(a.M, 8 * NT));
+    const int64_t share = (stages + split - 1) / split;
+    a.x_stages = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(share, kXBytes / (tokens * 2 * b200::kW4K))));
+    a.x_pitch = a.x_stages * 2 * b200::kW4K + 64;
+    const int smem = kRing + tokens * a.x_pitch;
+    cudaLaunchConfig_t lc = {};
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = static_cast<unsigned>(split);
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    lc.gridDim = dim3(static_cast<unsigned>(tiles * token_blocks * split));
+    lc.blockDim = dim3(32 * (b200::kW4Rows / (16 * MT)));
+    lc.dynamicSmemBytes = static_cast<size_t>(smem);
+    lc.stream = stream;
+    lc.attrs = &attr;
+    lc.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&lc, kernel, a);
+    return e == cudaSuccess ? GEMM_OK : b200::host::cuda_fail(e);
+}
+
+template <int NT, int MT>
+gemm_status_t dispatch_w4(int dev, int sm_count, const b200::W4Args &a, cudaStream_t stream) {
+    switch (a.group_shift) {
+        case 5: return launch_w4<NT, MT, 1>(dev, sm_count, a, stream);
+        case 6: return launch_w4<NT, MT, 2>(dev, sm_count, a, stream);
+        case 7: return launch_w4<NT, MT, 4>(dev, sm_count, a, stream);
+        default: return launch_w4<NT, MT, 8>(dev, sm_count, a, stream);
+    }
+}
+
+gemm_status_t zero_rows(void *p, int64_t rows, int64_t cols, int64_t ld, int64_t esize, cudaStream_t stream) {
+    const cudaError_t e = rows == 1 ? cudaMemsetAsync(p, 0, static_cast<size_t>(cols * esize), stream)
+                                    : cudaMemset2DAsync(p, static_cast<size_t>(ld * esize), 0,
+                                                        static_cast<size_t>(cols * esize), static_cast<size_t>(rows),
+                                                        stream);
+    return e == cudaSuccess ? GEMM_OK : b200::host::cuda_fail(e);
+}
+
+}  // namespace
+
+extern "C" {
+
+gemm_status_t gemm_rmsnorm(const void *X, const void *R, void *H, const float *weight, void *Y, uint8_t *Q, uint8_t *sf,
+                           float *rstd, int64_t M, int64_t K, int64_t ldx, int64_t ldr, int64_t ldh, int64_t ldy,
+                           int64_t ldq, gemm_out_t x_type, gemm_out_t h_type, float eps, cudaStream_t stream) {
+    if (M < 0 || K < 0) return GEMM_ERR_INVALID_VALUE;
+    if (M > kMaxDim || K > kMaxDim) return GEMM_ERR_TOO_LARGE;
+    if (!valid_type(x_type) || (R && !valid_type(h_type)) || !(eps > 0.0f)) return GEMM_ERR_INVALID_VALUE;
+    if (M == 0 || K == 0) return GEMM_OK;
+    if (!X || !weight || (!Y && !Q) || (H && !R) || (Q && !sf)) return GEMM_ERR_INVALID_VALUE;
+    if (Q && K % 32) return GEMM_ERR_INVALID_VALUE;
+    if (!aligned16(weight)) return GEMM_ERR_MISALIGNED;
+    const Mat none{nullptr, 0, 0, 0, 1};
+    const Mat mx{X, M, K, ldx, size_of(x_type)};
+    const Mat mr = R ? Mat{R, M, K, ldr, size_of(h_type)} : none;
+    const Mat mh = H ? Mat{H, M, K, ldh, size_of(h_type)} : none;
+    const Mat my = Y ? Mat{Y, M, K, ldy, 2} : none;
+    const Mat mq = Q ? Mat{Q, M, K, ldq, 1} : none;
+    const Mat mw{weight, 1, K, K, 4};
+    const Mat ms = Q ? Mat{sf, 1, M * (K / 32), M * (K / 32), 1} : none;
+    const Mat mt = rstd ? Mat{rstd, 1, M, M, 4} : none;
+    gemm_status_t s;
+    for (const Mat *m : {&mx, &mr, &mh, &my, &mq})
+        if (m->p && (s = check_mat(*m)) != GEMM_OK) return s;
+    if (rstd && (reinterpret_cast<uintptr_t>(rstd) & 3u)) return GEMM_ERR_MISALIGNED;
+    // outputs overlap nothing, except H, which may be R itself
+    if (any_overlap(mh, {mx, same(mh, mr) ? none : mr, mw, my, mq, ms, mt}) ||
+        any_overlap(my, {mx, mr, mw, mq, ms, mt}) || any_overlap(mq, {mx, mr, mw, ms, mt}) ||
+        any_overlap(ms, {mx, mr, mw, mt}) || any_overlap(mt, {mx, mr, mw}))
+        return GEMM_ERR_ALIAS;
+    int dev, sm_count;
+    if ((s = b200::host::device(dev, sm_count, stream)) != GEMM_OK) return s;
+    const b200::RmsnormArgs a{X, R, H, weight, Y, Q, sf, rstd, M, K, ldx, ldr, ldh, ldy, ldq, eps};
+    const int ht = !R ? kNone : h_type == GEMM_OUT_F32 ? kF32 : kBF16;
+    return x_type == GEMM_OUT_F32 ? dispatch_norm_h<kF32>(dev, sm_count, a, ht, stream)
+                                  : dispatch_norm_h<kBF16>(dev, sm_count, a, ht, stream);
+}
+
+int64_t gemm_rmsnorm_backward_workspace(int64_t M, int64_t K) {
+    if (M <= 0 || K <= 0 || M > kMaxDim || K > kMaxDim) return 0;
+    return std::min(M, kPartialRows) * K * 4;
+}
+
+gemm_status_t gemm_rmsnorm_backward(const void *dY, const void *H, const float *weight, const float *rstd, const void *dR,
+                                    void *dH, float *dW, void *workspace, int64_t workspace_bytes, int64_t M, int64_t K,
+                                    int64_t lddy, int64_t ldh, int64_t lddr, int64_t lddh, gemm_out_t dy_type,
+                                    gemm_out_t h_type, gemm_out_t dh_type, cudaStream_t stream) {
+    if (M < 0 || K < 0) return GEMM_ERR_INVALID_VALUE;
+    if (M > kMaxDim || K > kMaxDim) return GEMM_ERR_TOO_LARGE;
+    if (!valid_type(dy_type) || !valid_type(h_type) || !valid_type(dh_type)) return GEMM_ERR_INVALID_VALUE;
+    if (K == 0) return GEMM_OK;
+    gemm_status_t s;
+    int dev, sm_count;
+    const Mat none{nullptr, 0, 0, 0, 1};
+    if (dW && !aligned16(dW)) return GEMM_ERR_MISALIGNED;
+    if (M == 0) {   // the empty sum
+        if (!dW) return GEMM_OK;
+        if ((s = b200::host::device(dev, sm_count, stream)) != GEMM_OK) return s;
+        return zero_rows(dW, 1, K, K, 4, stream);
+    }
+    if (!dY || !H || !weight || !rstd || !dH) return GEMM_ERR_INVALID_VALUE;
+    const int64_t need = dW ? gemm_rmsnorm_backward_workspace(M, K) : 0;
+    if (dW && (!workspace || workspace_bytes < need)) return GEMM_ERR_INVALID_VALUE;
+    if (!aligned16(weight) || (dW && !aligned16(workspace)) || (reinterpret_cast<uintptr_t>(rstd) & 3u))
+        return GEMM_ERR_MISALIGNED;
+    const Mat my{dY, M, K, lddy, size_of(dy_type)};
+    const Mat mh{H, M, K, ldh, size_of(h_type)};
+    const Mat mr = dR ? Mat{dR, M, K, lddr, size_of(dh_type)} : none;
+    const Mat md{dH, M, K, lddh, size_of(dh_type)};
+    const Mat mw{weight, 1, K, K, 4};
+    const Mat mt{rstd, 1, M, M, 4};
+    const Mat mg = dW ? Mat{dW, 1, K, K, 4} : none;
+    const Mat mp = dW ? Mat{workspace, 1, need, need, 1} : none;
+    for (const Mat *m : {&my, &mh, &mr, &md})
+        if (m->p && (s = check_mat(*m)) != GEMM_OK) return s;
+    // outputs overlap nothing, except dH, which may be dY or dR itself
+    if (any_overlap(md, {same(md, my) ? none : my, same(md, mr) ? none : mr, mh, mw, mt, mg, mp}) ||
+        any_overlap(mg, {my, mh, mr, mw, mt, mp}) || any_overlap(mp, {my, mh, mr, mw, mt}))
+        return GEMM_ERR_ALIAS;
+    if ((s = b200::host::device(dev, sm_count, stream)) != GEMM_OK) return s;
+    const b200::RmsnormBackArgs a{dY, H, weight, rstd, dR, dH, nullptr, M, K, lddy, ldh, lddr, lddh};
+    float *ws = static_cast<float *>(workspace);
+    const int key = (dy_type == GEMM_OUT_F32 ? 4 : 0) | (h_type == GEMM_OUT_F32 ? 2 : 0) | (dh_type == GEMM_OUT_F32 ? 1 : 0);
+    switch (key) {
+        case 0: return dispatch_back<kBF16, kBF16, kBF16>(dev, sm_count, a, dW, ws, stream);
+        case 1: return dispatch_back<kBF16, kBF16, kF32>(dev, sm_count, a, dW, ws, stream);
+        case 2: return dispatch_back<kBF16, kF32, kBF16>(dev, sm_count, a, dW, ws, stream);
+        case 3: return dispatch_back<kBF16, kF32, kF32>(dev, sm_count, a, dW, ws, stream);
+        case 4: return dispatch_back<kF32, kBF16, kBF16>(dev, sm_count, a, dW, ws, stream);
+        case 5: return dispatch_back<kF32, kBF16, kF32>(dev, sm_count, a, dW, ws, stream);
+        case 6: return dispatch_back<kF32, kF32, kBF16>(dev, sm_count, a, dW, ws, stream);
+        default: return dispatch_back<kF32, kF32, kF32>(dev, sm_count, a, dW, ws, stream);
+    }
+}
+
+gemm_status_t gemm_mxfp8_quantize(const void *X, uint8_t *Q, uint8_t *sf, int64_t M, int64_t K, int64_t ldx, int64_t ldq,
+                                  gemm_out_t x_type, gemm_layout_t layout, cudaStream_t stream) {
+    if (M < 0 || K < 0) return GEMM_ERR_INVALID_VALUE;
+    if (M > kMaxDim || K > kMaxDim) return GEMM_ERR_TOO_LARGE;
+    if (!valid_type(x_type) || (layout != GEMM_LAYOUT_KMAJOR && layout != GEMM_LAYOUT_MNMAJOR) || K % 32)
+        return GEMM_ERR_INVALID_VALUE;
+    if (M == 0 || K == 0) return GEMM_OK;
+    if (!X || !Q || !sf) return GEMM_ERR_INVALID_VALUE;
+    const bool mn = layout == GEMM_LAYOUT_MNMAJOR;
+    const Mat mx{X, mn ? K : M, mn ? M : K, ldx, size_of(x_type)};
+    const Mat mq{Q, M, K, ldq, 1};
+    const Mat ms{sf, 1, M * (K / 32), M * (K / 32), 1};
+    gemm_status_t s;
+    if ((s = check_mat(mx)) != GEMM_OK || (s = check_mat(mq)) != GEMM_OK) return s;
+    if (overlap(mq, mx) || overlap(mq, ms) || overlap(ms, mx)) return GEMM_ERR_ALIAS;
+    int dev, sm_count;
+    if ((s = b200::host::device(dev, sm_count, stream)) != GEMM_OK) return s;
+    return x_type == GEMM_OUT_F32 ? launch_quantize<kF32>(dev, X, Q, sf, M, K, ldx, ldq, layout, stream)
+                                  : launch_quantize<kBF16>(dev, X, Q, sf, M, K, ldx, ldq, layout, stream);
+}
+
+gemm_status_t gemm_bf16_w4(const void *A, const uint8_t *B, const void *scales, const uint8_t *zeros, void *C, int64_t M,
+                           int64_t N, int64_t K, int64_t lda, int64_t ldb, int64_t lds, int64_t ldc, int64_t group,
+                           gemm_out_t c_type, cudaStream_t stream) {
+    if (M < 0 || N < 0 || K < 0) return GEMM_ERR_INVALID_VALUE;
+    if (M > kMaxDim || N > kMaxDim || K > kMaxDim) return GEMM_ERR_TOO_LARGE;
+    if (!valid_type(c_type) || K % 32 || group < 32 || (group & (group - 1))) return GEMM_ERR_INVALID_VALUE;
+    if (M == 0 || N == 0) return GEMM_OK;
+    const int64_t ec = size_of(c_type);
+    const Mat mc{C, M, N, ldc, ec};
+    gemm_status_t s;
+    if ((s = check_mat(mc)) != GEMM_OK) return s;
+    int dev, sm_count;
+    if (K == 0) {   // the empty sum
+        if ((s = b200::host::device(dev, sm_count, stream)) != GEMM_OK) return s;
+        return zero_rows(C, M, N, ldc, ec, stream);
+    }
+    const int64_t groups = (K + group - 1) / group;
+    const Mat ma{A, M, K, lda, 2};
+    const Mat mb{B, N, K / 2, ldb, 1};
+    const Mat ms{scales, N, groups, lds, 2};
+    const Mat mz{zeros, N, groups, lds, 1};
+    for (const Mat *m : {&ma, &mb, &ms, &mz})
+        if ((m != &mz || zeros) && (s = check_mat(*m)) != GEMM_OK) return s;
+    if (lds % 16) return GEMM_ERR_MISALIGNED;   // rows of zeros too, whether given or not
+    if (any_overlap(mc, {ma, mb, ms, mz})) return GEMM_ERR_ALIAS;
+    if ((s = b200::host::device(dev, sm_count, stream)) != GEMM_OK) return s;
+    int shift = 5;
+    while ((int64_t(1) << shift) < group && shift < 40) ++shift;
+    b200::W4Args a{};
+    a.a = static_cast<const uint16_t *>(A);
+    a.b = B;
+    a.scales = static_cast<const uint16_t *>(scales);
+    a.zeros = zeros;
+    a.c = C;
+    a.M = M, a.N = N, a.K = K, a.lda = lda, a.ldb = ldb, a.lds = lds, a.ldc = ldc;
+    a.groups = groups;
+    a.group_shift = shift;
+    a.out = c_type == GEMM_OUT_F32 ? kF32 : kBF16;
+    if (M <= 8) return dispatch_w4<1, 1>(dev, sm_count, a, stream);
+    if (M <= 16) return dispatch_w4<2, 1>(dev, sm_count, a, stream);
+    if (M <= 32) return dispatch_w4<4, 2>(dev, sm_count, a, stream);
+    return dispatch_w4<8, 2>(dev, sm_count, a, stream);
+}
+
+}  // extern "C"

@@ -1,0 +1,180 @@
+// Row-wise building blocks of the operators around the products: 16-byte
+// vectors of eight elements (bf16 or fp32), fixed-order sums, and the MXFP8
+// encoding of 32 consecutive values.
+#pragma once
+#include <cuda_bf16.h>
+
+#include <cstdint>
+
+namespace b200 {
+
+// Element types, numbered as gemm_out_t; kNone: no such operand.
+constexpr int kF32 = 0, kBF16 = 1, kNone = 2;
+
+template <int T>
+constexpr int elem_bytes = T == kF32 ? 4 : 2;
+
+// Eight consecutive elements as they are in memory.
+template <int T>
+struct Raw8 {
+    uint4 v[T == kF32 ? 2 : 1];
+};
+
+// Elements [e, e + 8) of a row, the first n of them valid (n may be below 0 or
+// above 8); the others read as zero without touching memory.  e is a multiple
+// of 8 and the row 16-byte aligned, so a full vector is one or two 16-byte
+// loads.
+template <int T>
+__device__ __forceinline__ Raw8<T> load_raw8(const void *row, int64_t e, int64_t n) {
+    Raw8<T> r;
+    const uint8_t *p = static_cast<const uint8_t *>(row) + e * elem_bytes<T>;
+    if (n >= 8) {
+#pragma unroll
+        for (int i = 0; i < (T == kF32 ? 2 : 1); ++i) r.v[i] = reinterpret_cast<const uint4 *>(p)[i];
+        return r;
+    }
+    uint32_t w[T == kF32 ? 8 : 4] = {};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        if (i < n) {
+            if constexpr (T == kF32) w[i] = reinterpret_cast<const uint32_t *>(p)[i];
+            else w[i / 2] |= static_cast<uint32_t>(reinterpret_cast<const uint16_t *>(p)[i]) << (16 * (i & 1));
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < (T == kF32 ? 2 : 1); ++i) r.v[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+    return r;
+}
+
+template <int T>
+__device__ __forceinline__ void widen8(const Raw8<T> &r, float (&f)[8]) {
+    if constexpr (T == kF32) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            f[4 * i] = __uint_as_float(r.v[i].x);
+            f[4 * i + 1] = __uint_as_float(r.v[i].y);
+            f[4 * i + 2] = __uint_as_float(r.v[i].z);
+            f[4 * i + 3] = __uint_as_float(r.v[i].w);
+        }
+    } else {
+        const uint32_t w[4] = {r.v[0].x, r.v[0].y, r.v[0].z, r.v[0].w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {   // a bf16 is the upper half of its fp32
+            f[2 * i] = __uint_as_float(w[i] << 16);
+            f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+        }
+    }
+}
+
+template <int T>
+__device__ __forceinline__ void load8(const void *row, int64_t e, int64_t n, float (&f)[8]) {
+    widen8<T>(load_raw8<T>(row, e, n), f);
+}
+
+__device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
+    const __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&p);
+}
+
+// Writes elements [e, e + 8) of a row, the first n of them, rounded to T
+// (nearest even); nothing outside them is written.
+template <int T>
+__device__ __forceinline__ void store8(void *row, int64_t e, int64_t n, const float (&f)[8]) {
+    uint8_t *p = static_cast<uint8_t *>(row) + e * elem_bytes<T>;
+    if (n >= 8) {
+        if constexpr (T == kF32) {
+            reinterpret_cast<float4 *>(p)[0] = make_float4(f[0], f[1], f[2], f[3]);
+            reinterpret_cast<float4 *>(p)[1] = make_float4(f[4], f[5], f[6], f[7]);
+        } else {
+            *reinterpret_cast<uint4 *>(p) = make_uint4(bf16_pair(f[0], f[1]), bf16_pair(f[2], f[3]),
+                                                       bf16_pair(f[4], f[5]), bf16_pair(f[6], f[7]));
+        }
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        if (i < n) {
+            if constexpr (T == kF32) reinterpret_cast<float *>(p)[i] = f[i];
+            else reinterpret_cast<__nv_bfloat16 *>(p)[i] = __float2bfloat16_rn(f[i]);
+        }
+    }
+}
+
+// The values as they will read back once stored as T.
+template <int T>
+__device__ __forceinline__ void round8(float (&f)[8]) {
+    if constexpr (T == kBF16) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] = __bfloat162float(__float2bfloat16_rn(f[i]));
+    }
+}
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+    for (int m = 16; m > 0; m >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, m);
+    return v;
+}
+
+// ------------------------------------------------------------------ MXFP8 --
+//
+// A block is 32 consecutive values along K.  Its scale is the smallest power
+// of two 2^e, e in [-127, 127], with |v| <= 448 * 2^e for every finite v of the
+// block (448 is E4M3's largest value), so no finite value saturates; a code
+// is v / 2^e rounded to nearest even.  NaN and infinities get E4M3's NaN code
+// 0x7F and do not count for the scale (E4M3 has no infinity).
+
+// Largest finite |v| of 8 values, as the bits of a non-negative fp32 (which
+// order as the values do).
+__device__ __forceinline__ uint32_t finite_max_bits(const float (&v)[8]) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const uint32_t b = __float_as_uint(v[i]) & 0x7FFFFFFFu;
+        m = max(m, b < 0x7F800000u ? b : 0u);
+    }
+    return m;
+}
+
+// The E8M0 byte (e + 127) for a block whose largest magnitude has these bits:
+// with amax = 1.f * 2^(E-127) and 448 = 1.75 * 2^8, e = E - 127 - 8, one more
+// where 1.f > 1.75.  Blocks of zeros and of values below 448 * 2^-127 get byte 0.
+__device__ __forceinline__ uint32_t mx_scale_byte(uint32_t amax_bits) {
+    const int b = static_cast<int>(amax_bits >> 23) - 8 + ((amax_bits & 0x7FFFFFu) > 0x600000u ? 1 : 0);
+    return static_cast<uint32_t>(max(b, 0));
+}
+
+// 2^-e for an E8M0 byte e + 127 <= 247: always a normal fp32.
+__device__ __forceinline__ float mx_inv_scale(uint32_t byte) { return __uint_as_float((254u - byte) << 23); }
+
+// Two codes: the value times 2^-e (exact, or far below the smallest code),
+// rounded; |v| times 2^-e of a non-finite value is made NaN first, because
+// the saturating conversion would turn an infinity into 448.
+__device__ __forceinline__ uint32_t e4m3_pair(float lo, float hi, float inv) {
+    const float nan = __uint_as_float(0x7FC00000u);
+    lo = (__float_as_uint(lo) & 0x7FFFFFFFu) < 0x7F800000u ? lo * inv : nan;
+    hi = (__float_as_uint(hi) & 0x7FFFFFFFu) < 0x7F800000u ? hi * inv : nan;
+    uint16_t d;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(d) : "f"(hi), "f"(lo));
+    return d;
+}
+
+__device__ __forceinline__ uint2 e4m3_codes8(const float (&v)[8], float inv) {
+    return make_uint2(e4m3_pair(v[0], v[1], inv) | (e4m3_pair(v[2], v[3], inv) << 16),
+                      e4m3_pair(v[4], v[5], inv) | (e4m3_pair(v[6], v[7], inv) << 16));
+}
+
+// Encodes a block held by four consecutive lanes, eight values each (lane & 3
+// gives the order).  All 32 lanes of the warp call it; those without a block
+// pass zeros and active = false.  q: this lane's 8 codes (8-byte aligned);
+// sf: the block's scale byte.
+__device__ __forceinline__ void mx_store8(const float (&v)[8], bool active, uint8_t *q, uint8_t *sf) {
+    uint32_t m = finite_max_bits(v);
+    m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+    m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
+    if (!active) return;
+    const uint32_t byte = mx_scale_byte(m);
+    *reinterpret_cast<uint2 *>(q) = e4m3_codes8(v, mx_inv_scale(byte));
+    if ((threadIdx.x & 3) == 0) *sf = static_cast<uint8_t>(byte);
+}
+
+}  // namespace b200

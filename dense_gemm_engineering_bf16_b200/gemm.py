@@ -72,6 +72,16 @@ lib.gemm_bf16_allgather.argtypes = [_vp, _vp, ctypes.POINTER(_vp), _int, _i64, _
 lib.gemm_bf16_allgather.restype = _int
 lib.gemm_mxfp8.argtypes = [_vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _i64, _i64, _i64, _vp]
 lib.gemm_mxfp8.restype = _int
+lib.gemm_rmsnorm.argtypes = [_vp] * 8 + [_i64] * 7 + [_int, _int, ctypes.c_float, _vp]
+lib.gemm_rmsnorm.restype = _int
+lib.gemm_rmsnorm_backward.argtypes = [_vp] * 8 + [_i64] * 7 + [_int, _int, _int, _vp]
+lib.gemm_rmsnorm_backward.restype = _int
+lib.gemm_rmsnorm_backward_workspace.argtypes = [_i64, _i64]
+lib.gemm_rmsnorm_backward_workspace.restype = _i64
+lib.gemm_mxfp8_quantize.argtypes = [_vp, _vp, _vp, _i64, _i64, _i64, _i64, _int, _int, _vp]
+lib.gemm_mxfp8_quantize.restype = _int
+lib.gemm_bf16_w4.argtypes = [_vp] * 5 + [_i64] * 8 + [_int, _vp]
+lib.gemm_bf16_w4.restype = _int
 lib.gemm_check_device_status.argtypes = [_vp]
 lib.gemm_check_device_status.restype = _int
 lib.gemm_last_timeout_detail.argtypes = [ctypes.POINTER(ctypes.c_int32), ctypes.POINTER(ctypes.c_int32)]
@@ -186,6 +196,98 @@ def gemm_bf16_noalloc(A, B, C, M: int, N: int, K: int, lda: int, ldb: int, ldc: 
     st = lib.gemm_bf16_noalloc(_ptr(A), _ptr(B), _ptr(C), M, N, K, lda, ldb, ldc, int(c_type),
                                _stream(stream))
     return _check(st, "gemm_bf16_noalloc", check)
+
+
+# Tensor types an operand may have, by gemm_out_t (and for the byte formats);
+# filled when a tensor is first checked, so that importing this module does
+# not import torch.
+_DTYPES: dict = {}
+
+
+def _dtypes(kind):
+    if not _DTYPES:
+        import torch
+        _DTYPES.update({OUT_F32: (torch.float32,), OUT_BF16: (torch.bfloat16,), "bytes": (torch.uint8,),
+                        "codes": (torch.float8_e4m3fn, torch.uint8),
+                        "scales": (torch.float8_e8m0fnu, torch.uint8), "any": None})
+    return _DTYPES.get(kind)
+
+
+def _operand(x, kind, what: str):
+    """Device pointer of an operand: None, a raw pointer, or a tensor, which
+    has to be on the current device (whose stream the call runs on) and to
+    hold the type that the call reads there."""
+    if x is None or isinstance(x, int):
+        return x
+    import torch
+    if x.get_device() != torch.cuda.current_device():
+        raise GemmError(1, f"{what} is on {x.device}, the call runs on cuda:{torch.cuda.current_device()}")
+    want = _dtypes(kind)
+    if want is not None and x.dtype not in want:
+        raise GemmError(1, f"{what} is {x.dtype}, expected {' or '.join(map(str, want))}")
+    return x.data_ptr()
+
+
+def gemm_rmsnorm(X, R, H, weight, Y, Q, sf, rstd, M: int, K: int, ldx: int, ldr: int, ldh: int, ldy: int, ldq: int,
+                 x_type: int = OUT_BF16, h_type: int = OUT_BF16, eps: float = 1e-5, stream=None,
+                 check: bool = True) -> int:
+    """h = X + R (stored to H), y = h / rms(h) * weight, written as bf16 to Y
+    and / or as MXFP8 codes and scales to Q and sf; 1 / rms to rstd.  R, H, Y,
+    Q with sf, and rstd may be None (see include/b200gemm.h, gemm_rmsnorm)."""
+    st = lib.gemm_rmsnorm(_operand(X, x_type, "gemm_rmsnorm: X"), _operand(R, h_type, "gemm_rmsnorm: R"),
+                          _operand(H, h_type, "gemm_rmsnorm: H"), _operand(weight, OUT_F32, "gemm_rmsnorm: weight"),
+                          _operand(Y, OUT_BF16, "gemm_rmsnorm: Y"), _operand(Q, "codes", "gemm_rmsnorm: Q"),
+                          _operand(sf, "scales", "gemm_rmsnorm: sf"), _operand(rstd, OUT_F32, "gemm_rmsnorm: rstd"),
+                          M, K, ldx, ldr, ldh, ldy, ldq, int(x_type), int(h_type), eps, _stream(stream))
+    return _check(st, "gemm_rmsnorm", check)
+
+
+def gemm_rmsnorm_backward_workspace(M: int, K: int) -> int:
+    """Bytes of workspace that gemm_rmsnorm_backward needs for a dW."""
+    return int(lib.gemm_rmsnorm_backward_workspace(M, K))
+
+
+def gemm_rmsnorm_backward(dY, H, weight, rstd, dR, dH, dW, workspace, M: int, K: int, lddy: int, ldh: int, lddr: int,
+                          lddh: int, dy_type: int = OUT_BF16, h_type: int = OUT_BF16, dh_type: int = OUT_BF16,
+                          workspace_bytes: int | None = None, stream=None, check: bool = True) -> int:
+    """Gradients of gemm_rmsnorm: dH (of X and of R alike, dR added) and dW.
+    dR may be None; dW with workspace may be None (see include/b200gemm.h,
+    gemm_rmsnorm_backward).  workspace_bytes: needed where workspace is a raw
+    pointer; a tensor's own size otherwise."""
+    if workspace_bytes is None:
+        workspace_bytes = 0 if workspace is None or isinstance(workspace, int) else \
+            workspace.numel() * workspace.element_size()
+    st = lib.gemm_rmsnorm_backward(
+        _operand(dY, dy_type, "gemm_rmsnorm_backward: dY"), _operand(H, h_type, "gemm_rmsnorm_backward: H"),
+        _operand(weight, OUT_F32, "gemm_rmsnorm_backward: weight"),
+        _operand(rstd, OUT_F32, "gemm_rmsnorm_backward: rstd"), _operand(dR, dh_type, "gemm_rmsnorm_backward: dR"),
+        _operand(dH, dh_type, "gemm_rmsnorm_backward: dH"), _operand(dW, OUT_F32, "gemm_rmsnorm_backward: dW"),
+        _operand(workspace, "any", "gemm_rmsnorm_backward: workspace"), workspace_bytes, M, K, lddy, ldh, lddr, lddh,
+        int(dy_type), int(h_type), int(dh_type), _stream(stream))
+    return _check(st, "gemm_rmsnorm_backward", check)
+
+
+def gemm_mxfp8_quantize(X, Q, sf, M: int, K: int, ldx: int, ldq: int, x_type: int = OUT_BF16, layout: int = KMAJOR,
+                        stream=None, check: bool = True) -> int:
+    """E4M3 codes Q (M x ldq) and E8M0 scales sf (M x K/32) of X, stored M x K
+    (KMAJOR) or K x M (MNMAJOR): an operand of gemm_mxfp8."""
+    st = lib.gemm_mxfp8_quantize(_operand(X, x_type, "gemm_mxfp8_quantize: X"),
+                                 _operand(Q, "codes", "gemm_mxfp8_quantize: Q"),
+                                 _operand(sf, "scales", "gemm_mxfp8_quantize: sf"), M, K, ldx, ldq, int(x_type),
+                                 int(layout), _stream(stream))
+    return _check(st, "gemm_mxfp8_quantize", check)
+
+
+def gemm_bf16_w4(A, B, scales, zeros, C, M: int, N: int, K: int, lda: int, ldb: int, lds: int, ldc: int, group: int,
+                 c_type: int = OUT_F32, stream=None, check: bool = True) -> int:
+    """C = A.W^T with W[j][k] = scales[j][k/group] (q[j][k] - zeros[j][k/group]):
+    bf16 A (M x K), 4-bit codes B (N x ldb bytes, two each, even k in the low
+    half), bf16 scales and byte zeros (N x lds; zeros None: 8), C M x N."""
+    st = lib.gemm_bf16_w4(_operand(A, OUT_BF16, "gemm_bf16_w4: A"), _operand(B, "bytes", "gemm_bf16_w4: B"),
+                          _operand(scales, OUT_BF16, "gemm_bf16_w4: scales"),
+                          _operand(zeros, "bytes", "gemm_bf16_w4: zeros"), _operand(C, c_type, "gemm_bf16_w4: C"),
+                          M, N, K, lda, ldb, lds, ldc, group, int(c_type), _stream(stream))
+    return _check(st, "gemm_bf16_w4", check)
 
 
 def gemm_check_device_status(stream=None, check: bool = True) -> int:

@@ -321,6 +321,126 @@ B200GEMM_API gemm_status_t gemm_bf16_noalloc(const void *A, const void *B, void 
                                              int64_t lda, int64_t ldb, int64_t ldc,
                                              gemm_out_t c_type, cudaStream_t stream);
 
+/*
+ * Operators around the products.  None of them allocates, keeps state or
+ * waits inside a kernel on another; scratch, where one needs any, is the
+ * caller's.  Calls on different streams are independent as long as their
+ * buffers are.  As for the products, the first call of each kind on a device
+ * may not be captured (GEMM_ERR_CAPTURE); matrices are row-major with 16-byte
+ * aligned bases and pitches, and no element outside their rows and columns is
+ * read or written.  Types are gemm_out_t's: a matrix that a product wrote can
+ * be passed on as it is.
+ */
+
+/*
+ * gemm_rmsnorm: root-mean-square norm of the rows of X, or of X + R, for the
+ * product that follows.
+ *
+ *   h = x + r, rounded to h_type   (without R: h = x)
+ *   rstd = 1 / sqrt(sum_k h_k^2 / K + eps)
+ *   y_k = h_k rstd weight_k
+ *
+ * y goes to Y as bf16 (an A of gemm_bf16 or gemm_bf16_w4), to Q and sf as
+ * MXFP8 (A and sfa of gemm_mxfp8, encoded as by gemm_mxfp8_quantize), or to
+ * both.  Sums and statistics are fp32; the norm is of h as it is stored, so
+ * that gemm_rmsnorm_backward, which reads H, differentiates what was computed.
+ *   X       M x K of x_type
+ *   R       M x K of h_type, the residual stream; NULL: none
+ *   H       M x K of h_type, the sum; NULL: not stored.  Only with R, and it
+ *           may be R itself (same pointer and pitch): the stream is updated
+ *           in place
+ *   weight  K floats, 16-byte aligned
+ *   Y       M x K bf16, or NULL
+ *   Q, sf   M x ldq bytes of codes and M x (K/32) scale bytes, rows packed, or
+ *           NULL; K must then be a multiple of 32
+ *   rstd    M floats for the backward pass, or NULL
+ *   eps     > 0
+ * At least one of Y and Q is given.  Outputs may not overlap one another nor
+ * an input (H == R aside).  M == 0 or K == 0: nothing to do.  One kernel.
+ * The sum of squares is fp32: a row whose squares pass 3.4e38 gives zeros.
+ */
+B200GEMM_API gemm_status_t gemm_rmsnorm(const void *X, const void *R, void *H, const float *weight, void *Y, uint8_t *Q,
+                                        uint8_t *sf, float *rstd, int64_t M, int64_t K, int64_t ldx, int64_t ldr,
+                                        int64_t ldh, int64_t ldy, int64_t ldq, gemm_out_t x_type, gemm_out_t h_type,
+                                        float eps, cudaStream_t stream);
+
+/*
+ * gemm_rmsnorm_backward: gradients of gemm_rmsnorm.  With n = h rstd and
+ * g = dy weight (per row, sums over k):
+ *
+ *   dh_k = rstd (g_k - n_k sum(g n) / K) (+ dr_k)
+ *   dW_k = sum over rows of dy_k n_k
+ *
+ * dH is the gradient of x and of r alike (their sum is h).
+ *   dY        M x K of dy_type, the gradient of y
+ *   H         M x K of h_type: gemm_rmsnorm's H (or X, where it had no R)
+ *   rstd      M floats from gemm_rmsnorm
+ *   dR        M x K of dh_type, the gradient that reaches h past the norm; NULL: none
+ *   dH        M x K of dh_type; it may be dY or dR itself (same pointer, pitch and type size)
+ *   dW        K floats, 16-byte aligned, overwritten; NULL: not wanted
+ *   workspace gemm_rmsnorm_backward_workspace(M, K) bytes, 16-byte aligned,
+ *             contents irrelevant; used only with dW (else it may be NULL).
+ *             Calls that may overlap in time need one each.
+ * Sums are fp32 in a fixed order: the same inputs give the same bits.
+ * M == 0: dW is set to zero; K == 0: nothing to do.  One kernel, and a second
+ * that adds up dW where more than one block worked on it.
+ */
+B200GEMM_API gemm_status_t gemm_rmsnorm_backward(const void *dY, const void *H, const float *weight, const float *rstd,
+                                                 const void *dR, void *dH, float *dW, void *workspace,
+                                                 int64_t workspace_bytes, int64_t M, int64_t K, int64_t lddy, int64_t ldh,
+                                                 int64_t lddr, int64_t lddh, gemm_out_t dy_type, gemm_out_t h_type,
+                                                 gemm_out_t dh_type, cudaStream_t stream);
+
+/* Bytes of workspace for gemm_rmsnorm_backward with a dW: 4 K min(M, 296). */
+B200GEMM_API int64_t gemm_rmsnorm_backward_workspace(int64_t M, int64_t K);
+
+/*
+ * gemm_mxfp8_quantize: the operands of gemm_mxfp8 from a bf16 or fp32 matrix.
+ * Row i's elements 32 kb .. 32 kb + 31 share the scale 2^e, the smallest with
+ * |x| <= 448 2^e for every finite x among them, -127 <= e <= 127 (448 is the
+ * largest E4M3 value: nothing finite saturates):
+ *
+ *   sf[i (K/32) + kb] = e + 127,   Q[i ldq + k] = E4M3(x / 2^e), to nearest even
+ *
+ * NaN and infinities become the E4M3 NaN code 0x7F and leave the scale alone.
+ *   X       layout K-major: M x K, element (i, k) at X[i ldx + k].  MN-major:
+ *           K x M, element (i, k) at X[k ldx + i]: the transposed operand,
+ *           as the gradient products need it
+ *   Q, sf   M x ldq bytes of codes, M x (K/32) scale bytes, rows packed
+ * K must be a multiple of 32.  Q and sf overlap neither X nor one another.
+ * M == 0 or K == 0: nothing to do.  One kernel.
+ */
+B200GEMM_API gemm_status_t gemm_mxfp8_quantize(const void *X, uint8_t *Q, uint8_t *sf, int64_t M, int64_t K, int64_t ldx,
+                                               int64_t ldq, gemm_out_t x_type, gemm_layout_t layout,
+                                               cudaStream_t stream);
+
+/*
+ * gemm_bf16_w4: the product with 4-bit weights,
+ *
+ *   C[i][j] = sum_k A[i][k] scales[j][k/group] (q[j][k] - zeros[j][k/group])
+ *
+ * for the few rows of a decoding batch, where the weights' bytes are the cost.
+ *   A       M x K bf16
+ *   B       N x ldb bytes, two codes each: q[j][k] is byte j ldb + k/2's low
+ *           half for even k, its high half for odd k
+ *   scales  N x lds bf16, one per `group` consecutive k of a row (the last
+ *           group of a row may be short)
+ *   zeros   N x lds bytes, values 0 .. 15 (the upper halves are not read);
+ *           NULL: 8 everywhere
+ *   C       M x N of c_type
+ *   group   a power of two >= 32; from K on: one scale per row
+ * K must be a multiple of 32, ldb (bytes) and lds of 16, lds >= ceil(K / group).
+ * Products are exact, sums fp32 and in a fixed order, the result rounded once.
+ * Any M is accepted; the kernel is built for M <= 64 (each 64 rows pass over
+ * the weights again, and larger M is bound by the warp-level tensor
+ * instruction: for long prompts, dequantise once and use gemm_bf16).
+ * C may not overlap an input.  M == 0 or N == 0: nothing to do; K == 0: C = 0.
+ * One kernel.
+ */
+B200GEMM_API gemm_status_t gemm_bf16_w4(const void *A, const uint8_t *B, const void *scales, const uint8_t *zeros, void *C,
+                                        int64_t M, int64_t N, int64_t K, int64_t lda, int64_t ldb, int64_t lds, int64_t ldc,
+                                        int64_t group, gemm_out_t c_type, cudaStream_t stream);
+
 /* Synchronises `stream`, then reports and clears the device watchdog status
  * of the current device (the status blocks of every entry point, the static
  * one of gemm_bf16_noalloc included): GEMM_OK, or GEMM_ERR_TIMEOUT if a
