@@ -5,7 +5,7 @@ The binding (``gemm_bf16``, ``gemm_mxfp8``, ``gemm_check_device_status``,
 ``gemm_status_string`` ...) is loaded on first attribute access, so that
 ``synth`` can be imported on machines without the built library.  Accessing
 a binding name when the library is missing raises immediately: there is no
-fallback path.
+fallback path.  A loaded name stays, so that later accesses cost nothing.
 """
 from importlib import import_module
 
@@ -22,5 +22,6 @@ _BINDING_NAMES = {
 
 def __getattr__(name):
     if name in _BINDING_NAMES:
-        return getattr(import_module(".gemm", __name__), name)
+        value = globals()[name] = getattr(import_module(".gemm", __name__), name)
+        return value
     raise AttributeError(name)

@@ -189,49 +189,49 @@ gemm_status_t launch_quantize(int dev, const void *X, uint8_t *Q, uint8_t *sf, i
 
 // ------------------------------------------------------- 4-bit weights --
 
-template <int NT, int MT, int U>
+template <class Cfg, int U>
 gemm_status_t launch_w4(int dev, int sm_count, b200::W4Args a, cudaStream_t stream) {
-    constexpr int S = 4;
-    constexpr int kXBytes = 32 * 1024;
-    constexpr int kRing = S * b200::kW4StageBytes;
-    constexpr int kMaxSmem = kRing + std::max(kXBytes, 8 * NT * (2 * b200::kW4K + 64)) + 8 * NT * 64;
-    auto kernel = b200::gemm_w4_kernel<NT, MT, U, S>;
+    constexpr int NT = Cfg::NT;
     gemm_status_t s;
-    if ((s = b200::host::prepare<b200::gemm_w4_kernel<NT, MT, U, S>>(dev, kMaxSmem, stream)) != GEMM_OK) return s;
-    const int64_t tiles = (a.N + b200::kW4Rows - 1) / b200::kW4Rows;
+    if ((s = b200::host::prepare<b200::gemm_w4_kernel<Cfg, U>>(dev, Cfg::MAX_SMEM, stream)) != GEMM_OK) return s;
+    const int64_t tiles = (a.N + Cfg::ROWS - 1) / Cfg::ROWS;
     const int64_t token_blocks = (a.M + 8 * NT - 1) / (8 * NT);
     const int64_t stages = (a.K + b200::kW4K - 1) / b200::kW4K;
     int64_t split = 1;
-    while (split < 8 && tiles * token_blocks * split < 2 * sm_count && 2 * split <= stages) split *= 2;
+    while (split < 8 && tiles * token_blocks * 2 * split <= 2 * sm_count && 2 * split <= stages) split *= 2;
     if (token_blocks > kMaxDim / 8 || tiles * token_blocks > kMaxDim / split) return GEMM_ERR_TOO_LARGE;
     a.token_blocks = static_cast<int>(token_blocks);
     const int tokens = static_cast<int>(std::min<int64_t>(a.M, 8 * NT));
+    // activations staged at a time: a power of two of stages, all of the block's share where that fits
     const int64_t share = (stages + split - 1) / split;
-    a.x_stages = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(share, kXBytes / (tokens * 2 * b200::kW4K))));
-    a.x_pitch = a.x_stages * 2 * b200::kW4K + 64;
-    const int smem = kRing + tokens * a.x_pitch;
+    int64_t x_stages = 1;
+    while (x_stages < share && tokens * 2 * x_stages * 2 * b200::kW4K <= Cfg::X_BYTES) x_stages *= 2;
+    a.x_shift = 5;
+    while ((int64_t(1) << (a.x_shift - 5)) < x_stages) ++a.x_shift;
+    a.x_pitch = static_cast<int>(x_stages * 2 * b200::kW4K + 64);   // + 64: conflict-free 16-byte reads
+    const int smem = Cfg::RING_BYTES + tokens * a.x_pitch;
     cudaLaunchConfig_t lc = {};
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeClusterDimension;
     attr.val.clusterDim.x = static_cast<unsigned>(split);
     attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
     lc.gridDim = dim3(static_cast<unsigned>(tiles * token_blocks * split));
-    lc.blockDim = dim3(32 * (b200::kW4Rows / (16 * MT)));
+    lc.blockDim = dim3(Cfg::THREADS);
     lc.dynamicSmemBytes = static_cast<size_t>(smem);
     lc.stream = stream;
     lc.attrs = &attr;
     lc.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&lc, kernel, a);
+    const cudaError_t e = cudaLaunchKernelEx(&lc, b200::gemm_w4_kernel<Cfg, U>, a);
     return e == cudaSuccess ? GEMM_OK : b200::host::cuda_fail(e);
 }
 
-template <int NT, int MT>
+template <class Cfg>
 gemm_status_t dispatch_w4(int dev, int sm_count, const b200::W4Args &a, cudaStream_t stream) {
     switch (a.group_shift) {
-        case 5: return launch_w4<NT, MT, 1>(dev, sm_count, a, stream);
-        case 6: return launch_w4<NT, MT, 2>(dev, sm_count, a, stream);
-        case 7: return launch_w4<NT, MT, 4>(dev, sm_count, a, stream);
-        default: return launch_w4<NT, MT, 8>(dev, sm_count, a, stream);
+        case 5: return launch_w4<Cfg, 1>(dev, sm_count, a, stream);
+        case 6: return launch_w4<Cfg, 2>(dev, sm_count, a, stream);
+        case 7: return launch_w4<Cfg, 4>(dev, sm_count, a, stream);
+        default: return launch_w4<Cfg, 8>(dev, sm_count, a, stream);
     }
 }
 
@@ -388,7 +388,7 @@ gemm_status_t gemm_bf16_w4(const void *A, const uint8_t *B, const void *scales, 
     if (any_overlap(mc, {ma, mb, ms, mz})) return GEMM_ERR_ALIAS;
     if ((s = b200::host::device(dev, sm_count, stream)) != GEMM_OK) return s;
     int shift = 5;
-    while ((int64_t(1) << shift) < group && shift < 40) ++shift;
+    while ((int64_t(1) << shift) < group && shift < 31) ++shift;   // K < 2^31: one group either way from there
     b200::W4Args a{};
     a.a = static_cast<const uint16_t *>(A);
     a.b = B;
@@ -399,10 +399,10 @@ gemm_status_t gemm_bf16_w4(const void *A, const uint8_t *B, const void *scales, 
     a.groups = groups;
     a.group_shift = shift;
     a.out = c_type == GEMM_OUT_F32 ? kF32 : kBF16;
-    if (M <= 8) return dispatch_w4<1, 1>(dev, sm_count, a, stream);
-    if (M <= 16) return dispatch_w4<2, 1>(dev, sm_count, a, stream);
-    if (M <= 32) return dispatch_w4<4, 2>(dev, sm_count, a, stream);
-    return dispatch_w4<8, 2>(dev, sm_count, a, stream);
+    if (M <= 8) return dispatch_w4<b200::W4Cfg<1, 1, 8, 3>>(dev, sm_count, a, stream);
+    if (M <= 16) return dispatch_w4<b200::W4Cfg<2, 1, 8, 3>>(dev, sm_count, a, stream);
+    if (M <= 32) return dispatch_w4<b200::W4Cfg<4, 2, 4, 3>>(dev, sm_count, a, stream);
+    return dispatch_w4<b200::W4Cfg<8, 2, 4, 3>>(dev, sm_count, a, stream);
 }
 
 }  // extern "C"

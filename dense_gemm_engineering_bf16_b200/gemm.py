@@ -198,33 +198,39 @@ def gemm_bf16_noalloc(A, B, C, M: int, N: int, K: int, lda: int, ldb: int, ldc: 
     return _check(st, "gemm_bf16_noalloc", check)
 
 
-# Tensor types an operand may have, by gemm_out_t (and for the byte formats);
-# filled when a tensor is first checked, so that importing this module does
-# not import torch.
+# The dtypes that an operand's tensor may have, by gemm_out_t (and for the byte
+# formats); filled on first use, so that importing this module does not import
+# torch.
 _DTYPES: dict = {}
 
 
-def _dtypes(kind):
+def _here(stream):
+    """The current device (None: not asked for yet) and the call's stream
+    handle.  Without a stream it is the device's current one, asked for
+    without building a Stream object, which would cost more than the launch."""
     if not _DTYPES:
         import torch
         _DTYPES.update({OUT_F32: (torch.float32,), OUT_BF16: (torch.bfloat16,), "bytes": (torch.uint8,),
-                        "codes": (torch.float8_e4m3fn, torch.uint8),
-                        "scales": (torch.float8_e8m0fnu, torch.uint8), "any": None})
-    return _DTYPES.get(kind)
+                        "codes": (torch.float8_e4m3fn, torch.uint8), "scales": (torch.float8_e8m0fnu, torch.uint8),
+                        "device": torch._C._cuda_getDevice, "stream": torch._C._cuda_getCurrentRawStream})
+    if stream is not None:
+        return None, _stream(stream)
+    dev = _DTYPES["device"]()
+    return dev, _DTYPES["stream"](dev)
 
 
-def _operand(x, kind, what: str):
+def _operand(x, kind, dev, what: str):
     """Device pointer of an operand: None, a raw pointer, or a tensor, which
     has to be on the current device (whose stream the call runs on) and to
     hold the type that the call reads there."""
-    if x is None or isinstance(x, int):
+    if x is None or type(x) is int:
         return x
-    import torch
-    if x.get_device() != torch.cuda.current_device():
-        raise GemmError(1, f"{what} is on {x.device}, the call runs on cuda:{torch.cuda.current_device()}")
-    want = _dtypes(kind)
-    if want is not None and x.dtype not in want:
-        raise GemmError(1, f"{what} is {x.dtype}, expected {' or '.join(map(str, want))}")
+    if dev is None:
+        dev = _DTYPES["device"]()
+    if x.get_device() != dev:
+        raise GemmError(1, f"{what} is on {x.device}, the call runs on cuda:{dev}")
+    if kind is not None and x.dtype not in _DTYPES.get(kind, ()):
+        raise GemmError(1, f"{what} is {x.dtype}")
     return x.data_ptr()
 
 
@@ -234,11 +240,14 @@ def gemm_rmsnorm(X, R, H, weight, Y, Q, sf, rstd, M: int, K: int, ldx: int, ldr:
     """h = X + R (stored to H), y = h / rms(h) * weight, written as bf16 to Y
     and / or as MXFP8 codes and scales to Q and sf; 1 / rms to rstd.  R, H, Y,
     Q with sf, and rstd may be None (see include/b200gemm.h, gemm_rmsnorm)."""
-    st = lib.gemm_rmsnorm(_operand(X, x_type, "gemm_rmsnorm: X"), _operand(R, h_type, "gemm_rmsnorm: R"),
-                          _operand(H, h_type, "gemm_rmsnorm: H"), _operand(weight, OUT_F32, "gemm_rmsnorm: weight"),
-                          _operand(Y, OUT_BF16, "gemm_rmsnorm: Y"), _operand(Q, "codes", "gemm_rmsnorm: Q"),
-                          _operand(sf, "scales", "gemm_rmsnorm: sf"), _operand(rstd, OUT_F32, "gemm_rmsnorm: rstd"),
-                          M, K, ldx, ldr, ldh, ldy, ldq, int(x_type), int(h_type), eps, _stream(stream))
+    dev, queue = _here(stream)
+    st = lib.gemm_rmsnorm(_operand(X, x_type, dev, "gemm_rmsnorm: X"), _operand(R, h_type, dev, "gemm_rmsnorm: R"),
+                          _operand(H, h_type, dev, "gemm_rmsnorm: H"),
+                          _operand(weight, OUT_F32, dev, "gemm_rmsnorm: weight"),
+                          _operand(Y, OUT_BF16, dev, "gemm_rmsnorm: Y"), _operand(Q, "codes", dev, "gemm_rmsnorm: Q"),
+                          _operand(sf, "scales", dev, "gemm_rmsnorm: sf"),
+                          _operand(rstd, OUT_F32, dev, "gemm_rmsnorm: rstd"), M, K, ldx, ldr, ldh, ldy, ldq,
+                          int(x_type), int(h_type), eps, queue)
     return _check(st, "gemm_rmsnorm", check)
 
 
@@ -257,13 +266,16 @@ def gemm_rmsnorm_backward(dY, H, weight, rstd, dR, dH, dW, workspace, M: int, K:
     if workspace_bytes is None:
         workspace_bytes = 0 if workspace is None or isinstance(workspace, int) else \
             workspace.numel() * workspace.element_size()
+    dev, queue = _here(stream)
     st = lib.gemm_rmsnorm_backward(
-        _operand(dY, dy_type, "gemm_rmsnorm_backward: dY"), _operand(H, h_type, "gemm_rmsnorm_backward: H"),
-        _operand(weight, OUT_F32, "gemm_rmsnorm_backward: weight"),
-        _operand(rstd, OUT_F32, "gemm_rmsnorm_backward: rstd"), _operand(dR, dh_type, "gemm_rmsnorm_backward: dR"),
-        _operand(dH, dh_type, "gemm_rmsnorm_backward: dH"), _operand(dW, OUT_F32, "gemm_rmsnorm_backward: dW"),
-        _operand(workspace, "any", "gemm_rmsnorm_backward: workspace"), workspace_bytes, M, K, lddy, ldh, lddr, lddh,
-        int(dy_type), int(h_type), int(dh_type), _stream(stream))
+        _operand(dY, dy_type, dev, "gemm_rmsnorm_backward: dY"), _operand(H, h_type, dev, "gemm_rmsnorm_backward: H"),
+        _operand(weight, OUT_F32, dev, "gemm_rmsnorm_backward: weight"),
+        _operand(rstd, OUT_F32, dev, "gemm_rmsnorm_backward: rstd"),
+        _operand(dR, dh_type, dev, "gemm_rmsnorm_backward: dR"),
+        _operand(dH, dh_type, dev, "gemm_rmsnorm_backward: dH"),
+        _operand(dW, OUT_F32, dev, "gemm_rmsnorm_backward: dW"),
+        _operand(workspace, None, dev, "gemm_rmsnorm_backward: workspace"), workspace_bytes, M, K, lddy, ldh, lddr,
+        lddh, int(dy_type), int(h_type), int(dh_type), queue)
     return _check(st, "gemm_rmsnorm_backward", check)
 
 
@@ -271,10 +283,11 @@ def gemm_mxfp8_quantize(X, Q, sf, M: int, K: int, ldx: int, ldq: int, x_type: in
                         stream=None, check: bool = True) -> int:
     """E4M3 codes Q (M x ldq) and E8M0 scales sf (M x K/32) of X, stored M x K
     (KMAJOR) or K x M (MNMAJOR): an operand of gemm_mxfp8."""
-    st = lib.gemm_mxfp8_quantize(_operand(X, x_type, "gemm_mxfp8_quantize: X"),
-                                 _operand(Q, "codes", "gemm_mxfp8_quantize: Q"),
-                                 _operand(sf, "scales", "gemm_mxfp8_quantize: sf"), M, K, ldx, ldq, int(x_type),
-                                 int(layout), _stream(stream))
+    dev, queue = _here(stream)
+    st = lib.gemm_mxfp8_quantize(_operand(X, x_type, dev, "gemm_mxfp8_quantize: X"),
+                                 _operand(Q, "codes", dev, "gemm_mxfp8_quantize: Q"),
+                                 _operand(sf, "scales", dev, "gemm_mxfp8_quantize: sf"), M, K, ldx, ldq, int(x_type),
+                                 int(layout), queue)
     return _check(st, "gemm_mxfp8_quantize", check)
 
 
@@ -283,10 +296,12 @@ def gemm_bf16_w4(A, B, scales, zeros, C, M: int, N: int, K: int, lda: int, ldb: 
     """C = A.W^T with W[j][k] = scales[j][k/group] (q[j][k] - zeros[j][k/group]):
     bf16 A (M x K), 4-bit codes B (N x ldb bytes, two each, even k in the low
     half), bf16 scales and byte zeros (N x lds; zeros None: 8), C M x N."""
-    st = lib.gemm_bf16_w4(_operand(A, OUT_BF16, "gemm_bf16_w4: A"), _operand(B, "bytes", "gemm_bf16_w4: B"),
-                          _operand(scales, OUT_BF16, "gemm_bf16_w4: scales"),
-                          _operand(zeros, "bytes", "gemm_bf16_w4: zeros"), _operand(C, c_type, "gemm_bf16_w4: C"),
-                          M, N, K, lda, ldb, lds, ldc, group, int(c_type), _stream(stream))
+    dev, queue = _here(stream)
+    st = lib.gemm_bf16_w4(_operand(A, OUT_BF16, dev, "gemm_bf16_w4: A"), _operand(B, "bytes", dev, "gemm_bf16_w4: B"),
+                          _operand(scales, OUT_BF16, dev, "gemm_bf16_w4: scales"),
+                          _operand(zeros, "bytes", dev, "gemm_bf16_w4: zeros"),
+                          _operand(C, c_type, dev, "gemm_bf16_w4: C"), M, N, K, lda, ldb, lds, ldc, group,
+                          int(c_type), queue)
     return _check(st, "gemm_bf16_w4", check)
 
 
