@@ -6,28 +6,26 @@
 
 namespace b200 {
 
-// X stored K-major (M rows of K): VPT vectors of eight per thread, four
-// lanes per block of 32.  A row (or a part of it: blockIdx.y) takes
-// blockDim.x threads; short rows share a block (blockDim.y).
+// X stored K-major (M rows of K): VPT eights per thread.  A row (or a part of
+// it: blockIdx.y) takes blockDim.x threads; short rows share a block
+// (blockDim.y).
 template <int XT, int VPT>
 __global__ void __launch_bounds__(256) mx_quantize_kernel(const void *x, uint8_t *q, uint8_t *sf, int64_t M, int64_t K,
                                                           int64_t ldx, int64_t ldq) {
+    constexpr bool SPLIT = XT == kF32;
     const int64_t row = static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y;
     if (row >= M) return;   // whole warps
     const uint8_t *p = static_cast<const uint8_t *>(x) + row * ldx * elem_bytes<XT>;
-    const int64_t e0 = 8 * (static_cast<int64_t>(blockIdx.y) * VPT * blockDim.x + threadIdx.x);
     Raw8<XT> r[VPT];
 #pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-        const int64_t e = e0 + 8 * static_cast<int64_t>(i) * blockDim.x;
-        r[i] = load_raw8<XT>(p, e, K - e);
-    }
+    for (int i = 0; i < VPT; ++i)
+        r[i] = load_raw8<XT, SPLIT>(p, first8<SPLIT>(threadIdx.x, blockIdx.y * VPT + i, blockDim.x), K);
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-        const int64_t e = e0 + 8 * static_cast<int64_t>(i) * blockDim.x;
         float v[8];
         widen8<XT>(r[i], v);
-        mx_store8(v, e < K, q + row * ldq + e, sf + row * (K / 32) + e / 32);
+        mx_store8<SPLIT>(v, first8<SPLIT>(threadIdx.x, blockIdx.y * VPT + i, blockDim.x), K, q + row * ldq,
+                         sf + row * (K / 32));
     }
 }
 
@@ -70,10 +68,7 @@ __global__ void __launch_bounds__(128) mx_quantize_mn_kernel(const void *x, uint
         if (c == 1 && !two) break;
         uint32_t m = 0;
 #pragma unroll
-        for (int k = 0; k < 32; ++k) {
-            const uint32_t b = __float_as_uint(v[c][k]) & 0x7FFFFFFFu;
-            m = max(m, b < 0x7F800000u ? b : 0u);
-        }
+        for (int k = 0; k < 32; ++k) m = finite_max_bits(m, v[c][k]);
         const uint32_t byte = mx_scale_byte(m);
         const float inv = mx_inv_scale(byte);
         uint32_t w[8];

@@ -59,6 +59,10 @@ gemm_status_t launched() {
     return e == cudaSuccess ? GEMM_OK : b200::host::cuda_fail(e);
 }
 
+// Dynamic shared memory that the blocks of an SM may take together (of its
+// 228 KB, 1 KB per block is the system's, and static arrays count too).
+constexpr int kSmemPerSm = 222 * 1024;
+
 int round_up(int64_t n, int m) { return static_cast<int>((n + m - 1) / m * m); }
 
 // ---------------------------------------------------------------- RMS norm --
@@ -113,14 +117,35 @@ gemm_status_t dispatch_norm_h(int dev, int sm_count, const b200::RmsnormArgs &a,
                       : dispatch_norm<XT, kBF16>(dev, sm_count, a, stream);
 }
 
-// Blocks of the backward pass, at most: the rows of its workspace.
+// Blocks of the backward pass, at most: the rows of its workspace (two per SM).
 constexpr int64_t kPartialRows = 296;
+static_assert(kPartialRows <= 320, "rmsnorm_dw_kernel adds up to 320 shares");
 
+// The second kernel of the backward pass: starts early (programmatic
+// dependence) and waits for the first one's shares itself.
+gemm_status_t launch_dw(const float *partial, float *dw, int rows, int64_t K, cudaStream_t stream) {
+    cudaLaunchConfig_t lc = {};
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    lc.gridDim = dim3(static_cast<unsigned>((K + 31) / 32));
+    lc.blockDim = dim3(1024);
+    lc.stream = stream;
+    lc.attrs = &attr;
+    lc.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&lc, b200::rmsnorm_dw_kernel, partial, dw, rows, K);
+    return e == cudaSuccess ? GEMM_OK : b200::host::cuda_fail(e);
+}
+
+// VPT 0: rows too long for registers.
 template <int YT, int HT, int DT, int VPT>
 gemm_status_t launch_back(int dev, int sm_count, b200::RmsnormBackArgs a, dim3 block, float *dw, float *ws,
                           cudaStream_t stream) {
-    constexpr int kAccBytes = VPT * 8 * 32 * 4;
-    const int64_t per_sm = block.x * block.y <= 512 ? 2 : 1;
+    // rows in shared memory: as many (2 to 4) as leave room for two blocks per
+    // SM, or else for one
+    const int row_bytes = static_cast<int>(VPT * b200::back_pieces<YT, HT, DT> * 16 * block.x * block.y);
+    const int64_t per_sm = block.x * block.y <= 256 && 4 * row_bytes <= kSmemPerSm ? 2 : 1;
+    a.ring = VPT == 0 ? 0 : static_cast<int>(std::min<int64_t>(4, kSmemPerSm / (per_sm * row_bytes)));
     const int64_t rows = (a.M + block.y - 1) / block.y;
     const int64_t blocks = std::min({rows, per_sm * sm_count, kPartialRows});
     // one block's share of dw is dw itself
@@ -131,34 +156,31 @@ gemm_status_t launch_back(int dev, int sm_count, b200::RmsnormBackArgs a, dim3 b
         if ((s = b200::host::prepare<b200::rmsnorm_back_long_kernel<YT, HT, DT>>(dev, 0, stream)) != GEMM_OK) return s;
         b200::rmsnorm_back_long_kernel<YT, HT, DT><<<static_cast<unsigned>(blocks), block, 0, stream>>>(a);
     } else {
-        if ((s = b200::host::prepare<b200::rmsnorm_back_kernel<YT, HT, DT, VPT>>(dev, 0, stream)) != GEMM_OK) return s;
+        if ((s = b200::host::prepare<b200::rmsnorm_back_kernel<YT, HT, DT, VPT>>(dev, kSmemPerSm, stream)) != GEMM_OK)
+            return s;
         b200::rmsnorm_back_kernel<YT, HT, DT, VPT>
-            <<<static_cast<unsigned>(blocks), block, block.y > 1 ? kAccBytes : 0, stream>>>(a);
+            <<<static_cast<unsigned>(blocks), block, a.ring * row_bytes, stream>>>(a);
     }
     if ((s = launched()) != GEMM_OK || !dw || blocks == 1) return s;
-    cudaLaunchConfig_t lc = {};
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    lc.gridDim = dim3(static_cast<unsigned>((a.K + 31) / 32));
-    lc.blockDim = dim3(256);
-    lc.stream = stream;
-    lc.attrs = &attr;
-    lc.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&lc, b200::rmsnorm_dw_kernel, static_cast<const float *>(ws), dw, blocks, a.K);
-    return e == cudaSuccess ? GEMM_OK : b200::host::cuda_fail(e);
+    return launch_dw(ws, dw, static_cast<int>(blocks), a.K, stream);
 }
 
+// Rows of up to 1024 elements take a warp each (one, two or four vectors per
+// thread); longer ones a block with two vectors per thread, as far as 512
+// threads go, then four: what a thread does once per row (addresses, the sum
+// across the block) is spread over more elements than with one.
 template <int YT, int HT, int DT>
 gemm_status_t dispatch_back(int dev, int sm_count, const b200::RmsnormBackArgs &a, float *dw, float *ws,
                             cudaStream_t stream) {
-    const RowShape r = row_shape(a.K, a.M <= 2 * sm_count);
-    switch (r.vpt) {
-        case 1: return launch_back<YT, HT, DT, 1>(dev, sm_count, a, r.block, dw, ws, stream);
-        case 2: return launch_back<YT, HT, DT, 2>(dev, sm_count, a, r.block, dw, ws, stream);
-        case 4: return launch_back<YT, HT, DT, 4>(dev, sm_count, a, r.block, dw, ws, stream);
-        default: return launch_back<YT, HT, DT, 0>(dev, sm_count, a, r.block, dw, ws, stream);
-    }
+    const int64_t vecs = (a.K + 7) / 8;
+    const auto block = [&](int vpt) { return dim3(static_cast<unsigned>(round_up((vecs + vpt - 1) / vpt, 32))); };
+    if (vecs <= 32) return launch_back<YT, HT, DT, 1>(dev, sm_count, a, dim3(32, 8), dw, ws, stream);
+    if (vecs <= 64) return launch_back<YT, HT, DT, 2>(dev, sm_count, a, dim3(32, 8), dw, ws, stream);
+    if (vecs <= 128) return launch_back<YT, HT, DT, 4>(dev, sm_count, a, dim3(32, 8), dw, ws, stream);
+    if (vecs <= 1024) return launch_back<YT, HT, DT, 2>(dev, sm_count, a, block(2), dw, ws, stream);
+    if (vecs <= 2048 && 2 * 16 * b200::back_pieces<YT, HT, DT> * 4 * block(4).x <= kSmemPerSm)
+        return launch_back<YT, HT, DT, 4>(dev, sm_count, a, block(4), dw, ws, stream);
+    return launch_back<YT, HT, DT, 0>(dev, sm_count, a, dim3(1024), dw, ws, stream);
 }
 
 // --------------------------------------------------------- MXFP8 quantiser --
@@ -325,7 +347,8 @@ gemm_status_t gemm_rmsnorm_backward(const void *dY, const void *H, const float *
         any_overlap(mg, {my, mh, mr, mw, mt, mp}) || any_overlap(mp, {my, mh, mr, mw, mt}))
         return GEMM_ERR_ALIAS;
     if ((s = b200::host::device(dev, sm_count, stream)) != GEMM_OK) return s;
-    const b200::RmsnormBackArgs a{dY, H, weight, rstd, dR, dH, nullptr, M, K, lddy, ldh, lddr, lddh};
+    const b200::RmsnormBackArgs a{dY, H, weight, rstd, dR, dH, nullptr, M, K, lddy, ldh, lddr, lddh, 0,
+                                  1.0f / static_cast<float>(K)};
     float *ws = static_cast<float *>(workspace);
     const int key = (dy_type == GEMM_OUT_F32 ? 4 : 0) | (h_type == GEMM_OUT_F32 ? 2 : 0) | (dh_type == GEMM_OUT_F32 ? 1 : 0);
     switch (key) {

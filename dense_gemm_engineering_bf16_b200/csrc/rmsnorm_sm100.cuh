@@ -7,8 +7,8 @@
 //
 // Both are bound by memory: a row is read once, stays in registers between
 // the sum over it and its use, and is written once.  A row belongs to
-// blockDim.x threads (a multiple of 32), thread t holding the vectors t,
-// t + blockDim.x, ... of eight elements; short rows take one warp each, and
+// blockDim.x threads (a multiple of 32), each holding one or more eights of
+// elements; short rows take one warp each, and
 // blockDim.y of them share a block.  All sums are fp32, in a fixed order.
 #pragma once
 #include "rows.cuh"
@@ -44,18 +44,20 @@ struct RmsnormArgs {
     float eps;
 };
 
+template <bool SPLIT>
 __device__ __forceinline__ void rmsnorm_write(const RmsnormArgs &a, int64_t row, int64_t e, const float (&h)[8],
                                               const float (&w)[8], float rstd) {
     float y[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) y[i] = h[i] * rstd * w[i];
-    if (a.y) store8<kBF16>(static_cast<__nv_bfloat16 *>(a.y) + row * a.ldy, e, a.K - e, y);
-    if (a.q) mx_store8(y, e < a.K, a.q + row * a.ldq + e, a.sf + row * (a.K / 32) + e / 32);
+    if (a.y) store8<kBF16, SPLIT>(static_cast<__nv_bfloat16 *>(a.y) + row * a.ldy, e, a.K, y);
+    if (a.q) mx_store8<SPLIT>(y, e, a.K, a.q + row * a.ldq, a.sf + row * (a.K / 32));
 }
 
-// One row in registers: VPT vectors per thread.
+// One row in registers: VPT eights per thread.
 template <int XT, int HT, int VPT>
 __global__ void __launch_bounds__(VPT == 1 ? 1024 : 512) rmsnorm_kernel(RmsnormArgs a) {
+    constexpr bool SPLIT = XT == kF32 || HT == kF32;
     __shared__ float red[2][1][32];
     const int64_t row = static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y;
     if (row >= a.M) return;   // whole warps, and only where a row has one warp
@@ -64,37 +66,32 @@ __global__ void __launch_bounds__(VPT == 1 ? 1024 : 512) rmsnorm_kernel(RmsnormA
     {
         Raw8<XT> rx[VPT];
 #pragma unroll
-        for (int i = 0; i < VPT; ++i) {
-            const int64_t e = 8 * (static_cast<int64_t>(threadIdx.x) + static_cast<int64_t>(i) * blockDim.x);
-            rx[i] = load_raw8<XT>(x, e, a.K - e);
-        }
+        for (int i = 0; i < VPT; ++i)
+            rx[i] = load_raw8<XT, SPLIT>(x, first8<SPLIT>(threadIdx.x, i, blockDim.x), a.K);
         if constexpr (HT != kNone) {
             const uint8_t *r = static_cast<const uint8_t *>(a.r) + row * a.ldr * elem_bytes<HT>;
             uint8_t *h = static_cast<uint8_t *>(a.h) + row * a.ldh * elem_bytes<HT>;
             Raw8<HT> rr[VPT];
 #pragma unroll
-            for (int i = 0; i < VPT; ++i) {
-                const int64_t e = 8 * (static_cast<int64_t>(threadIdx.x) + static_cast<int64_t>(i) * blockDim.x);
-                rr[i] = load_raw8<HT>(r, e, a.K - e);
-            }
+            for (int i = 0; i < VPT; ++i)
+                rr[i] = load_raw8<HT, SPLIT>(r, first8<SPLIT>(threadIdx.x, i, blockDim.x), a.K);
 #pragma unroll
             for (int i = 0; i < VPT; ++i) {
-                const int64_t e = 8 * (static_cast<int64_t>(threadIdx.x) + static_cast<int64_t>(i) * blockDim.x);
                 float f[8];
                 widen8<XT>(rx[i], v[i]);
                 widen8<HT>(rr[i], f);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) v[i][j] += f[j];
                 round8<HT>(v[i]);   // the norm is of the sum as it is stored
-                if (a.h) store8<HT>(h, e, a.K - e, v[i]);
+                if (a.h) store8<HT, SPLIT>(h, first8<SPLIT>(threadIdx.x, i, blockDim.x), a.K, v[i]);
             }
         } else {
 #pragma unroll
             for (int i = 0; i < VPT; ++i) widen8<XT>(rx[i], v[i]);
         }
     }
-    // with one vector per thread (few rows) the weights' latency overlaps the sum
-    if constexpr (VPT == 1) load8<kF32>(a.w, 8 * static_cast<int64_t>(threadIdx.x), a.K - 8 * static_cast<int64_t>(threadIdx.x), w);
+    // with one eight per thread (few rows) the weights' latency overlaps the sum
+    if constexpr (VPT == 1) load8<kF32, SPLIT>(a.w, first8<SPLIT>(threadIdx.x, 0, blockDim.x), a.K, w);
     float s[1] = {0.0f};
 #pragma unroll
     for (int i = 0; i < VPT; ++i)
@@ -105,9 +102,9 @@ __global__ void __launch_bounds__(VPT == 1 ? 1024 : 512) rmsnorm_kernel(RmsnormA
     if (a.rstd && threadIdx.x == 0) a.rstd[row] = rstd;
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-        const int64_t e = 8 * (static_cast<int64_t>(threadIdx.x) + static_cast<int64_t>(i) * blockDim.x);
-        if constexpr (VPT > 1) load8<kF32>(a.w, e, a.K - e, w);
-        rmsnorm_write(a, row, e, v[i], w, rstd);
+        const int64_t e = first8<SPLIT>(threadIdx.x, i, blockDim.x);
+        if constexpr (VPT > 1) load8<kF32, SPLIT>(a.w, e, a.K, w);
+        rmsnorm_write<SPLIT>(a, row, e, v[i], w, rstd);
     }
 }
 
@@ -116,28 +113,30 @@ __global__ void __launch_bounds__(VPT == 1 ? 1024 : 512) rmsnorm_kernel(RmsnormA
 // then holds h by now: each thread reads back what it wrote itself).
 template <int XT, int HT>
 __global__ void __launch_bounds__(1024) rmsnorm_long_kernel(RmsnormArgs a) {
+    constexpr bool SPLIT = XT == kF32 || HT == kF32;
     __shared__ float red[2][1][32];
     const int64_t row = blockIdx.x;
     const uint8_t *x = static_cast<const uint8_t *>(a.x) + row * a.ldx * elem_bytes<XT>;
     const uint8_t *r = static_cast<const uint8_t *>(a.r) + row * a.ldr * elem_bytes<HT>;
     uint8_t *h = static_cast<uint8_t *>(a.h) + row * a.ldh * elem_bytes<HT>;
-    const int64_t step = 8 * static_cast<int64_t>(blockDim.x);
+    const int64_t steps = (a.K + 8191) / 8192;
     auto sum_of = [&](int64_t e, float (&v)[8]) {
-        load8<XT>(x, e, a.K - e, v);
+        load8<XT, SPLIT>(x, e, a.K, v);
         if constexpr (HT != kNone) {
             float f[8];
-            load8<HT>(r, e, a.K - e, f);
+            load8<HT, SPLIT>(r, e, a.K, f);
 #pragma unroll
             for (int j = 0; j < 8; ++j) v[j] += f[j];
             round8<HT>(v);
         }
     };
     float s[1] = {0.0f};
-    for (int64_t e = 8 * static_cast<int64_t>(threadIdx.x); e < a.K; e += step) {
+    for (int64_t i = 0; i < steps; ++i) {
+        const int64_t e = 8192 * i + first8<SPLIT>(threadIdx.x, 0, 1024);
         float v[8];
         sum_of(e, v);
         if constexpr (HT != kNone) {
-            if (a.h) store8<HT>(h, e, a.K - e, v);
+            if (a.h) store8<HT, SPLIT>(h, e, a.K, v);
         }
         float p = 0.0f;
 #pragma unroll
@@ -147,14 +146,13 @@ __global__ void __launch_bounds__(1024) rmsnorm_long_kernel(RmsnormArgs a) {
     row_sum<1>(s, red, 0);
     const float rstd = 1.0f / sqrtf(s[0] / static_cast<float>(a.K) + a.eps);
     if (a.rstd && threadIdx.x == 0) a.rstd[row] = rstd;
-    // every thread of a warp stays in the loop (the codes' maximum is taken across lanes)
-    for (int64_t e0 = 0; e0 < a.K; e0 += step) {
-        const int64_t e = e0 + 8 * static_cast<int64_t>(threadIdx.x);
+    for (int64_t i = 0; i < steps; ++i) {
+        const int64_t e = 8192 * i + first8<SPLIT>(threadIdx.x, 0, 1024);
         float v[8], w[8];
-        if (HT != kNone && a.h) load8<HT == kNone ? kF32 : HT>(h, e, a.K - e, v);
+        if (HT != kNone && a.h) load8<HT == kNone ? kF32 : HT, SPLIT>(h, e, a.K, v);
         else sum_of(e, v);
-        load8<kF32>(a.w, e, a.K - e, w);
-        rmsnorm_write(a, row, e, v, w, rstd);
+        load8<kF32, SPLIT>(a.w, e, a.K, w);
+        rmsnorm_write<SPLIT>(a, row, e, v, w, rstd);
     }
 }
 
@@ -167,79 +165,190 @@ struct RmsnormBackArgs {
     void *dh;
     float *partial;   // [gridDim.x][K]: this block's share of dw; null: no dw
     int64_t M, K, lddy, ldh, lddr, lddh;
+    int ring;         // rows in shared memory at a time: 2, 3 or 4
+    float inv_k;      // 1 / K
 };
+
+// This thread's eight elements at e into shared memory, asynchronously, the
+// row's end included (a thread that waited for its few last elements there
+// would hold up the whole block once per row).  Copied by the thread that
+// reads them back, so that no barrier stands between.  What lies at K and
+// beyond stays as it is in the slot.
+template <int BYTES>
+__device__ __forceinline__ void stage_copy(uint8_t *dst, const uint8_t *src) {
+    const uint32_t d = static_cast<uint32_t>(__cvta_generic_to_shared(dst));
+    if constexpr (BYTES == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(d), "l"(src) : "memory");
+    else if constexpr (BYTES == 2)      // two bytes read, two more zero
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4, 2;" ::"r"(d), "l"(src) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(d), "l"(src), "n"(BYTES) : "memory");
+}
+
+template <int T>
+__device__ __forceinline__ void stage4(uint8_t *dst, const uint8_t *src, int n) {
+    if (n >= 4) {
+        stage_copy<4 * elem_bytes<T>>(dst, src);
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 3; i += 4 / elem_bytes<T>) {
+        if (i + 4 / elem_bytes<T> <= n) stage_copy<4>(dst + i * elem_bytes<T>, src + i * elem_bytes<T>);
+        else if (i < n) stage_copy<2>(dst + i * elem_bytes<T>, src + i * elem_bytes<T>);
+    }
+}
+
+template <int T, bool SPLIT>
+__device__ __forceinline__ void stage8(uint8_t *slot, unsigned pitch, const uint8_t *row, int e, int K) {
+    const uint8_t *p = row + e * elem_bytes<T>;
+    if constexpr (T == kBF16 && !SPLIT) {
+        if (e + 8 <= K) {
+            stage_copy<16>(slot, p);
+            return;
+        }
+    }
+    stage4<T>(slot, p, K - e);
+    stage4<T>(slot + (T == kF32 ? pitch : 8), p + at8<SPLIT>(4) * elem_bytes<T>, K - e - at8<SPLIT>(4));
+}
+
+template <int T>
+__device__ __forceinline__ void staged8(const uint8_t *slot, unsigned pitch, float (&f)[8]) {
+    Raw8<T> r;
+#pragma unroll
+    for (int i = 0; i < (T == kF32 ? 2 : 1); ++i) r.v[i] = *reinterpret_cast<const uint4 *>(slot + i * pitch);
+    widen8<T>(r, f);
+}
+
+// 16-byte pieces per vector of dy, h and dr
+template <int YT, int HT, int DT>
+constexpr int back_pieces = (YT == kF32 ? 2 : 1) + (HT == kF32 ? 2 : 1) + (DT == kF32 ? 2 : 1);
 
 // Persistent blocks: block b takes rows b, b + gridDim.x, ... (times
 // blockDim.y) and keeps its share of dw in registers, written out once at
 // the end and summed over the blocks by rmsnorm_dw_kernel in block order.
+// The next rows are on their way into shared memory while one is summed and
+// written (the barrier in the middle of each row would leave memory idle
+// otherwise), and what a row's second half needs is read from there again,
+// which keeps registers free.
 template <int YT, int HT, int DT, int VPT>
-__global__ void __launch_bounds__(VPT == 1 ? 1024 : 512) rmsnorm_back_kernel(RmsnormBackArgs a) {
+__global__ void __launch_bounds__(512) rmsnorm_back_kernel(RmsnormBackArgs a) {
+    constexpr bool SPLIT = YT == kF32 || HT == kF32 || DT == kF32;
     __shared__ float red[2][1][32];
-    float dw[VPT][8] = {};
-    int phase = 0;
+    extern __shared__ __align__(16) uint8_t dyn[];
+    constexpr int kY = YT == kF32 ? 2 : 1, kH = HT == kF32 ? 2 : 1, kPieces = back_pieces<YT, HT, DT>;
+    const unsigned pitch = 16 * blockDim.x * blockDim.y;       // between a thread's pieces
+    const unsigned row_pitch = VPT * kPieces * pitch, ring_end = a.ring * row_pitch;
+    uint8_t *const mine = dyn + 16 * (threadIdx.y * blockDim.x + threadIdx.x);
     const int64_t stride = static_cast<int64_t>(gridDim.x) * blockDim.y;
-    for (int64_t row = static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y; row < a.M; row += stride) {
-        const uint8_t *dy = static_cast<const uint8_t *>(a.dy) + row * a.lddy * elem_bytes<YT>;
-        const uint8_t *h = static_cast<const uint8_t *>(a.h) + row * a.ldh * elem_bytes<HT>;
-        const uint8_t *dr = static_cast<const uint8_t *>(a.dr) + row * a.lddr * elem_bytes<DT>;
-        uint8_t *dh = static_cast<uint8_t *>(a.dh) + row * a.lddh * elem_bytes<DT>;
-        const float rstd = a.rstd[row];
-        Raw8<YT> ry[VPT];
-        Raw8<HT> rh[VPT];
-        Raw8<DT> rr[VPT];
-#pragma unroll
-        for (int i = 0; i < VPT; ++i) {
-            const int64_t e = 8 * (static_cast<int64_t>(threadIdx.x) + static_cast<int64_t>(i) * blockDim.x);
-            ry[i] = load_raw8<YT>(dy, e, a.K - e);
-            rh[i] = load_raw8<HT>(h, e, a.K - e);
-        }
-        if (a.dr) {
+    const int64_t first = static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y;
+    const int K = static_cast<int>(a.K);                       // at most 16384 here
+    unsigned fill = 0;
+    // the next row to load, and this thread's first vector of it
+    const int e0 = static_cast<int>(first8<SPLIT>(threadIdx.x, 0, blockDim.x));
+    int64_t ahead = first;
+    const uint8_t *dy = static_cast<const uint8_t *>(a.dy) + first * a.lddy * elem_bytes<YT>;
+    const uint8_t *h = static_cast<const uint8_t *>(a.h) + first * a.ldh * elem_bytes<HT>;
+    const uint8_t *dr = static_cast<const uint8_t *>(a.dr) + first * a.lddr * elem_bytes<DT>;
+    const int64_t dy_step = stride * a.lddy * elem_bytes<YT>, h_step = stride * a.ldh * elem_bytes<HT>;
+    const int64_t dr_step = stride * a.lddr * elem_bytes<DT>;
+    auto load_row = [&]() {
+        if (ahead < a.M) {
 #pragma unroll
             for (int i = 0; i < VPT; ++i) {
-                const int64_t e = 8 * (static_cast<int64_t>(threadIdx.x) + static_cast<int64_t>(i) * blockDim.x);
-                rr[i] = load_raw8<DT>(dr, e, a.K - e);
+                const int e = e0 + 8 * i * static_cast<int>(blockDim.x);
+                if (e >= K) break;
+                uint8_t *p = mine + fill + i * kPieces * pitch;
+                stage8<YT, SPLIT>(p, pitch, dy, e, K);
+                stage8<HT, SPLIT>(p + kY * pitch, pitch, h, e, K);
+                if (a.dr) stage8<DT, SPLIT>(p + (kY + kH) * pitch, pitch, dr, e, K);
             }
         }
+        ahead += stride;
+        dy += dy_step;
+        h += h_step;
+        dr += dr_step;
+        fill = fill + row_pitch == ring_end ? 0 : fill + row_pitch;
+        asm volatile("cp.async.commit_group;" ::: "memory");   // one group per row, empty ones too
+    };
+    // elements past K read as zero from every slot: they add nothing to any sum
+    for (int r = 0; r < a.ring; ++r)
+#pragma unroll
+        for (int i = 0; i < VPT; ++i)
+            if (e0 + 8 * i * static_cast<int>(blockDim.x) + at8<SPLIT>(7) >= K)
+                for (int q = 0; q < kPieces; ++q)
+                    *reinterpret_cast<uint4 *>(mine + r * row_pitch + (i * kPieces + q) * pitch) =
+                        make_uint4(0, 0, 0, 0);
+    for (int i = 1; i < a.ring; ++i) load_row();
+
+    float dw[VPT][8] = {}, w[VPT][8];
+    if constexpr (VPT < 4) {
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            const int e = e0 + 8 * i * static_cast<int>(blockDim.x);
+            load8<kF32, SPLIT>(a.w, e, K, w[i]);
+        }
+    }
+    float rstd = first < a.M ? a.rstd[first] : 0.0f;
+    uint8_t *dh = static_cast<uint8_t *>(a.dh) + first * a.lddh * elem_bytes<DT>;
+    int phase = 0;
+    unsigned slot = 0;
+    for (int64_t row = first; row < a.M; row += stride) {
+        if (a.ring == 4) asm volatile("cp.async.wait_group 2;" ::: "memory");
+        else if (a.ring == 3) asm volatile("cp.async.wait_group 1;" ::: "memory");
+        else asm volatile("cp.async.wait_group 0;" ::: "memory");
+        load_row();     // into the slot this thread read in the previous iteration
+        const float next_rstd = row + stride < a.M ? a.rstd[row + stride] : 0.0f;
         float s[1] = {0.0f};
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
-            const int64_t e = 8 * (static_cast<int64_t>(threadIdx.x) + static_cast<int64_t>(i) * blockDim.x);
-            float y[8], v[8], w[8];
-            widen8<YT>(ry[i], y);
-            widen8<HT>(rh[i], v);
-            load8<kF32>(a.w, e, a.K - e, w);
+            const int e = e0 + 8 * i * static_cast<int>(blockDim.x);
+            const uint8_t *p = mine + slot + i * kPieces * pitch;
+            float y[8], v[8];
+            staged8<YT>(p, pitch, y);
+            staged8<HT>(p + kY * pitch, pitch, v);
+            if constexpr (VPT == 4) load8<kF32, SPLIT>(a.w, e, K, w[i]);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                const float n = v[j] * rstd;
-                s[0] += y[j] * w[j] * n;
-                dw[i][j] += y[j] * n;
+                const float p = y[j] * v[j];        // dy h: times rstd for dw, times w for the sum
+                dw[i][j] += p * rstd;
+                s[0] += p * w[i][j];
             }
         }
         row_sum<1>(s, red, phase);
         phase ^= 1;
-        const float mean = s[0] / static_cast<float>(a.K);
+        // n mean(g n) = h c with c = rstd^2 sum(dy h w) / K
+        const float c = rstd * rstd * (s[0] * a.inv_k);
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
-            const int64_t e = 8 * (static_cast<int64_t>(threadIdx.x) + static_cast<int64_t>(i) * blockDim.x);
-            float y[8], v[8], w[8], d[8];
-            widen8<YT>(ry[i], y);
-            widen8<HT>(rh[i], v);
-            load8<kF32>(a.w, e, a.K - e, w);
+            const int e = e0 + 8 * i * static_cast<int>(blockDim.x);
+            const uint8_t *p = mine + slot + i * kPieces * pitch;
+            float y[8], v[8], d[8];
+            staged8<YT>(p, pitch, y);
+            staged8<HT>(p + kY * pitch, pitch, v);
+            if constexpr (VPT == 4) load8<kF32, SPLIT>(a.w, e, K, w[i]);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) d[j] = rstd * (y[j] * w[j] - v[j] * rstd * mean);
+            for (int j = 0; j < 8; ++j) d[j] = y[j] * w[i][j] - v[j] * c;
             if (a.dr) {
                 float f[8];
-                widen8<DT>(rr[i], f);
+                staged8<DT>(p + (kY + kH) * pitch, pitch, f);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) d[j] += f[j];
+                for (int j = 0; j < 8; ++j) d[j] = rstd * d[j] + f[j];
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) d[j] *= rstd;
             }
-            store8<DT>(dh, e, a.K - e, d);
+            store8<DT, SPLIT>(dh, e, K, d);
         }
+        rstd = next_rstd;
+        dh += stride * a.lddh * elem_bytes<DT>;
+        slot = slot + row_pitch == ring_end ? 0 : slot + row_pitch;
     }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
     if (!a.partial) return;
     // the rows of one block (short rows: one warp each) in threadIdx.y order
-    extern __shared__ float acc[];
     if (blockDim.y > 1) {
+        float *acc = reinterpret_cast<float *>(dyn);
+        __syncthreads();
         for (unsigned r = 0; r < blockDim.y; ++r) {
             if (threadIdx.y == r) {
 #pragma unroll
@@ -258,17 +367,17 @@ __global__ void __launch_bounds__(VPT == 1 ? 1024 : 512) rmsnorm_back_kernel(Rms
 #pragma unroll
             for (int j = 0; j < 8; ++j) dw[i][j] = acc[(i * 8 + j) * 32 + threadIdx.x];
     }
-    // rows of `partial` are K floats apart, which need not keep 16-byte alignment
+    // rows of `partial` are K floats apart: 16-byte aligned where K is a multiple of four
     float *p = a.partial + static_cast<int64_t>(blockIdx.x) * a.K;
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-        const int64_t e = 8 * (static_cast<int64_t>(threadIdx.x) + static_cast<int64_t>(i) * blockDim.x);
-        if ((a.K & 3) == 0) {
-            store8<kF32>(p, e, a.K - e, dw[i]);
+        const int e = e0 + 8 * i * static_cast<int>(blockDim.x);
+        if ((K & 3) == 0) {
+            store8<kF32, SPLIT>(p, e, K, dw[i]);
         } else {
 #pragma unroll
             for (int j = 0; j < 8; ++j)
-                if (e + j < a.K) p[e + j] = dw[i][j];
+                if (e + at8<SPLIT>(j) < K) p[e + at8<SPLIT>(j)] = dw[i][j];
         }
     }
 }
@@ -277,9 +386,10 @@ __global__ void __launch_bounds__(VPT == 1 ? 1024 : 512) rmsnorm_back_kernel(Rms
 // of dw kept in `partial` itself (each thread owns its columns there).
 template <int YT, int HT, int DT>
 __global__ void __launch_bounds__(1024) rmsnorm_back_long_kernel(RmsnormBackArgs a) {
+    constexpr bool SPLIT = YT == kF32 || HT == kF32 || DT == kF32;
     __shared__ float red[2][1][32];
     int phase = 0;
-    const int64_t step = 8 * static_cast<int64_t>(blockDim.x);
+    const int64_t steps = (a.K + 8191) / 8192;
     bool first = true;
     for (int64_t row = blockIdx.x; row < a.M; row += gridDim.x, first = false) {
         const uint8_t *dy = static_cast<const uint8_t *>(a.dy) + row * a.lddy * elem_bytes<YT>;
@@ -288,11 +398,12 @@ __global__ void __launch_bounds__(1024) rmsnorm_back_long_kernel(RmsnormBackArgs
         uint8_t *dh = static_cast<uint8_t *>(a.dh) + row * a.lddh * elem_bytes<DT>;
         const float rstd = a.rstd[row];
         float s[1] = {0.0f};
-        for (int64_t e = 8 * static_cast<int64_t>(threadIdx.x); e < a.K; e += step) {
+        for (int64_t i = 0; i < steps; ++i) {
+            const int64_t e = 8192 * i + first8<SPLIT>(threadIdx.x, 0, 1024);
             float y[8], v[8], w[8], p = 0.0f;
-            load8<YT>(dy, e, a.K - e, y);
-            load8<HT>(h, e, a.K - e, v);
-            load8<kF32>(a.w, e, a.K - e, w);
+            load8<YT, SPLIT>(dy, e, a.K, y);
+            load8<HT, SPLIT>(h, e, a.K, v);
+            load8<kF32, SPLIT>(a.w, e, a.K, w);
 #pragma unroll
             for (int j = 0; j < 8; ++j) p += y[j] * w[j] * (v[j] * rstd);
             s[0] += p;
@@ -300,48 +411,52 @@ __global__ void __launch_bounds__(1024) rmsnorm_back_long_kernel(RmsnormBackArgs
         row_sum<1>(s, red, phase);
         phase ^= 1;
         const float mean = s[0] / static_cast<float>(a.K);
-        for (int64_t e = 8 * static_cast<int64_t>(threadIdx.x); e < a.K; e += step) {
+        for (int64_t i = 0; i < steps; ++i) {
+            const int64_t e = 8192 * i + first8<SPLIT>(threadIdx.x, 0, 1024);
             float y[8], v[8], w[8], d[8];
-            load8<YT>(dy, e, a.K - e, y);
-            load8<HT>(h, e, a.K - e, v);
-            load8<kF32>(a.w, e, a.K - e, w);
-            if (a.dr) load8<DT>(dr, e, a.K - e, d);
+            load8<YT, SPLIT>(dy, e, a.K, y);
+            load8<HT, SPLIT>(h, e, a.K, v);
+            load8<kF32, SPLIT>(a.w, e, a.K, w);
+            if (a.dr) load8<DT, SPLIT>(dr, e, a.K, d);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 const float n = v[j] * rstd;
                 const float g = rstd * (y[j] * w[j] - n * mean);
                 d[j] = a.dr ? g + d[j] : g;
-                if (a.partial && e + j < a.K) {
-                    float *p = a.partial + static_cast<int64_t>(blockIdx.x) * a.K + e + j;
+                if (a.partial && e + at8<SPLIT>(j) < a.K) {
+                    float *p = a.partial + static_cast<int64_t>(blockIdx.x) * a.K + e + at8<SPLIT>(j);
                     *p = first ? y[j] * n : *p + y[j] * n;
                 }
             }
-            store8<DT>(dh, e, a.K - e, d);
+            store8<DT, SPLIT>(dh, e, a.K, d);
         }
     }
 }
 
-// dw[k] = sum over the blocks' shares, in block order within each of the 8
-// warps of a block and then over the warps: 32 columns per block.
-__global__ void __launch_bounds__(256) rmsnorm_dw_kernel(const float *__restrict__ partial, float *dw, int64_t rows,
-                                                         int64_t K) {
-    __shared__ float part[8][32];
-    const int64_t col = static_cast<int64_t>(blockIdx.x) * 32 + threadIdx.x % 32;
-    const int warp = threadIdx.x / 32;
+// dw[k] = sum over the blocks' shares: 32 columns per block, each of its 32
+// warps adds every 32nd share, then warp w adds the 32 sums of column w: a fixed
+// order, and all of a warp's loads (at most ten) are in flight together.
+__global__ void __launch_bounds__(1024) rmsnorm_dw_kernel(const float *__restrict__ partial, float *dw, int rows,
+                                                          int64_t K) {
+    __shared__ float part[32][33];
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+    const int64_t col = static_cast<int64_t>(blockIdx.x) * 32 + lane;
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    float s = 0.0f;
-    if (col < K) {
-#pragma unroll 4
-        for (int64_t r = warp; r < rows; r += 8) s += __ldcg(&partial[r * K + col]);
-    }
-    part[warp][threadIdx.x % 32] = s;
-    __syncthreads();
-    if (warp == 0 && col < K) {
-        s = 0.0f;
+    float v[10];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) s += part[i][threadIdx.x];
-        dw[col] = s;
+    for (int i = 0; i < 10; ++i) {
+        const int r = warp + 32 * i;
+        v[i] = col < K && r < rows ? __ldcg(&partial[r * K + col]) : 0.0f;
     }
+    float s = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 10; ++i) s += v[i];
+    part[warp][lane] = s;
+    __syncthreads();
+    // warp w sums column w over the 32 warps
+    s = warp_sum(part[lane][warp]);
+    const int64_t out = static_cast<int64_t>(blockIdx.x) * 32 + warp;
+    if (lane == 0 && out < K) dw[out] = s;
 }
 
 }  // namespace b200

@@ -1,5 +1,5 @@
-// Row-wise building blocks of the operators around the products: 16-byte
-// vectors of eight elements (bf16 or fp32), fixed-order sums, and the MXFP8
+// Row-wise building blocks of the operators around the products: eight
+// elements (bf16 or fp32) per thread and step, fixed-order sums, and the MXFP8
 // encoding of 32 consecutive values.
 #pragma once
 #include <cuda_bf16.h>
@@ -14,35 +14,75 @@ constexpr int kF32 = 0, kBF16 = 1, kNone = 2;
 template <int T>
 constexpr int elem_bytes = T == kF32 ? 4 : 2;
 
-// Eight consecutive elements as they are in memory.
+// Eight elements of a row, as they are in memory: a thread's share of one step.
+// With SPLIT they are two groups of four, 128 elements apart, so that each
+// load or store instruction of a warp covers consecutive bytes when an
+// operand is fp32 (eight consecutive fp32 per thread would touch every
+// 32-byte sector twice); without it they are consecutive, one 16-byte access
+// of bf16.  e is the first one's index; element j of the eight is at
+// e + at8<SPLIT>(j).
 template <int T>
 struct Raw8 {
     uint4 v[T == kF32 ? 2 : 1];
 };
 
-// Elements [e, e + 8) of a row, the first n of them valid (n may be below 0 or
-// above 8); the others read as zero without touching memory.  e is a multiple
-// of 8 and the row 16-byte aligned, so a full vector is one or two 16-byte
-// loads.
+template <bool SPLIT>
+__device__ __forceinline__ constexpr int at8(int j) {
+    return SPLIT && j >= 4 ? j + 124 : j;
+}
+
+// First index of the i-th eight of a thread, in a row that `threads` share
+// (a multiple of 32).
+template <bool SPLIT>
+__device__ __forceinline__ int64_t first8(unsigned thread, unsigned i, unsigned threads) {
+    const int64_t t = static_cast<int64_t>(i) * threads + thread;
+    return SPLIT ? 8 * (t & ~static_cast<int64_t>(31)) + 4 * (thread & 31) : 8 * t;
+}
+
+// Four elements from p on, the first n of them valid, as words (fp32: four,
+// bf16: two); the others are zero, without touching memory.
 template <int T>
-__device__ __forceinline__ Raw8<T> load_raw8(const void *row, int64_t e, int64_t n) {
-    Raw8<T> r;
-    const uint8_t *p = static_cast<const uint8_t *>(row) + e * elem_bytes<T>;
-    if (n >= 8) {
-#pragma unroll
-        for (int i = 0; i < (T == kF32 ? 2 : 1); ++i) r.v[i] = reinterpret_cast<const uint4 *>(p)[i];
-        return r;
+__device__ __forceinline__ void load_raw4(const uint8_t *p, int64_t n, uint32_t *w) {
+    if (n >= 4) {
+        if constexpr (T == kF32) {
+            const uint4 v = *reinterpret_cast<const uint4 *>(p);
+            w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+        } else {
+            const uint2 v = *reinterpret_cast<const uint2 *>(p);
+            w[0] = v.x, w[1] = v.y;
+        }
+        return;
     }
-    uint32_t w[T == kF32 ? 8 : 4] = {};
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < (T == kF32 ? 4 : 2); ++i) w[i] = 0u;
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
         if (i < n) {
             if constexpr (T == kF32) w[i] = reinterpret_cast<const uint32_t *>(p)[i];
             else w[i / 2] |= static_cast<uint32_t>(reinterpret_cast<const uint16_t *>(p)[i]) << (16 * (i & 1));
         }
     }
+}
+
+// The eight elements at e, those at K and beyond as zero.  Rows are 16-byte
+// aligned and groups start at multiples of four (SPLIT) or eight, so a whole
+// group is one aligned access.
+template <int T, bool SPLIT>
+__device__ __forceinline__ Raw8<T> load_raw8(const void *row, int64_t e, int64_t K) {
+    Raw8<T> r;
+    const uint8_t *p = static_cast<const uint8_t *>(row) + e * elem_bytes<T>;
+    if constexpr (T == kBF16 && !SPLIT) {
+        if (e + 8 <= K) {
+            r.v[0] = *reinterpret_cast<const uint4 *>(p);
+            return r;
+        }
+    }
+    uint32_t w[T == kF32 ? 8 : 4];
+    load_raw4<T>(p, K - e, w);
+    load_raw4<T>(p + at8<SPLIT>(4) * elem_bytes<T>, K - e - at8<SPLIT>(4), w + (T == kF32 ? 4 : 2));
 #pragma unroll
-    for (int i = 0; i < (T == kF32 ? 2 : 1); ++i) r.v[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+    for (int i = 0; i < (T == kF32 ? 2 : 1); ++i)
+        r.v[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
     return r;
 }
 
@@ -66,9 +106,9 @@ __device__ __forceinline__ void widen8(const Raw8<T> &r, float (&f)[8]) {
     }
 }
 
-template <int T>
-__device__ __forceinline__ void load8(const void *row, int64_t e, int64_t n, float (&f)[8]) {
-    widen8<T>(load_raw8<T>(row, e, n), f);
+template <int T, bool SPLIT>
+__device__ __forceinline__ void load8(const void *row, int64_t e, int64_t K, float (&f)[8]) {
+    widen8<T>(load_raw8<T, SPLIT>(row, e, K), f);
 }
 
 __device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
@@ -76,28 +116,36 @@ __device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
     return *reinterpret_cast<const uint32_t *>(&p);
 }
 
-// Writes elements [e, e + 8) of a row, the first n of them, rounded to T
-// (nearest even); nothing outside them is written.
 template <int T>
-__device__ __forceinline__ void store8(void *row, int64_t e, int64_t n, const float (&f)[8]) {
-    uint8_t *p = static_cast<uint8_t *>(row) + e * elem_bytes<T>;
-    if (n >= 8) {
-        if constexpr (T == kF32) {
-            reinterpret_cast<float4 *>(p)[0] = make_float4(f[0], f[1], f[2], f[3]);
-            reinterpret_cast<float4 *>(p)[1] = make_float4(f[4], f[5], f[6], f[7]);
-        } else {
-            *reinterpret_cast<uint4 *>(p) = make_uint4(bf16_pair(f[0], f[1]), bf16_pair(f[2], f[3]),
-                                                       bf16_pair(f[4], f[5]), bf16_pair(f[6], f[7]));
-        }
+__device__ __forceinline__ void store4(uint8_t *p, int64_t n, const float *f) {
+    if (n >= 4) {
+        if constexpr (T == kF32) *reinterpret_cast<float4 *>(p) = make_float4(f[0], f[1], f[2], f[3]);
+        else *reinterpret_cast<uint2 *>(p) = make_uint2(bf16_pair(f[0], f[1]), bf16_pair(f[2], f[3]));
         return;
     }
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < 3; ++i) {
         if (i < n) {
             if constexpr (T == kF32) reinterpret_cast<float *>(p)[i] = f[i];
             else reinterpret_cast<__nv_bfloat16 *>(p)[i] = __float2bfloat16_rn(f[i]);
         }
     }
+}
+
+// Writes the eight elements at e, rounded to T (nearest even); those at K and
+// beyond are not written.
+template <int T, bool SPLIT>
+__device__ __forceinline__ void store8(void *row, int64_t e, int64_t K, const float (&f)[8]) {
+    uint8_t *p = static_cast<uint8_t *>(row) + e * elem_bytes<T>;
+    if constexpr (T == kBF16 && !SPLIT) {
+        if (e + 8 <= K) {
+            *reinterpret_cast<uint4 *>(p) = make_uint4(bf16_pair(f[0], f[1]), bf16_pair(f[2], f[3]),
+                                                       bf16_pair(f[4], f[5]), bf16_pair(f[6], f[7]));
+            return;
+        }
+    }
+    store4<T>(p, K - e, &f[0]);
+    store4<T>(p + at8<SPLIT>(4) * elem_bytes<T>, K - e - at8<SPLIT>(4), &f[4]);
 }
 
 // The values as they will read back once stored as T.
@@ -123,16 +171,11 @@ __device__ __forceinline__ float warp_sum(float v) {
 // is v / 2^e rounded to nearest even.  NaN and infinities get E4M3's NaN code
 // 0x7F and do not count for the scale (E4M3 has no infinity).
 
-// Largest finite |v| of 8 values, as the bits of a non-negative fp32 (which
-// order as the values do).
-__device__ __forceinline__ uint32_t finite_max_bits(const float (&v)[8]) {
-    uint32_t m = 0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const uint32_t b = __float_as_uint(v[i]) & 0x7FFFFFFFu;
-        m = max(m, b < 0x7F800000u ? b : 0u);
-    }
-    return m;
+// Bits of the largest finite |v|, a non-negative fp32 (whose bits order as the
+// values do).
+__device__ __forceinline__ uint32_t finite_max_bits(uint32_t m, float v) {
+    const uint32_t b = __float_as_uint(v) & 0x7FFFFFFFu;
+    return max(m, b < 0x7F800000u ? b : 0u);
 }
 
 // The E8M0 byte (e + 127) for a block whose largest magnitude has these bits:
@@ -158,23 +201,45 @@ __device__ __forceinline__ uint32_t e4m3_pair(float lo, float hi, float inv) {
     return d;
 }
 
-__device__ __forceinline__ uint2 e4m3_codes8(const float (&v)[8], float inv) {
-    return make_uint2(e4m3_pair(v[0], v[1], inv) | (e4m3_pair(v[2], v[3], inv) << 16),
-                      e4m3_pair(v[4], v[5], inv) | (e4m3_pair(v[6], v[7], inv) << 16));
+__device__ __forceinline__ uint32_t e4m3_codes4(const float *v, float inv) {
+    return e4m3_pair(v[0], v[1], inv) | (e4m3_pair(v[2], v[3], inv) << 16);
 }
 
-// Encodes a block held by four consecutive lanes, eight values each (lane & 3
-// gives the order).  All 32 lanes of the warp call it; those without a block
-// pass zeros and active = false.  q: this lane's 8 codes (8-byte aligned);
-// sf: the block's scale byte.
-__device__ __forceinline__ void mx_store8(const float (&v)[8], bool active, uint8_t *q, uint8_t *sf) {
-    uint32_t m = finite_max_bits(v);
-    m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
-    m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
-    if (!active) return;
-    const uint32_t byte = mx_scale_byte(m);
-    *reinterpret_cast<uint2 *>(q) = e4m3_codes8(v, mx_inv_scale(byte));
-    if ((threadIdx.x & 3) == 0) *sf = static_cast<uint8_t>(byte);
+// Encodes the eights of a warp (the values at e of each lane, K a multiple of
+// 32): a block of 32 is four lanes' eights, or with SPLIT eight lanes' fours.
+// All 32 lanes call it, those past K with zeros.  q, sf: the row's codes
+// and scales.
+template <bool SPLIT>
+__device__ __forceinline__ void mx_store8(const float (&v)[8], int64_t e, int64_t K, uint8_t *q, uint8_t *sf) {
+    if constexpr (SPLIT) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            uint32_t m = 0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) m = finite_max_bits(m, v[4 * h + i]);
+            m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+            m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
+            m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 4));
+            const int64_t eh = e + 128 * h;
+            if (eh < K) {
+                const uint32_t byte = mx_scale_byte(m);
+                *reinterpret_cast<uint32_t *>(q + eh) = e4m3_codes4(&v[4 * h], mx_inv_scale(byte));
+                if ((threadIdx.x & 7) == 0) sf[eh / 32] = static_cast<uint8_t>(byte);
+            }
+        }
+    } else {
+        uint32_t m = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) m = finite_max_bits(m, v[i]);
+        m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+        m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
+        if (e < K) {
+            const uint32_t byte = mx_scale_byte(m);
+            const float inv = mx_inv_scale(byte);
+            *reinterpret_cast<uint2 *>(q + e) = make_uint2(e4m3_codes4(&v[0], inv), e4m3_codes4(&v[4], inv));
+            if ((threadIdx.x & 3) == 0) sf[e / 32] = static_cast<uint8_t>(byte);
+        }
+    }
 }
 
 }  // namespace b200
