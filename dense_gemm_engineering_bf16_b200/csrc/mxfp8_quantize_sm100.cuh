@@ -31,54 +31,78 @@ __global__ void __launch_bounds__(256) mx_quantize_kernel(const void *x, uint8_t
 
 // X stored MN-major (K rows of M: element (i, k) at X[k * ldx + i]).  A warp
 // takes 32 K of 64 rows i, two per lane: 32 coalesced loads, then each lane
-// holds two whole blocks and writes each as 32 consecutive bytes.  The four
-// warps of a block take 128 consecutive K, so that they fill whole 128-byte
-// lines of codes together.
+// holds two whole blocks, without a shuffle.  The four warps of a block take
+// 128 consecutive K; their codes and scales meet in shared memory, from where
+// each row i goes out as one 128-byte line of codes and its four scales
+// together (written straight from the lanes, 32 bytes of a row each and single
+// scale bytes, the stores took as long as the rest: 8192 x 8192 bf16 in 58 us).
 template <int XT>
 __global__ void __launch_bounds__(128) mx_quantize_mn_kernel(const void *x, uint8_t *q, uint8_t *sf, int64_t M,
                                                              int64_t K, int64_t ldx, int64_t ldq, int64_t k_tiles) {
+    constexpr int kPitch = 128 + 16;
+    __shared__ __align__(16) uint8_t tile[64 * kPitch];
+    __shared__ __align__(4) uint8_t scales[64][4];
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-    const int64_t i = (static_cast<int64_t>(blockIdx.x) / k_tiles) * 64 + 2 * lane;
-    const int64_t k0 = (static_cast<int64_t>(blockIdx.x) % k_tiles) * 128 + 32 * warp;
-    if (k0 >= K || i >= M) return;
-    const bool two = i + 1 < M;
-    const uint8_t *p = static_cast<const uint8_t *>(x) + (k0 * ldx + i) * elem_bytes<XT>;
-    const int64_t pitch = ldx * elem_bytes<XT>;
-    float v[2][32];
+    const int64_t i0 = (static_cast<int64_t>(blockIdx.x) / k_tiles) * 64;
+    const int64_t kb = (static_cast<int64_t>(blockIdx.x) % k_tiles) * 128, k0 = kb + 32 * warp;
+    const int64_t left = M - i0 - 2 * lane;      // rows from this lane's first on
+    if (k0 < K && left > 0) {
+        const uint8_t *p = static_cast<const uint8_t *>(x) + (k0 * ldx + i0 + 2 * lane) * elem_bytes<XT>;
+        const int64_t pitch = ldx * elem_bytes<XT>;
+        float v[2][32];
+        if (left > 1) {
 #pragma unroll
-    for (int k = 0; k < 32; ++k) {
-        const uint8_t *pk = p + k * pitch;
-        if constexpr (XT == kF32) {
-            if (two) {
-                const float2 f = *reinterpret_cast<const float2 *>(pk);
-                v[0][k] = f.x;
-                v[1][k] = f.y;
-            } else {
-                v[0][k] = *reinterpret_cast<const float *>(pk);
-                v[1][k] = 0.0f;
+            for (int k = 0; k < 32; ++k) {
+                if constexpr (XT == kF32) {
+                    const float2 f = *reinterpret_cast<const float2 *>(p + k * pitch);
+                    v[0][k] = f.x;
+                    v[1][k] = f.y;
+                } else {
+                    const uint32_t w = *reinterpret_cast<const uint32_t *>(p + k * pitch);
+                    v[0][k] = __uint_as_float(w << 16);
+                    v[1][k] = __uint_as_float(w & 0xFFFF0000u);
+                }
             }
         } else {
-            const uint32_t w = two ? *reinterpret_cast<const uint32_t *>(pk) : *reinterpret_cast<const uint16_t *>(pk);
-            v[0][k] = __uint_as_float(w << 16);
-            v[1][k] = __uint_as_float(w & 0xFFFF0000u);
+#pragma unroll
+            for (int k = 0; k < 32; ++k) {
+                if constexpr (XT == kF32)
+                    v[0][k] = *reinterpret_cast<const float *>(p + k * pitch);
+                else
+                    v[0][k] = __uint_as_float(
+                        static_cast<uint32_t>(*reinterpret_cast<const uint16_t *>(p + k * pitch)) << 16);
+                v[1][k] = 0.0f;
+            }
+        }
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            const uint32_t byte = mx_scale_byte(finite_max<32>(v[c]));
+            const float inv = mx_inv_scale(byte);
+            uint4 *d = reinterpret_cast<uint4 *>(&tile[(2 * lane + c) * kPitch + 32 * warp]);
+            d[0] = make_uint4(e4m3_codes4(&v[c][0], inv), e4m3_codes4(&v[c][4], inv), e4m3_codes4(&v[c][8], inv),
+                              e4m3_codes4(&v[c][12], inv));
+            d[1] = make_uint4(e4m3_codes4(&v[c][16], inv), e4m3_codes4(&v[c][20], inv), e4m3_codes4(&v[c][24], inv),
+                              e4m3_codes4(&v[c][28], inv));
+            scales[2 * lane + c][warp] = static_cast<uint8_t>(byte);
         }
     }
+    __syncthreads();
+    const int rows = static_cast<int>(min(M - i0, static_cast<int64_t>(64)));
+    const int64_t k_left = K - kb;               // a multiple of 32
+    const int col = 16 * (threadIdx.x % 8);
 #pragma unroll
-    for (int c = 0; c < 2; ++c) {
-        if (c == 1 && !two) break;
-        uint32_t m = 0;
-#pragma unroll
-        for (int k = 0; k < 32; ++k) m = finite_max_bits(m, v[c][k]);
-        const uint32_t byte = mx_scale_byte(m);
-        const float inv = mx_inv_scale(byte);
-        uint32_t w[8];
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-            w[k] = e4m3_pair(v[c][4 * k], v[c][4 * k + 1], inv) | (e4m3_pair(v[c][4 * k + 2], v[c][4 * k + 3], inv) << 16);
-        uint4 *d = reinterpret_cast<uint4 *>(q + (i + c) * ldq + k0);
-        d[0] = make_uint4(w[0], w[1], w[2], w[3]);
-        d[1] = make_uint4(w[4], w[5], w[6], w[7]);
-        sf[(i + c) * (K / 32) + k0 / 32] = static_cast<uint8_t>(byte);
+    for (int r = threadIdx.x / 8; r < 64; r += 16)
+        if (r < rows && col < k_left)
+            *reinterpret_cast<uint4 *>(q + (i0 + r) * ldq + kb + col) =
+                *reinterpret_cast<const uint4 *>(&tile[r * kPitch + col]);
+    const int r = threadIdx.x;
+    if (r < rows) {
+        uint8_t *d = sf + (i0 + r) * (K / 32) + kb / 32;
+        if (k_left >= 128 && (reinterpret_cast<uintptr_t>(d) & 3) == 0) {
+            *reinterpret_cast<uint32_t *>(d) = *reinterpret_cast<const uint32_t *>(scales[r]);
+        } else {
+            for (int j = 0; j < 4 && 32 * j < k_left; ++j) d[j] = scales[r][j];
+        }
     }
 }
 

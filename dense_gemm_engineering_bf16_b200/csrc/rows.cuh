@@ -171,33 +171,42 @@ __device__ __forceinline__ float warp_sum(float v) {
 // is v / 2^e rounded to nearest even.  NaN and infinities get E4M3's NaN code
 // 0x7F and do not count for the scale (E4M3 has no infinity).
 
-// Bits of the largest finite |v|, a non-negative fp32 (whose bits order as the
-// values do).
-__device__ __forceinline__ uint32_t finite_max_bits(uint32_t m, float v) {
-    const uint32_t b = __float_as_uint(v) & 0x7FFFFFFFu;
-    return max(m, b < 0x7F800000u ? b : 0u);
+// Largest finite |v| of N values.  Infinities become NaN on the way, which the
+// maximum passes over and the conversion turns into the NaN code; testing for
+// them once per N values keeps the common path at one instruction a value.
+template <int N>
+__device__ __forceinline__ float finite_max(float *v) {
+    float m = 0.0f;
+#pragma unroll
+    for (int i = 0; i < N; ++i) m = fmaxf(m, fabsf(v[i]));
+    if (m == __uint_as_float(0x7F800000u)) {
+        m = 0.0f;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            if (fabsf(v[i]) == __uint_as_float(0x7F800000u)) v[i] = __uint_as_float(0x7FC00000u);
+            m = fmaxf(m, fabsf(v[i]));
+        }
+    }
+    return m;
 }
 
-// The E8M0 byte (e + 127) for a block whose largest magnitude has these bits:
-// with amax = 1.f * 2^(E-127) and 448 = 1.75 * 2^8, e = E - 127 - 8, one more
-// where 1.f > 1.75.  Blocks of zeros and of values below 448 * 2^-127 get byte 0.
-__device__ __forceinline__ uint32_t mx_scale_byte(uint32_t amax_bits) {
-    const int b = static_cast<int>(amax_bits >> 23) - 8 + ((amax_bits & 0x7FFFFFu) > 0x600000u ? 1 : 0);
+// The E8M0 byte (e + 127) for a block whose largest magnitude is amax = 1.f *
+// 2^(E-127): with 448 = 1.75 * 2^8, e = E - 127 - 8, one more where 1.f > 1.75.
+// Blocks of zeros and of values below 448 * 2^-127 get byte 0.
+__device__ __forceinline__ uint32_t mx_scale_byte(float amax) {
+    const uint32_t bits = __float_as_uint(amax);
+    const int b = static_cast<int>(bits >> 23) - 8 + ((bits & 0x7FFFFFu) > 0x600000u ? 1 : 0);
     return static_cast<uint32_t>(max(b, 0));
 }
 
 // 2^-e for an E8M0 byte e + 127 <= 247: always a normal fp32.
 __device__ __forceinline__ float mx_inv_scale(uint32_t byte) { return __uint_as_float((254u - byte) << 23); }
 
-// Two codes: the value times 2^-e (exact, or far below the smallest code),
-// rounded; |v| times 2^-e of a non-finite value is made NaN first, because
-// the saturating conversion would turn an infinity into 448.
+// Two codes: the values times 2^-e (exact, or far below the smallest code),
+// rounded; a NaN gives 0x7F.
 __device__ __forceinline__ uint32_t e4m3_pair(float lo, float hi, float inv) {
-    const float nan = __uint_as_float(0x7FC00000u);
-    lo = (__float_as_uint(lo) & 0x7FFFFFFFu) < 0x7F800000u ? lo * inv : nan;
-    hi = (__float_as_uint(hi) & 0x7FFFFFFFu) < 0x7F800000u ? hi * inv : nan;
     uint16_t d;
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(d) : "f"(hi), "f"(lo));
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(d) : "f"(hi * inv), "f"(lo * inv));
     return d;
 }
 
@@ -210,16 +219,14 @@ __device__ __forceinline__ uint32_t e4m3_codes4(const float *v, float inv) {
 // All 32 lanes call it, those past K with zeros.  q, sf: the row's codes
 // and scales.
 template <bool SPLIT>
-__device__ __forceinline__ void mx_store8(const float (&v)[8], int64_t e, int64_t K, uint8_t *q, uint8_t *sf) {
+__device__ __forceinline__ void mx_store8(float (&v)[8], int64_t e, int64_t K, uint8_t *q, uint8_t *sf) {
     if constexpr (SPLIT) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            uint32_t m = 0;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) m = finite_max_bits(m, v[4 * h + i]);
-            m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
-            m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
-            m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 4));
+            float m = finite_max<4>(&v[4 * h]);
+            m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+            m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
+            m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 4));
             const int64_t eh = e + 128 * h;
             if (eh < K) {
                 const uint32_t byte = mx_scale_byte(m);
@@ -228,11 +235,9 @@ __device__ __forceinline__ void mx_store8(const float (&v)[8], int64_t e, int64_
             }
         }
     } else {
-        uint32_t m = 0;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) m = finite_max_bits(m, v[i]);
-        m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
-        m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
+        float m = finite_max<8>(v);
+        m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+        m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
         if (e < K) {
             const uint32_t byte = mx_scale_byte(m);
             const float inv = mx_inv_scale(byte);
