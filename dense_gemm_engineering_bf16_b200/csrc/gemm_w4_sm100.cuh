@@ -8,22 +8,21 @@
 // warp-level tensor instruction mma.sync m16n8k16 with 16 weight rows as its
 // M and 8 activation rows as its N, and the scale is applied to the fp32 sum
 // of a group, not to each weight.  q - z is an integer in [-15, 15], exact in
-// bf16, so the products are exact and the only roundings are those of the
+// bf16 (over 64 too), so the products are exact and the only roundings are those of the
 // fp32 sums and of the output.
 //
-// Codes to bf16: the bits 0x4300 | q are the bf16 number 128 + q (its last
-// place is 1 there), so two codes sit ready after one AND-OR, and subtracting
-// 128 + z, exact as well, leaves q - z.  The AND-OR picks nibbles i and i + 4 of
-// a 32-bit word of eight codes, so an MMA's K order is 0 4 1 5 2 6 3 7 within
-// each eight; the activations are put in that order once, when they are
-// staged in shared memory.
+// Codes to bf16 (w4_codes): one AND and one fused multiply-add per pair.  The
+// AND picks nibbles i and i + 4 of a 32-bit word of eight codes, so an MMA's K
+// order is 0 4 1 5 2 6 3 7 within each eight; the activations are put in that
+// order when they are staged in shared memory.  The weights come out divided by
+// 64, which the result makes good, exactly.
 //
-// A block takes 128 or 256 weight rows and a share of K (cluster rank r of s),
-// its warps 16 * MT rows each.  Every warp streams its own rows through a ring of
+// A block takes 16 * MT weight rows per warp and a share of K (its rank in a
+// cluster).  Every warp streams its own rows through a ring of
 // shared-memory stages of 256 K with 16-byte cp.async copies (one 128-byte
-// line per row and stage) and synchronises with no other warp for it.  The
-// cluster's partial sums meet in distributed shared memory and are added in
-// rank order: no workspace, and the same result every time.
+// line per row and stage); the activations are shared by the block and staged
+// one stage ahead through registers.  The cluster's partial sums meet in
+// distributed shared memory and are added in a fixed order: no workspace, and the same result every time.
 #pragma once
 #include <cuda_bf16.h>
 
@@ -37,6 +36,7 @@ namespace b200 {
 constexpr int kW4K = 256;                    // K per stage
 constexpr int kW4Pitch = kW4K / 2 + 16;      // staged row of codes: 144 bytes, conflict-free 32-bit reads
 constexpr int kW4StageRow = kW4Pitch + 16 + 8;   // + its scales (16 bytes) and zeros (8 bytes)
+constexpr int kW4XPitch = 2 * kW4K + 64;     // staged activation row: conflict-free 16-byte reads
 
 // Asynchronous copy of 4, 8 or 16 bytes.  (The form with a byte count in a
 // register costs several instructions and a branch per copy; here the ends of
@@ -52,21 +52,36 @@ __device__ __forceinline__ void w4_copy(uint32_t dst, const void *src) {
 // d = A . B + c; with c = 0 given as constants no register has to be cleared.
 __device__ __forceinline__ void w4_mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1, float c0,
                                        float c1, float c2, float c3) {
-    asm volatile(
+    asm(
         "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 "
         "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %11, %12, %13};"
         : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
 }
 
-// Codes i and i + 4 of a word of eight as bf16 q - z, with `minus` the pair
-// -(128 + z).  `mask` and `one28` come in registers of their own: as literals
-// the AND and the OR would be two instructions, since one takes one literal.
+// Codes i and i + 4 of a word of eight (I = 0: i = 0, I = 1: i = 1; codes 2, 3,
+// 6 and 7 from the word shifted right by 8) as bf16 (q - z) / 64, with `minus`
+// the pair -z / 64.  The AND leaves q 16^I in each half, as a bf16 the
+// subnormal q 16^I 2^-133 (bf16 patterns below 0x0100 grow linearly through the
+// subnormals and the first binade), and one fused multiply-add by 2^127 or
+// 2^123 makes q / 64 - z / 64 of it, exactly.  Bit operations run at half the
+// rate of multiply-adds here and bound this kernel, so their number counts:
+// five per word (without the subnormals it takes seven).
 template <int I>
-__device__ __forceinline__ uint32_t w4_codes(uint32_t word, uint32_t minus, uint32_t mask, uint32_t one28) {
-    uint32_t t, d;
-    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(t) : "r"(word >> (4 * I)), "r"(mask), "r"(one28));   // (a & b) | c
-    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(t), "r"(0x3F803F80u), "r"(minus));
+__device__ __forceinline__ uint32_t w4_codes(uint32_t word, uint32_t minus) {
+    uint32_t d;
+    asm("fma.rn.bf16x2 %0, %1, %2, %3;"
+        : "=r"(d)
+        : "r"(word & (I ? 0x00F000F0u : 0x000F000Fu)), "r"(I ? 0x7D007D00u : 0x7F007F00u), "r"(minus));
+    return d;
+}
+
+// -z / 64 of the byte z = zeros[i], as a bf16 pair.
+__device__ __forceinline__ uint32_t w4_minus(uint32_t zeros, int i) {
+    uint32_t d;
+    asm("fma.rn.bf16x2 %0, %1, %2, %3;"       // z as a subnormal times -2^127, minus 0
+        : "=r"(d)
+        : "r"(__byte_perm(zeros, 0u, 0x4040u | 0x101u * i)), "r"(0xFF00FF00u), "r"(0x80008000u));
     return d;
 }
 
@@ -80,9 +95,8 @@ struct W4Args {
     int64_t groups;          // ceil(K / G)
     int group_shift;         // log2 G
     int out;                 // kF32 or kBF16
-    int token_blocks;        // ceil(M / (8 * NT))
-    int x_shift;             // log2 of the 16-byte vectors per staged activation row
-    int x_pitch;             // bytes per staged activation row
+    uint32_t stages;         // ceil(K / kW4K)
+    int split_shift;         // log2 of the cluster's size
 };
 
 // NT: activation rows in eights; MT: weight rows per warp in sixteens; WARPS
@@ -93,14 +107,31 @@ struct W4Cfg {
     static constexpr int THREADS = 32 * WARPS;
     static constexpr int WROWS = 16 * MT;                  // weight rows per warp
     static constexpr int ROWS = WROWS * WARPS;             // and per block
-    static constexpr int STAGE_BYTES = ROWS * kW4StageRow;
-    static constexpr int RING_BYTES = S * STAGE_BYTES;
-    static constexpr int RED_PITCH = ROWS + 4;             // partial sums [token][row], over the ring
-    static constexpr int X_BYTES = 32 * 1024;              // staged activations, one stage of K at least
-    static constexpr int X_STAGE = 8 * NT * 2 * kW4K;
-    static constexpr int MAX_SMEM = RING_BYTES + (X_BYTES > X_STAGE ? X_BYTES : X_STAGE) + 8 * NT * 64;
-    static_assert(8 * NT * RED_PITCH * 4 <= RING_BYTES, "partial sums fit into the ring");
+    static constexpr int SLOT_BYTES = WROWS * kW4StageRow;
+    static constexpr int RING_BYTES = S * SLOT_BYTES;      // per warp
+    static constexpr int X_BYTES = 8 * NT * kW4XPitch;     // activations of one stage, staged twice
+    static constexpr int X_ROWS = (8 * NT + WARPS - 1) / WARPS;    // activation rows that a warp stages
+    static constexpr int SMEM_BYTES = WARPS * RING_BYTES + 2 * X_BYTES;
+    static constexpr int RED_PITCH = ROWS + 4;             // partial sums [token][row], in the rings' place
+    static constexpr int PER_SM = SMEM_BYTES <= 112 * 1024 ? 2 : 1;    // blocks that an SM holds
+    static_assert(8 * NT * RED_PITCH * 4 <= SMEM_BYTES, "partial sums fit");
 };
+
+// Sum over the cluster's SPLIT blocks of the float at one shared address.
+template <int SPLIT>
+__device__ __forceinline__ float w4_gather(uint32_t at) {
+    float f[SPLIT], v = 0.0f;
+#pragma unroll
+    for (uint32_t p = 0; p < SPLIT; ++p)
+        asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(f[p]) : "r"(map_to_cta(at, p)));
+#pragma unroll
+    for (int p = 0; p < SPLIT; ++p) v += f[p];
+    return v;
+}
+
+// The two bf16 of a pair as fp32.
+__device__ __forceinline__ float w4_low(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float w4_high(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 
 // U: 32-K steps per scale (G = 32 U; 8 also for larger groups).
 template <class Cfg, int U>
@@ -109,18 +140,22 @@ __global__ void __launch_bounds__(Cfg::THREADS) gemm_w4_kernel(W4Args a) {
     extern __shared__ __align__(128) uint8_t smem[];
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
     const int g = lane / 4, t = lane % 4;
-    const uint32_t split = cluster_num_ctas(), rank = cluster_cta_rank();
-    const int64_t unit = blockIdx.x / split;
-    const int64_t n0 = unit / a.token_blocks * Cfg::ROWS;
-    const int64_t m0 = unit % a.token_blocks * (8 * NT);
+    // grid: x = weight tile and K share (the cluster's ranks), y = activation rows
+    const uint32_t split = 1u << a.split_shift, rank = blockIdx.x & (split - 1);
+    const int64_t n0 = static_cast<int64_t>(blockIdx.x >> a.split_shift) * Cfg::ROWS;
+    const int64_t m0 = static_cast<int64_t>(blockIdx.y) * (8 * NT);
     const int tokens = static_cast<int>(min(a.M - m0, static_cast<int64_t>(8 * NT)));
-    const uint32_t stages = static_cast<uint32_t>((a.K + kW4K - 1) / kW4K);
-    const uint32_t s_begin = static_cast<uint32_t>(static_cast<uint64_t>(rank) * stages / split);
-    const uint32_t s_end = static_cast<uint32_t>(static_cast<uint64_t>(rank + 1) * stages / split);
+    // at most 2^23 stages of K, split by at most 8
+    const uint32_t s_begin = rank * a.stages >> a.split_shift, s_end = (rank + 1) * a.stages >> a.split_shift;
 
-    // this warp's part of a ring slot: codes, then scales, then zeros
-    uint8_t *const ring = smem + warp * WROWS * kW4StageRow;
-    uint8_t *const x_smem = smem + Cfg::RING_BYTES;
+    // this warp's ring; a slot holds codes, then scales, then zeros
+    uint8_t *const ring = smem + warp * Cfg::RING_BYTES;
+    uint8_t *const x_smem = smem + Cfg::WARPS * Cfg::RING_BYTES;
+    if (!a.zeros) {     // zeros of 8 in every slot, once
+        for (int i = lane; i < S * WROWS; i += 32)
+            *reinterpret_cast<uint2 *>(ring + (i / WROWS) * Cfg::SLOT_BYTES + WROWS * (kW4Pitch + 16) + 8 * (i % WROWS)) =
+                make_uint2(0x08080808u, 0x08080808u);
+    }
 
     // What this lane copies of each stage: 16 bytes (32 codes) of every fourth
     // row, and one row's scales and zeros.  Rows past N repeat the last row
@@ -174,76 +209,98 @@ __global__ void __launch_bounds__(Cfg::THREADS) gemm_w4_kernel(W4Args a) {
                 }
             }
         }
-        fill = fill == (S - 1) * Cfg::STAGE_BYTES ? 0 : fill + Cfg::STAGE_BYTES;
+        fill = fill == (S - 1) * Cfg::SLOT_BYTES ? 0 : fill + Cfg::SLOT_BYTES;
         asm volatile("cp.async.commit_group;" ::: "memory");   // one group per stage, empty ones too
     };
 
 #pragma unroll
     for (int i = 0; i < S - 1; ++i) load_stage(s_begin + i);
 
-    // activation rows of the MMA's columns; columns past the last row repeat it and are not stored
+    // Activations: warp w stages rows w, w + WARPS, ... of each stage, 32 lanes
+    // to a row, in the MMA's K order and zero past K.  Two buffers: the next
+    // stage's are loaded while this one is worked on.
+    const uint16_t *x_src[Cfg::X_ROWS];
+#pragma unroll
+    for (int i = 0; i < Cfg::X_ROWS; ++i)
+        x_src[i] = a.a + (m0 + min(warp + i * Cfg::WARPS, tokens - 1)) * a.lda + static_cast<int64_t>(s_begin) * kW4K +
+                   8 * lane;
+    uint4 x_next[Cfg::X_ROWS];
+    auto load_x = [&](uint32_t st) {
+        const bool in = st < s_end && st * (kW4K / 8) + lane < 4 * k_steps;
+#pragma unroll
+        for (int i = 0; i < Cfg::X_ROWS; ++i) {
+            x_next[i] = make_uint4(0, 0, 0, 0);
+            if (in && warp + i * Cfg::WARPS < tokens) x_next[i] = *reinterpret_cast<const uint4 *>(x_src[i]);
+            x_src[i] += kW4K;
+        }
+    };
+    auto store_x = [&](uint8_t *buffer) {
+#pragma unroll
+        for (int i = 0; i < Cfg::X_ROWS; ++i) {
+            const uint4 x = x_next[i];
+            if (warp + i * Cfg::WARPS < tokens)
+                *reinterpret_cast<uint4 *>(buffer + (warp + i * Cfg::WARPS) * kW4XPitch + 16 * lane) =
+                    make_uint4(__byte_perm(x.x, x.z, 0x5410), __byte_perm(x.x, x.z, 0x7632),
+                               __byte_perm(x.y, x.w, 0x5410), __byte_perm(x.y, x.w, 0x7632));
+        }
+    };
+    // rows of the MMA's columns; columns past the last row repeat it and are not stored
     uint32_t x_row[NT];
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) x_row[nt] = min(8 * nt + g, tokens - 1) * a.x_pitch + 16 * t;
+    for (int nt = 0; nt < NT; ++nt) x_row[nt] = min(8 * nt + g, tokens - 1) * kW4XPitch + 16 * t;
 
-    uint32_t mask, one28;                 // kept in registers
-    asm volatile("mov.b32 %0, 0x000F000F;" : "=r"(mask));
-    asm volatile("mov.b32 %0, 0x43004300;" : "=r"(one28));
     float acc[MT][NT][4] = {};
-    const uint32_t x_stages = 1u << (a.x_shift - 5);    // stages staged at a time
-    uint32_t x_at = x_stages;             // next of them
     uint32_t read = 0;                    // ring slot (byte offset) to read
+    uint32_t x_read = 0;                  // and activation buffer
+    load_x(s_begin);
     for (uint32_t st = s_begin; st < s_end; ++st) {
-        if (x_at == x_stages) {
-            // activations of the next stages, in the MMA's K order, zero past
-            // K; several loads in flight per thread
-            if (st != s_begin) __syncthreads();
-            const int64_t k_end = min(a.K, static_cast<int64_t>(s_end) * kW4K);
-            const int total = tokens << a.x_shift;
-            for (int i0 = tid; i0 < total; i0 += 8 * THREADS) {
-                uint4 x[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const int v = i0 + i * THREADS;
-                    const int64_t k = static_cast<int64_t>(st) * kW4K + 8 * (v & ((1 << a.x_shift) - 1));
-                    x[i] = make_uint4(0, 0, 0, 0);
-                    if (v < total && k < k_end)
-                        x[i] = *reinterpret_cast<const uint4 *>(a.a + (m0 + (v >> a.x_shift)) * a.lda + k);
-                }
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const int v = i0 + i * THREADS;
-                    if (v < total)
-                        *reinterpret_cast<uint4 *>(x_smem + (v >> a.x_shift) * a.x_pitch +
-                                                   16 * (v & ((1 << a.x_shift) - 1))) =
-                            make_uint4(__byte_perm(x[i].x, x[i].z, 0x5410), __byte_perm(x[i].x, x[i].z, 0x7632),
-                                       __byte_perm(x[i].y, x[i].w, 0x5410), __byte_perm(x[i].y, x[i].w, 0x7632));
-                }
-            }
-            __syncthreads();
-            x_at = 0;
-        }
+        // this buffer was last read two stages ago, before the barrier of the previous one
+        store_x(x_smem + x_read);
         asm volatile("cp.async.wait_group %0;" ::"n"(S - 2) : "memory");
-        __syncwarp();
-        load_stage(st + S - 1);     // into the slot read in the previous iteration
+        __syncthreads();
+        load_x(st + 1);
+        load_stage(st + S - 1);           // into the slot read in the previous iteration
         const uint8_t *src = ring + read;
-        read = read == (S - 1) * Cfg::STAGE_BYTES ? 0 : read + Cfg::STAGE_BYTES;
+        const uint8_t *xs = x_smem + x_read;
+        read = read == (S - 1) * Cfg::SLOT_BYTES ? 0 : read + Cfg::SLOT_BYTES;
+        x_read ^= Cfg::X_BYTES;
+        // the stage's scales and zeros of this lane's rows: 8 / U groups from g_low on
         const uint32_t g_low = U == 8 ? st >> (a.group_shift - 8) : U == 4 ? 2 * st : 0u;
-        const uint8_t *sc = src + WROWS * kW4Pitch + 2 * (g_low & 1);
-        const uint8_t *zr = src + WROWS * (kW4Pitch + 16) + (g_low & 3);
-        const uint8_t *xs = x_smem + x_at * (2 * kW4K);
-        ++x_at;
+        constexpr int GROUPS = 8 / U;
+        float scale[MT][2][GROUPS];
+        uint32_t zero[MT][2][(GROUPS + 3) / 4];
 #pragma unroll
-        for (int grp = 0; grp < 8 / U; ++grp) {
-            float part[MT][NT][4];
-            uint32_t minus[MT][2];      // -(128 + z), twice
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int row = 16 * mt + 8 * h + g;
+                const uint8_t *sc = src + WROWS * kW4Pitch + 16 * row;
+                if constexpr (U == 8) {
+                    scale[mt][h][0] = w4_low(*reinterpret_cast<const uint16_t *>(sc + 2 * (g_low & 1)));
+                } else {
+#pragma unroll
+                    for (int i = 0; i < GROUPS / 2; ++i) {
+                        const uint32_t w = reinterpret_cast<const uint32_t *>(sc)[i];
+                        scale[mt][h][2 * i] = w4_low(w);
+                        scale[mt][h][2 * i + 1] = w4_high(w);
+                    }
+                }
+                const uint8_t *zr = src + WROWS * (kW4Pitch + 16) + 8 * row;
+#pragma unroll
+                for (int i = 0; i < (GROUPS + 3) / 4; ++i)
+                    zero[mt][h][i] = (reinterpret_cast<const uint32_t *>(zr)[i] & 0x0F0F0F0Fu) >> (8 * (g_low & 3));
+            }
+#pragma unroll
+        for (int grp = 0; grp < GROUPS; ++grp) {
+            // The two MMAs of a step add to one sum only where other sums stand
+            // between them: a dependent MMA waits some 20 cycles.
+            constexpr int CHAINS = NT <= 2 ? 2 : 1;
+            float part[CHAINS][MT][NT][4];
+            uint32_t minus[MT][2];
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const uint32_t z = a.zeros ? zr[8 * (16 * mt + 8 * h + g) + grp] & 15u : 8u;
-                    minus[mt][h] = (0xC300u | z) * 0x10001u;
-                }
+                for (int h = 0; h < 2; ++h) minus[mt][h] = w4_minus(zero[mt][h][grp / 4], grp % 4);
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 const int j = grp * U + u;
@@ -262,43 +319,44 @@ __global__ void __launch_bounds__(Cfg::THREADS) gemm_w4_kernel(W4Args a) {
                     const uint32_t lo = *reinterpret_cast<const uint32_t *>(w);
                     const uint32_t hi = *reinterpret_cast<const uint32_t *>(w + 8 * kW4Pitch);
                     uint32_t a0[4], a1[4];
-                    a0[0] = w4_codes<0>(lo, minus[mt][0], mask, one28);
-                    a0[1] = w4_codes<0>(hi, minus[mt][1], mask, one28);
-                    a0[2] = w4_codes<1>(lo, minus[mt][0], mask, one28);
-                    a0[3] = w4_codes<1>(hi, minus[mt][1], mask, one28);
-                    a1[0] = w4_codes<2>(lo, minus[mt][0], mask, one28);
-                    a1[1] = w4_codes<2>(hi, minus[mt][1], mask, one28);
-                    a1[2] = w4_codes<3>(lo, minus[mt][0], mask, one28);
-                    a1[3] = w4_codes<3>(hi, minus[mt][1], mask, one28);
+                    a0[0] = w4_codes<0>(lo, minus[mt][0]);
+                    a0[1] = w4_codes<0>(hi, minus[mt][1]);
+                    a0[2] = w4_codes<1>(lo, minus[mt][0]);
+                    a0[3] = w4_codes<1>(hi, minus[mt][1]);
+                    a1[0] = w4_codes<0>(lo >> 8, minus[mt][0]);
+                    a1[1] = w4_codes<0>(hi >> 8, minus[mt][1]);
+                    a1[2] = w4_codes<1>(lo >> 8, minus[mt][0]);
+                    a1[3] = w4_codes<1>(hi >> 8, minus[mt][1]);
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
-                        float (&p)[4] = part[mt][nt];
+                        float (&p)[4] = part[0][mt][nt];
                         if (u == 0) w4_mma(p, a0, x[nt][0], x[nt][1], 0.0f, 0.0f, 0.0f, 0.0f);
                         else w4_mma(p, a0, x[nt][0], x[nt][1], p[0], p[1], p[2], p[3]);
-                        w4_mma(p, a1, x[nt][2], x[nt][3], p[0], p[1], p[2], p[3]);
+                    }
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        float (&p)[4] = part[CHAINS - 1][mt][nt];
+                        if (u == 0 && CHAINS == 2) w4_mma(p, a1, x[nt][2], x[nt][3], 0.0f, 0.0f, 0.0f, 0.0f);
+                        else w4_mma(p, a1, x[nt][2], x[nt][3], p[0], p[1], p[2], p[3]);
                     }
                 }
             }
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt) {
-                float s[2];
-#pragma unroll
-                for (int h = 0; h < 2; ++h)
-                    s[h] = __uint_as_float(static_cast<uint32_t>(*reinterpret_cast<const uint16_t *>(
-                                               sc + 16 * (16 * mt + 8 * h + g) + 2 * grp))
-                                           << 16);
+            for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) acc[mt][nt][r] += s[r / 2] * part[mt][nt][r];
-            }
+                    for (int r = 0; r < 4; ++r) {
+                        float p = part[0][mt][nt][r];
+                        if (CHAINS == 2) p += part[1][mt][nt][r];
+                        acc[mt][nt][r] += scale[mt][r / 2][grp] * p;
+                    }
         }
-        __syncwarp();               // the slot may be overwritten from the next iteration on
     }
     asm volatile("cp.async.wait_group 0;" ::: "memory");
     __syncthreads();
 
-    // partial sums [token][row] over the ring
+    // partial sums [token][row] over the rings
     float *red = reinterpret_cast<float *>(smem);
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt)
@@ -310,17 +368,21 @@ __global__ void __launch_bounds__(Cfg::THREADS) gemm_w4_kernel(W4Args a) {
                     acc[mt][nt][r];
     if (split > 1) cluster_sync_all();
     else __syncthreads();
-    // rank r writes its share of the rows, summed in rank order
-    const int rows = Cfg::ROWS / static_cast<int>(split), row0 = rows * static_cast<int>(rank);
-    for (int i = tid; i < tokens * rows; i += THREADS) {
-        const int token = i / rows, row = row0 + i % rows;
-        const uint32_t at = smem_addr(red + token * Cfg::RED_PITCH + row);
-        float v = 0.0f;
-        for (uint32_t p = 0; p < split; ++p) {
-            float f;
-            asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(f) : "r"(map_to_cta(at, p)) : "memory");
-            v += f;
-        }
+    // Rank r writes its share of the rows, summed in rank order; the shares of
+    // an output are read together (one after the other their latencies through
+    // the cluster would add up).
+    const int rows = Cfg::ROWS >> a.split_shift, row0 = rows * static_cast<int>(rank);     // a power of two
+    const int row_shift = 31 - __clz(rows);
+    const uint32_t red_addr = smem_addr(red);
+    for (int i = tid; i < tokens << row_shift; i += THREADS) {
+        const int token = i >> row_shift, row = row0 + (i & (rows - 1));
+        const uint32_t at = red_addr + 4 * (token * Cfg::RED_PITCH + row);
+        float v;
+        if (a.split_shift == 3) v = w4_gather<8>(at);
+        else if (a.split_shift == 2) v = w4_gather<4>(at);
+        else if (a.split_shift == 1) v = w4_gather<2>(at);
+        else v = red[token * Cfg::RED_PITCH + row];
+        v *= 64.0f;         // the weights went in over 64
         if (n0 + row < a.N) {
             const int64_t o = (m0 + token) * a.ldc + n0 + row;
             if (a.out == kF32) static_cast<float *>(a.c)[o] = v;

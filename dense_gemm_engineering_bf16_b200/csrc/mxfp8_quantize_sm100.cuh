@@ -6,25 +6,26 @@
 
 namespace b200 {
 
-// X stored K-major (M rows of K): VPT eights per thread.  A row (or a part of
-// it: blockIdx.y) takes blockDim.x threads; short rows share a block
+// X stored K-major (M rows of K): VPT eights per thread.  A row takes
+// blockDim.x threads in each of `parts` blocks; short rows share a block
 // (blockDim.y).
 template <int XT, int VPT>
 __global__ void __launch_bounds__(256) mx_quantize_kernel(const void *x, uint8_t *q, uint8_t *sf, int64_t M, int64_t K,
-                                                          int64_t ldx, int64_t ldq) {
+                                                          int64_t ldx, int64_t ldq, unsigned parts) {
     constexpr bool SPLIT = XT == kF32;
-    const int64_t row = static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y;
+    const unsigned part = blockIdx.x % parts;
+    const int64_t row = static_cast<int64_t>(blockIdx.x / parts) * blockDim.y + threadIdx.y;
     if (row >= M) return;   // whole warps
     const uint8_t *p = static_cast<const uint8_t *>(x) + row * ldx * elem_bytes<XT>;
     Raw8<XT> r[VPT];
 #pragma unroll
     for (int i = 0; i < VPT; ++i)
-        r[i] = load_raw8<XT, SPLIT>(p, first8<SPLIT>(threadIdx.x, blockIdx.y * VPT + i, blockDim.x), K);
+        r[i] = load_raw8<XT, SPLIT>(p, first8<SPLIT>(threadIdx.x, part * VPT + i, blockDim.x), K);
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
         float v[8];
         widen8<XT>(r[i], v);
-        mx_store8<SPLIT>(v, first8<SPLIT>(threadIdx.x, blockIdx.y * VPT + i, blockDim.x), K, q + row * ldq,
+        mx_store8<SPLIT>(v, first8<SPLIT>(threadIdx.x, part * VPT + i, blockDim.x), K, q + row * ldq,
                          sf + row * (K / 32));
     }
 }
