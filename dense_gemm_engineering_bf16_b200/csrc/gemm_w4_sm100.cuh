@@ -135,7 +135,7 @@ __device__ __forceinline__ float w4_high(uint32_t w) { return __uint_as_float(w 
 
 // U: 32-K steps per scale (G = 32 U; 8 also for larger groups).
 template <class Cfg, int U>
-__global__ void __launch_bounds__(Cfg::THREADS) gemm_w4_kernel(W4Args a) {
+__global__ void __launch_bounds__(Cfg::THREADS, Cfg::PER_SM) gemm_w4_kernel(W4Args a) {
     constexpr int NT = Cfg::NT, MT = Cfg::MT, S = Cfg::S, THREADS = Cfg::THREADS, WROWS = Cfg::WROWS;
     extern __shared__ __align__(128) uint8_t smem[];
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
