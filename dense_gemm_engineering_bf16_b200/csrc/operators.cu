@@ -67,21 +67,25 @@ int round_up(int64_t n, int m) { return static_cast<int>((n + m - 1) / m * m); }
 
 // ---------------------------------------------------------------- RMS norm --
 
-// Threads and vectors of eight per thread for a row of K elements.  Up to
-// 1024 elements a warp holds the row, and eight rows share a block.  Longer
-// rows take a block each: with fewer rows than would fill the SMs, one vector
-// per thread (the shortest chain of loads); else four, which leaves room for
-// several blocks per SM.  VPT 0: the row does not fit into registers.
+// Threads per row and eights per thread.  Up to 1024 elements a warp holds the
+// row, and eight rows share a block.  Longer rows take a block each: with
+// fewer rows than would fill the SMs, one eight per thread (the shortest chain
+// of loads); else four of bf16 or, with an fp32 operand, two, about the same
+// bytes in flight (8192 x 8192 bf16: 75.8 us with four, 79.6 with two; 4000 x
+// 3000 with an fp32 stream: 26.3 and 24.9).  VPT 0: the row does not fit into
+// registers.
 struct RowShape {
     int vpt;
     dim3 block;
 };
 
-RowShape row_shape(int64_t K, bool few_rows) {
+RowShape row_shape(int64_t K, bool few_rows, bool fp32) {
     const int64_t vecs = (K + 7) / 8;
+    const auto block = [&](int vpt) { return dim3(static_cast<unsigned>(round_up((vecs + vpt - 1) / vpt, 32))); };
     if (vecs <= 128) return {vecs <= 32 ? 1 : vecs <= 64 ? 2 : 4, dim3(32, 8)};
-    if (vecs <= 1024 && few_rows) return {1, dim3(static_cast<unsigned>(round_up(vecs, 32)))};
-    if (vecs <= 4 * 512) return {4, dim3(static_cast<unsigned>(round_up((vecs + 3) / 4, 32)))};
+    if (vecs <= 1024 && few_rows) return {1, block(1)};
+    if (vecs <= 1024 && fp32) return {2, block(2)};
+    if (vecs <= 2048) return {4, block(4)};
     return {0, dim3(1024)};
 }
 
@@ -101,7 +105,7 @@ gemm_status_t launch_norm(int dev, const b200::RmsnormArgs &a, dim3 block, cudaS
 
 template <int XT, int HT>
 gemm_status_t dispatch_norm(int dev, int sm_count, const b200::RmsnormArgs &a, cudaStream_t stream) {
-    const RowShape r = row_shape(a.K, a.M <= 2 * sm_count);
+    const RowShape r = row_shape(a.K, a.M <= 2 * sm_count, XT == kF32 || HT == kF32);
     switch (r.vpt) {
         case 1: return launch_norm<XT, HT, 1>(dev, a, r.block, stream);
         case 2: return launch_norm<XT, HT, 2>(dev, a, r.block, stream);
@@ -143,7 +147,9 @@ gemm_status_t launch_back(int dev, int sm_count, b200::RmsnormBackArgs a, dim3 b
                           cudaStream_t stream) {
     // rows in shared memory: as many (2 to 4) as leave room for two blocks per
     // SM, or else for one
-    const int row_bytes = static_cast<int>(VPT * b200::back_pieces<YT, HT, DT> * 16 * block.x * block.y);
+    const int piece_bytes = static_cast<int>(VPT * 16 * block.x * block.y);
+    a.stage_dr = VPT < 4 || 2 * b200::back_pieces<YT, HT, DT>(true) * piece_bytes <= kSmemPerSm;
+    const int row_bytes = b200::back_pieces<YT, HT, DT>(a.stage_dr) * piece_bytes;
     const int64_t per_sm = block.x * block.y <= 256 && 4 * row_bytes <= kSmemPerSm ? 2 : 1;
     a.ring = VPT == 0 ? 0 : static_cast<int>(std::min<int64_t>(4, kSmemPerSm / (per_sm * row_bytes)));
     const int64_t rows = (a.M + block.y - 1) / block.y;
@@ -178,7 +184,7 @@ gemm_status_t dispatch_back(int dev, int sm_count, const b200::RmsnormBackArgs &
     if (vecs <= 64) return launch_back<YT, HT, DT, 2>(dev, sm_count, a, dim3(32, 8), dw, ws, stream);
     if (vecs <= 128) return launch_back<YT, HT, DT, 4>(dev, sm_count, a, dim3(32, 8), dw, ws, stream);
     if (vecs <= 1024) return launch_back<YT, HT, DT, 2>(dev, sm_count, a, block(2), dw, ws, stream);
-    if (vecs <= 2048 && 2 * 16 * b200::back_pieces<YT, HT, DT> * 4 * block(4).x <= kSmemPerSm)
+    if (vecs <= 2048 && 2 * 16 * b200::back_pieces<YT, HT, DT>(false) * 4 * block(4).x <= kSmemPerSm)
         return launch_back<YT, HT, DT, 4>(dev, sm_count, a, block(4), dw, ws, stream);
     return launch_back<YT, HT, DT, 0>(dev, sm_count, a, dim3(1024), dw, ws, stream);
 }
@@ -356,7 +362,7 @@ gemm_status_t gemm_rmsnorm_backward(const void *dY, const void *H, const float *
         return GEMM_ERR_ALIAS;
     if ((s = b200::host::device(dev, sm_count, stream)) != GEMM_OK) return s;
     const b200::RmsnormBackArgs a{dY, H, weight, rstd, dR, dH, nullptr, M, K, lddy, ldh, lddr, lddh, 0,
-                                  1.0f / static_cast<float>(K)};
+                                  1.0f / static_cast<float>(K), true};
     float *ws = static_cast<float *>(workspace);
     const int key = (dy_type == GEMM_OUT_F32 ? 4 : 0) | (h_type == GEMM_OUT_F32 ? 2 : 0) | (dh_type == GEMM_OUT_F32 ? 1 : 0);
     switch (key) {

@@ -167,6 +167,7 @@ struct RmsnormBackArgs {
     int64_t M, K, lddy, ldh, lddr, lddh;
     int ring;         // rows in shared memory at a time: 2, 3 or 4
     float inv_k;      // 1 / K
+    bool stage_dr;    // dr goes through shared memory too
 };
 
 // This thread's eight elements at e into shared memory, asynchronously, the
@@ -219,9 +220,12 @@ __device__ __forceinline__ void staged8(const uint8_t *slot, unsigned pitch, flo
     widen8<T>(r, f);
 }
 
-// 16-byte pieces per vector of dy, h and dr
+// 16-byte pieces per eight of what is staged: dy, h, and dr where two rows with
+// it fit into shared memory (else dr is read when it is needed).
 template <int YT, int HT, int DT>
-constexpr int back_pieces = (YT == kF32 ? 2 : 1) + (HT == kF32 ? 2 : 1) + (DT == kF32 ? 2 : 1);
+constexpr int back_pieces(bool stage_dr) {
+    return (YT == kF32 ? 2 : 1) + (HT == kF32 ? 2 : 1) + (!stage_dr ? 0 : DT == kF32 ? 2 : 1);
+}
 
 // Persistent blocks: block b takes rows b, b + gridDim.x, ... (times
 // blockDim.y) and keeps its share of dw in registers, written out once at
@@ -235,9 +239,11 @@ __global__ void __launch_bounds__(512) rmsnorm_back_kernel(RmsnormBackArgs a) {
     constexpr bool SPLIT = YT == kF32 || HT == kF32 || DT == kF32;
     __shared__ float red[2][1][32];
     extern __shared__ __align__(16) uint8_t dyn[];
-    constexpr int kY = YT == kF32 ? 2 : 1, kH = HT == kF32 ? 2 : 1, kPieces = back_pieces<YT, HT, DT>;
+    constexpr int kY = YT == kF32 ? 2 : 1, kH = HT == kF32 ? 2 : 1, kD = DT == kF32 ? 2 : 1;
+    const bool stage_dr = VPT < 4 || a.stage_dr;
+    const int pieces = kY + kH + (stage_dr ? kD : 0);
     const unsigned pitch = 16 * blockDim.x * blockDim.y;       // between a thread's pieces
-    const unsigned row_pitch = VPT * kPieces * pitch, ring_end = a.ring * row_pitch;
+    const unsigned row_pitch = VPT * pieces * pitch, ring_end = a.ring * row_pitch;
     uint8_t *const mine = dyn + 16 * (threadIdx.y * blockDim.x + threadIdx.x);
     const int64_t stride = static_cast<int64_t>(gridDim.x) * blockDim.y;
     const int64_t first = static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y;
@@ -257,10 +263,10 @@ __global__ void __launch_bounds__(512) rmsnorm_back_kernel(RmsnormBackArgs a) {
             for (int i = 0; i < VPT; ++i) {
                 const int e = e0 + 8 * i * static_cast<int>(blockDim.x);
                 if (e >= K) break;
-                uint8_t *p = mine + fill + i * kPieces * pitch;
+                uint8_t *p = mine + fill + i * pieces * pitch;
                 stage8<YT, SPLIT>(p, pitch, dy, e, K);
                 stage8<HT, SPLIT>(p + kY * pitch, pitch, h, e, K);
-                if (a.dr) stage8<DT, SPLIT>(p + (kY + kH) * pitch, pitch, dr, e, K);
+                if (stage_dr && a.dr) stage8<DT, SPLIT>(p + (kY + kH) * pitch, pitch, dr, e, K);
             }
         }
         ahead += stride;
@@ -275,19 +281,14 @@ __global__ void __launch_bounds__(512) rmsnorm_back_kernel(RmsnormBackArgs a) {
 #pragma unroll
         for (int i = 0; i < VPT; ++i)
             if (e0 + 8 * i * static_cast<int>(blockDim.x) + at8<SPLIT>(7) >= K)
-                for (int q = 0; q < kPieces; ++q)
-                    *reinterpret_cast<uint4 *>(mine + r * row_pitch + (i * kPieces + q) * pitch) =
+                for (int q = 0; q < pieces; ++q)
+                    *reinterpret_cast<uint4 *>(mine + r * row_pitch + (i * pieces + q) * pitch) =
                         make_uint4(0, 0, 0, 0);
     for (int i = 1; i < a.ring; ++i) load_row();
 
     float dw[VPT][8] = {}, w[VPT][8];
-    if constexpr (VPT < 4) {
 #pragma unroll
-        for (int i = 0; i < VPT; ++i) {
-            const int e = e0 + 8 * i * static_cast<int>(blockDim.x);
-            load8<kF32, SPLIT>(a.w, e, K, w[i]);
-        }
-    }
+    for (int i = 0; i < VPT; ++i) load8<kF32, SPLIT>(a.w, e0 + 8 * i * static_cast<int>(blockDim.x), K, w[i]);
     float rstd = first < a.M ? a.rstd[first] : 0.0f;
     uint8_t *dh = static_cast<uint8_t *>(a.dh) + first * a.lddh * elem_bytes<DT>;
     int phase = 0;
@@ -302,11 +303,10 @@ __global__ void __launch_bounds__(512) rmsnorm_back_kernel(RmsnormBackArgs a) {
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
             const int e = e0 + 8 * i * static_cast<int>(blockDim.x);
-            const uint8_t *p = mine + slot + i * kPieces * pitch;
+            const uint8_t *p = mine + slot + i * pieces * pitch;
             float y[8], v[8];
             staged8<YT>(p, pitch, y);
             staged8<HT>(p + kY * pitch, pitch, v);
-            if constexpr (VPT == 4) load8<kF32, SPLIT>(a.w, e, K, w[i]);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 const float p = y[j] * v[j];        // dy h: times rstd for dw, times w for the sum
@@ -321,16 +321,18 @@ __global__ void __launch_bounds__(512) rmsnorm_back_kernel(RmsnormBackArgs a) {
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
             const int e = e0 + 8 * i * static_cast<int>(blockDim.x);
-            const uint8_t *p = mine + slot + i * kPieces * pitch;
+            const uint8_t *p = mine + slot + i * pieces * pitch;
             float y[8], v[8], d[8];
             staged8<YT>(p, pitch, y);
             staged8<HT>(p + kY * pitch, pitch, v);
-            if constexpr (VPT == 4) load8<kF32, SPLIT>(a.w, e, K, w[i]);
 #pragma unroll
             for (int j = 0; j < 8; ++j) d[j] = y[j] * w[i][j] - v[j] * c;
             if (a.dr) {
                 float f[8];
-                staged8<DT>(p + (kY + kH) * pitch, pitch, f);
+                if (stage_dr)
+                    staged8<DT>(p + (kY + kH) * pitch, pitch, f);
+                else
+                    load8<DT, SPLIT>(static_cast<const uint8_t *>(a.dr) + row * a.lddr * elem_bytes<DT>, e, K, f);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) d[j] = rstd * d[j] + f[j];
             } else {
@@ -345,6 +347,8 @@ __global__ void __launch_bounds__(512) rmsnorm_back_kernel(RmsnormBackArgs a) {
     }
     asm volatile("cp.async.wait_group 0;" ::: "memory");
     if (!a.partial) return;
+    // the second kernel's blocks may start; they wait for this grid's end themselves
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     // the rows of one block (short rows: one warp each) in threadIdx.y order
     if (blockDim.y > 1) {
         float *acc = reinterpret_cast<float *>(dyn);
