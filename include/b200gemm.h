@@ -325,8 +325,9 @@ B200GEMM_API gemm_status_t gemm_bf16_noalloc(const void *A, const void *B, void 
  * Operators around the products.  None of them allocates, keeps state or
  * waits inside a kernel on another; scratch, where one needs any, is the
  * caller's.  Calls on different streams are independent as long as their
- * buffers are.  As for the products, the first call of each kind on a device
- * may not be captured (GEMM_ERR_CAPTURE); matrices are row-major with 16-byte
+ * buffers are.  As for the products, the first use of a kernel on a device may
+ * not be captured (GEMM_ERR_CAPTURE): make one call of the same shapes and
+ * types outside the capture first.  Matrices are row-major with 16-byte
  * aligned bases and pitches, and no element outside their rows and columns is
  * read or written.  Types are gemm_out_t's: a matrix that a product wrote can
  * be passed on as it is.
@@ -431,9 +432,10 @@ B200GEMM_API gemm_status_t gemm_mxfp8_quantize(const void *X, uint8_t *Q, uint8_
  *   group   a power of two >= 32; from K on: one scale per row
  * K must be a multiple of 32, ldb (bytes) and lds of 16, lds >= ceil(K / group).
  * Products are exact, sums fp32 and in a fixed order, the result rounded once.
- * Any M is accepted; the kernel is built for M <= 64 (each 64 rows pass over
- * the weights again, and larger M is bound by the warp-level tensor
- * instruction: for long prompts, dequantise once and use gemm_bf16).
+ * The kernel is built for M <= 64.  More rows (up to 64 * 65535, beyond that
+ * GEMM_ERR_TOO_LARGE) are taken 64 at a time, each time over all weights, and
+ * are bound by the warp-level tensor instruction: for long prompts, keep a
+ * bf16 copy of the weights and use gemm_bf16.
  * C may not overlap an input.  M == 0 or N == 0: nothing to do; K == 0: C = 0.
  * One kernel.
  */
