@@ -213,6 +213,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, Cfg::PER_SM) gemm_w4_kernel(W4Ar
         asm volatile("cp.async.commit_group;" ::: "memory");   // one group per stage, empty ones too
     };
 
+    wait_for_stream();
 #pragma unroll
     for (int i = 0; i < S - 1; ++i) load_stage(s_begin + i);
 

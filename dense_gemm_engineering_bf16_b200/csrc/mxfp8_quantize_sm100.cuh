@@ -13,6 +13,7 @@ template <int XT, int VPT>
 __global__ void __launch_bounds__(256) mx_quantize_kernel(const void *x, uint8_t *q, uint8_t *sf, int64_t M, int64_t K,
                                                           int64_t ldx, int64_t ldq, unsigned parts) {
     constexpr bool SPLIT = XT == kF32;
+    wait_for_stream();
     const unsigned part = blockIdx.x % parts;
     const int64_t row = static_cast<int64_t>(blockIdx.x / parts) * blockDim.y + threadIdx.y;
     if (row >= M) return;   // whole warps
@@ -43,6 +44,7 @@ __global__ void __launch_bounds__(128) mx_quantize_mn_kernel(const void *x, uint
     constexpr int kPitch = 128 + 16;
     __shared__ __align__(16) uint8_t tile[64 * kPitch];
     __shared__ __align__(4) uint8_t scales[64][4];
+    wait_for_stream();
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
     const int64_t i0 = (static_cast<int64_t>(blockIdx.x) / k_tiles) * 64;
     const int64_t kb = (static_cast<int64_t>(blockIdx.x) % k_tiles) * 128, k0 = kb + 32 * warp;

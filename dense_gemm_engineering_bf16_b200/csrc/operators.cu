@@ -54,8 +54,27 @@ bool any_overlap(const Mat &out, const Mat (&others)[N]) {
     return false;
 }
 
-gemm_status_t launched() {
-    const cudaError_t e = cudaGetLastError();
+// One launch with programmatic dependence on the kernel before it in the
+// stream (wait_for_stream in the kernels): its blocks take their places while
+// that one finishes, which saves about a microsecond between two calls.
+// cluster: blocks per cluster along x.
+template <class... Params, class... Args>
+gemm_status_t launch(void (*kernel)(Params...), dim3 grid, dim3 block, int smem, cudaStream_t stream, int cluster,
+                     Args... args) {
+    cudaLaunchConfig_t lc = {};
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = static_cast<unsigned>(cluster);
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    lc.gridDim = grid;
+    lc.blockDim = block;
+    lc.dynamicSmemBytes = static_cast<size_t>(smem);
+    lc.stream = stream;
+    lc.attrs = attr;
+    lc.numAttrs = cluster > 1 ? 2 : 1;
+    const cudaError_t e = cudaLaunchKernelEx(&lc, kernel, static_cast<Params>(args)...);
     return e == cudaSuccess ? GEMM_OK : b200::host::cuda_fail(e);
 }
 
@@ -95,12 +114,11 @@ gemm_status_t launch_norm(int dev, const b200::RmsnormArgs &a, dim3 block, cudaS
     gemm_status_t s;
     if constexpr (VPT == 0) {
         if ((s = b200::host::prepare<b200::rmsnorm_long_kernel<XT, HT>>(dev, 0, stream)) != GEMM_OK) return s;
-        b200::rmsnorm_long_kernel<XT, HT><<<static_cast<unsigned>(blocks), block, 0, stream>>>(a);
+        return launch(b200::rmsnorm_long_kernel<XT, HT>, dim3(static_cast<unsigned>(blocks)), block, 0, stream, 1, a);
     } else {
         if ((s = b200::host::prepare<b200::rmsnorm_kernel<XT, HT, VPT>>(dev, 0, stream)) != GEMM_OK) return s;
-        b200::rmsnorm_kernel<XT, HT, VPT><<<static_cast<unsigned>(blocks), block, 0, stream>>>(a);
+        return launch(b200::rmsnorm_kernel<XT, HT, VPT>, dim3(static_cast<unsigned>(blocks)), block, 0, stream, 1, a);
     }
-    return launched();
 }
 
 template <int XT, int HT>
@@ -125,22 +143,6 @@ gemm_status_t dispatch_norm_h(int dev, int sm_count, const b200::RmsnormArgs &a,
 constexpr int64_t kPartialRows = 296;
 static_assert(kPartialRows <= 320, "rmsnorm_dw_kernel adds up to 320 shares");
 
-// The second kernel of the backward pass: starts early (programmatic
-// dependence) and waits for the first one's shares itself.
-gemm_status_t launch_dw(const float *partial, float *dw, int rows, int64_t K, cudaStream_t stream) {
-    cudaLaunchConfig_t lc = {};
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    lc.gridDim = dim3(static_cast<unsigned>((K + 31) / 32));
-    lc.blockDim = dim3(1024);
-    lc.stream = stream;
-    lc.attrs = &attr;
-    lc.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&lc, b200::rmsnorm_dw_kernel, partial, dw, rows, K);
-    return e == cudaSuccess ? GEMM_OK : b200::host::cuda_fail(e);
-}
-
 // VPT 0: rows too long for registers.
 template <int YT, int HT, int DT, int VPT>
 gemm_status_t launch_back(int dev, int sm_count, b200::RmsnormBackArgs a, dim3 block, float *dw, float *ws,
@@ -154,21 +156,22 @@ gemm_status_t launch_back(int dev, int sm_count, b200::RmsnormBackArgs a, dim3 b
     a.ring = VPT == 0 ? 0 : static_cast<int>(std::min<int64_t>(4, kSmemPerSm / (per_sm * row_bytes)));
     const int64_t rows = (a.M + block.y - 1) / block.y;
     const int64_t blocks = std::min({rows, per_sm * sm_count, kPartialRows});
+    const dim3 grid(static_cast<unsigned>(blocks));
     // one block's share of dw is dw itself
     if (dw) a.partial = blocks == 1 ? dw : ws;
     gemm_status_t s;
     if (dw && blocks > 1 && (s = b200::host::prepare<b200::rmsnorm_dw_kernel>(dev, 0, stream)) != GEMM_OK) return s;
     if constexpr (VPT == 0) {
         if ((s = b200::host::prepare<b200::rmsnorm_back_long_kernel<YT, HT, DT>>(dev, 0, stream)) != GEMM_OK) return s;
-        b200::rmsnorm_back_long_kernel<YT, HT, DT><<<static_cast<unsigned>(blocks), block, 0, stream>>>(a);
+        s = launch(b200::rmsnorm_back_long_kernel<YT, HT, DT>, grid, block, 0, stream, 1, a);
     } else {
         if ((s = b200::host::prepare<b200::rmsnorm_back_kernel<YT, HT, DT, VPT>>(dev, kSmemPerSm, stream)) != GEMM_OK)
             return s;
-        b200::rmsnorm_back_kernel<YT, HT, DT, VPT>
-            <<<static_cast<unsigned>(blocks), block, a.ring * row_bytes, stream>>>(a);
+        s = launch(b200::rmsnorm_back_kernel<YT, HT, DT, VPT>, grid, block, a.ring * row_bytes, stream, 1, a);
     }
-    if ((s = launched()) != GEMM_OK || !dw || blocks == 1) return s;
-    return launch_dw(ws, dw, static_cast<int>(blocks), a.K, stream);
+    if (s != GEMM_OK || !dw || blocks == 1) return s;
+    return launch(b200::rmsnorm_dw_kernel, dim3(static_cast<unsigned>((a.K + 31) / 32)), dim3(1024), 0, stream, 1, ws,
+                  dw, blocks, a.K);
 }
 
 // Rows of up to 1024 elements take a warp each (one, two or four vectors per
@@ -195,29 +198,27 @@ template <int XT, int VPT>
 gemm_status_t launch_quantize_rows(int dev, const void *X, uint8_t *Q, uint8_t *sf, int64_t M, int64_t K, int64_t ldx,
                                    int64_t ldq, cudaStream_t stream) {
     const int64_t vecs = K / 8;
-    const dim3 block = vecs <= 32 * VPT ? dim3(32, 8)
-                                        : dim3(static_cast<unsigned>(std::min(256, round_up((vecs + VPT - 1) / VPT, 32))));
+    dim3 block(32, 8);
+    if (vecs > 32 * VPT) block = dim3(static_cast<unsigned>(std::min(256, round_up((vecs + VPT - 1) / VPT, 32))));
     const int64_t parts = (vecs + VPT * block.x - 1) / (VPT * block.x);
     const int64_t blocks = (M + block.y - 1) / block.y * parts;
     if (blocks > kMaxDim) return GEMM_ERR_TOO_LARGE;
     gemm_status_t s;
     if ((s = b200::host::prepare<b200::mx_quantize_kernel<XT, VPT>>(dev, 0, stream)) != GEMM_OK) return s;
-    b200::mx_quantize_kernel<XT, VPT><<<static_cast<unsigned>(blocks), block, 0, stream>>>(
-        X, Q, sf, M, K, ldx, ldq, static_cast<unsigned>(parts));
-    return launched();
+    return launch(b200::mx_quantize_kernel<XT, VPT>, dim3(static_cast<unsigned>(blocks)), block, 0, stream, 1, X, Q, sf,
+                  M, K, ldx, ldq, parts);
 }
 
 template <int XT>
-gemm_status_t launch_quantize(int dev, int sm_count, const void *X, uint8_t *Q, uint8_t *sf, int64_t M, int64_t K, int64_t ldx,
-                              int64_t ldq, gemm_layout_t layout, cudaStream_t stream) {
+gemm_status_t launch_quantize(int dev, int sm_count, const void *X, uint8_t *Q, uint8_t *sf, int64_t M, int64_t K,
+                              int64_t ldx, int64_t ldq, gemm_layout_t layout, cudaStream_t stream) {
     gemm_status_t s;
     if (layout == GEMM_LAYOUT_MNMAJOR) {
         const int64_t k_tiles = (K + 127) / 128, blocks = k_tiles * ((M + 63) / 64);
         if (blocks > kMaxDim) return GEMM_ERR_TOO_LARGE;
         if ((s = b200::host::prepare<b200::mx_quantize_mn_kernel<XT>>(dev, 0, stream)) != GEMM_OK) return s;
-        b200::mx_quantize_mn_kernel<XT><<<static_cast<unsigned>(blocks), 128, 0, stream>>>(X, Q, sf, M, K, ldx, ldq,
-                                                                                         k_tiles);
-        return launched();
+        return launch(b200::mx_quantize_mn_kernel<XT>, dim3(static_cast<unsigned>(blocks)), dim3(128), 0, stream, 1, X,
+                      Q, sf, M, K, ldx, ldq, k_tiles);
     }
     // Four eights per thread; eight of bf16 where there are many rows: a block
     // then has as many bytes in flight as with fp32 (8192 x 8192 bf16: 32.1
@@ -246,19 +247,8 @@ gemm_status_t launch_w4(int dev, int sm_count, b200::W4Args a, cudaStream_t stre
     if (token_blocks > 65535 || tiles << shift > kMaxDim) return GEMM_ERR_TOO_LARGE;
     a.stages = static_cast<uint32_t>(stages);
     a.split_shift = shift;
-    cudaLaunchConfig_t lc = {};
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = 1u << shift;
-    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-    lc.gridDim = dim3(static_cast<unsigned>(tiles << shift), static_cast<unsigned>(token_blocks));
-    lc.blockDim = dim3(Cfg::THREADS);
-    lc.dynamicSmemBytes = Cfg::SMEM_BYTES;
-    lc.stream = stream;
-    lc.attrs = &attr;
-    lc.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&lc, b200::gemm_w4_kernel<Cfg, U>, a);
-    return e == cudaSuccess ? GEMM_OK : b200::host::cuda_fail(e);
+    const dim3 grid(static_cast<unsigned>(tiles << shift), static_cast<unsigned>(token_blocks));
+    return launch(b200::gemm_w4_kernel<Cfg, U>, grid, dim3(Cfg::THREADS), Cfg::SMEM_BYTES, stream, 1 << shift, a);
 }
 
 template <class Cfg>
@@ -364,8 +354,8 @@ gemm_status_t gemm_rmsnorm_backward(const void *dY, const void *H, const float *
     const b200::RmsnormBackArgs a{dY, H, weight, rstd, dR, dH, nullptr, M, K, lddy, ldh, lddr, lddh, 0,
                                   1.0f / static_cast<float>(K), true};
     float *ws = static_cast<float *>(workspace);
-    const int key = (dy_type == GEMM_OUT_F32 ? 4 : 0) | (h_type == GEMM_OUT_F32 ? 2 : 0) | (dh_type == GEMM_OUT_F32 ? 1 : 0);
-    switch (key) {
+    const auto f32 = [](gemm_out_t t) { return t == GEMM_OUT_F32 ? 1 : 0; };
+    switch (4 * f32(dy_type) + 2 * f32(h_type) + f32(dh_type)) {
         case 0: return dispatch_back<kBF16, kBF16, kBF16>(dev, sm_count, a, dW, ws, stream);
         case 1: return dispatch_back<kBF16, kBF16, kF32>(dev, sm_count, a, dW, ws, stream);
         case 2: return dispatch_back<kBF16, kF32, kBF16>(dev, sm_count, a, dW, ws, stream);

@@ -59,6 +59,7 @@ template <int XT, int HT, int VPT>
 __global__ void __launch_bounds__(VPT == 1 ? 1024 : 512) rmsnorm_kernel(RmsnormArgs a) {
     constexpr bool SPLIT = XT == kF32 || HT == kF32;
     __shared__ float red[2][1][32];
+    wait_for_stream();
     const int64_t row = static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y;
     if (row >= a.M) return;   // whole warps, and only where a row has one warp
     const uint8_t *x = static_cast<const uint8_t *>(a.x) + row * a.ldx * elem_bytes<XT>;
@@ -115,6 +116,7 @@ template <int XT, int HT>
 __global__ void __launch_bounds__(1024) rmsnorm_long_kernel(RmsnormArgs a) {
     constexpr bool SPLIT = XT == kF32 || HT == kF32;
     __shared__ float red[2][1][32];
+    wait_for_stream();
     const int64_t row = blockIdx.x;
     const uint8_t *x = static_cast<const uint8_t *>(a.x) + row * a.ldx * elem_bytes<XT>;
     const uint8_t *r = static_cast<const uint8_t *>(a.r) + row * a.ldr * elem_bytes<HT>;
@@ -238,6 +240,7 @@ template <int YT, int HT, int DT, int VPT>
 __global__ void __launch_bounds__(512) rmsnorm_back_kernel(RmsnormBackArgs a) {
     constexpr bool SPLIT = YT == kF32 || HT == kF32 || DT == kF32;
     __shared__ float red[2][1][32];
+    wait_for_stream();
     extern __shared__ __align__(16) uint8_t dyn[];
     constexpr int kY = YT == kF32 ? 2 : 1, kH = HT == kF32 ? 2 : 1, kD = DT == kF32 ? 2 : 1;
     const bool stage_dr = VPT < 4 || a.stage_dr;
@@ -347,8 +350,6 @@ __global__ void __launch_bounds__(512) rmsnorm_back_kernel(RmsnormBackArgs a) {
     }
     asm volatile("cp.async.wait_group 0;" ::: "memory");
     if (!a.partial) return;
-    // the second kernel's blocks may start; they wait for this grid's end themselves
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     // the rows of one block (short rows: one warp each) in threadIdx.y order
     if (blockDim.y > 1) {
         float *acc = reinterpret_cast<float *>(dyn);
@@ -392,6 +393,7 @@ template <int YT, int HT, int DT>
 __global__ void __launch_bounds__(1024) rmsnorm_back_long_kernel(RmsnormBackArgs a) {
     constexpr bool SPLIT = YT == kF32 || HT == kF32 || DT == kF32;
     __shared__ float red[2][1][32];
+    wait_for_stream();
     int phase = 0;
     const int64_t steps = (a.K + 8191) / 8192;
     bool first = true;
@@ -445,7 +447,7 @@ __global__ void __launch_bounds__(1024) rmsnorm_dw_kernel(const float *__restric
     __shared__ float part[32][33];
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
     const int64_t col = static_cast<int64_t>(blockIdx.x) * 32 + lane;
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    wait_for_stream();
     float v[10];
 #pragma unroll
     for (int i = 0; i < 10; ++i) {

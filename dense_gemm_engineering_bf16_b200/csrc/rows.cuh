@@ -157,6 +157,15 @@ __device__ __forceinline__ void round8(float (&f)[8]) {
     }
 }
 
+// Start of every kernel here (launched with programmatic dependence, so that
+// its blocks may take their places while the kernel before it in the stream
+// still runs): nothing is read or written before that kernel has finished
+// and its writes are visible; then the next one's blocks may come.
+__device__ __forceinline__ void wait_for_stream() {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
     for (int m = 16; m > 0; m >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, m);
