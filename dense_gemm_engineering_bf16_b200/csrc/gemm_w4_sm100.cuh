@@ -22,7 +22,15 @@
 // shared-memory stages of 256 K with 16-byte cp.async copies (one 128-byte
 // line per row and stage); the activations are shared by the block and staged
 // one stage ahead through registers.  The cluster's partial sums meet in
-// distributed shared memory and are added in a fixed order: no workspace, and the same result every time.
+// distributed shared memory and are added in a fixed order: no workspace, and
+// the same result every time.
+//
+// What bounds it: at 1 x 8192 x 8192 the copies alone take 8.1 us (5.3 is the
+// bytes' floor, the rest start and end), with the arithmetic 13.0; at 16 rows
+// 17.0.  Per 16 x 32 weights a warp issues 53 instructions, 20 of them bit
+// operations, which run at half rate, and an MMA takes some 6 of its 8 cycles
+// from them (measured: 8 multiply-adds and 8 bit operations 16.3 cycles, with an
+// MMA 22.7).  Each further 8 rows of a batch cost 4 to 5 us at this size.
 #pragma once
 #include <cuda_bf16.h>
 

@@ -5,6 +5,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cstdint>
 
 #include "b200gemm.h"
@@ -229,20 +230,58 @@ gemm_status_t launch_quantize(int dev, int sm_count, const void *X, uint8_t *Q, 
 
 // ------------------------------------------------------- 4-bit weights --
 
+// Blocks of a kernel that a device holds at once in clusters of 1, 2, 4 and 8:
+// fewer for larger clusters, which the SMs of a GPC do not always fill (two
+// blocks per SM: 296 of 148 SMs alone, but 284 in fours and 264 in eights).
+// Asked once per kernel and device, before any capture.
+struct ClusterRoom {
+    std::atomic<int> blocks[b200::host::kMaxDevices][4];
+};
+
+template <class Cfg, int U>
+gemm_status_t cluster_room(int dev, int sm_count, cudaStream_t stream, int (&room)[4]) {
+    static ClusterRoom known{};
+    gemm_status_t s;
+    if ((s = b200::host::prepare<b200::gemm_w4_kernel<Cfg, U>>(dev, Cfg::SMEM_BYTES, stream)) != GEMM_OK) return s;
+    for (int shift = 0; shift < 4; ++shift) {
+        room[shift] = known.blocks[dev][shift].load(std::memory_order_relaxed);
+        if (room[shift] > 0) continue;
+        int n = Cfg::PER_SM * sm_count;
+        if (shift > 0) {
+            cudaLaunchConfig_t lc = {};
+            cudaLaunchAttribute attr;
+            attr.id = cudaLaunchAttributeClusterDimension;
+            attr.val.clusterDim.x = 1u << shift;
+            attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+            lc.gridDim = dim3(1024);
+            lc.blockDim = dim3(Cfg::THREADS);
+            lc.dynamicSmemBytes = Cfg::SMEM_BYTES;
+            lc.attrs = &attr;
+            lc.numAttrs = 1;
+            int clusters = 0;
+            const cudaError_t e = cudaOccupancyMaxActiveClusters(&clusters, b200::gemm_w4_kernel<Cfg, U>, &lc);
+            if (e != cudaSuccess) return b200::host::cuda_fail(e);
+            n = std::max(1, clusters << shift);
+        }
+        known.blocks[dev][shift].store(n, std::memory_order_relaxed);
+        room[shift] = n;
+    }
+    return GEMM_OK;
+}
+
 template <class Cfg, int U>
 gemm_status_t launch_w4(int dev, int sm_count, b200::W4Args a, cudaStream_t stream) {
     gemm_status_t s;
-    if ((s = b200::host::prepare<b200::gemm_w4_kernel<Cfg, U>>(dev, Cfg::SMEM_BYTES, stream)) != GEMM_OK) return s;
+    int room[4];
+    if ((s = cluster_room<Cfg, U>(dev, sm_count, stream, room)) != GEMM_OK) return s;
     const int64_t tiles = (a.N + Cfg::ROWS - 1) / Cfg::ROWS;
     const int64_t token_blocks = (a.M + 8 * Cfg::NT - 1) / (8 * Cfg::NT);
     const int64_t stages = (a.K + b200::kW4K - 1) / b200::kW4K;
-    // K in 1, 2, 4 or 8 shares: as many as leave all blocks resident at once.
-    // (112-row blocks, which would be two for every SM at 8192 rows, were
-    // slower, 27.9 against 19.2 us at 16 x 8192 x 8192: clusters of four do not
-    // tile the SMs fully, and the last few ran as a second round.)
+    // K in 1, 2, 4 or 8 shares: as many as leave all blocks resident at once (a
+    // second round of a few clusters took half as long again: 27.9 against
+    // 19.2 us at 16 x 8192 x 8192 with 74 clusters of four)
     int shift = 0;
-    while (shift < 3 && (tiles * token_blocks << (shift + 1)) <= Cfg::PER_SM * sm_count &&
-           (int64_t(2) << shift) <= stages)
+    while (shift < 3 && (tiles * token_blocks << (shift + 1)) <= room[shift + 1] && (int64_t(2) << shift) <= stages)
         ++shift;
     if (token_blocks > 65535 || tiles << shift > kMaxDim) return GEMM_ERR_TOO_LARGE;
     a.stages = static_cast<uint32_t>(stages);
