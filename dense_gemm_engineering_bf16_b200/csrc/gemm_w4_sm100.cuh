@@ -8,8 +8,8 @@
 // warp-level tensor instruction mma.sync m16n8k16 with 16 weight rows as its
 // M and 8 activation rows as its N, and the scale is applied to the fp32 sum
 // of a group, not to each weight.  q - z is an integer in [-15, 15], exact in
-// bf16 (over 64 too), so the products are exact and the only roundings are those of the
-// fp32 sums and of the output.
+// bf16 (over 64 too), so the products are exact and the only roundings are
+// those of the fp32 sums and of the output.
 //
 // Codes to bf16 (w4_codes): one AND and one fused multiply-add per pair.  The
 // AND picks nibbles i and i + 4 of a 32-bit word of eight codes, so an MMA's K
@@ -17,13 +17,13 @@
 // order when they are staged in shared memory.  The weights come out divided by
 // 64, which the result makes good, exactly.
 //
-// A block takes 16 * MT weight rows per warp and a share of K (its rank in a
-// cluster).  Every warp streams its own rows through a ring of
-// shared-memory stages of 256 K with 16-byte cp.async copies (one 128-byte
-// line per row and stage); the activations are shared by the block and staged
-// one stage ahead through registers.  The cluster's partial sums meet in
-// distributed shared memory and are added in a fixed order: no workspace, and
-// the same result every time.
+// A block takes 16 weight rows per warp and a share of K (its rank in a
+// cluster).  Every warp streams its own rows through a ring of shared-memory
+// stages of 256 K with 16-byte cp.async copies (one 128-byte line per row and
+// stage); the activations are shared by the block and staged one stage ahead
+// through registers.  The cluster's partial sums meet in distributed shared
+// memory and are added in a fixed order: no workspace, and the same result
+// every time.
 //
 // What bounds it: at 1 x 8192 x 8192 the copies alone take 8.1 us (5.3 is the
 // bytes' floor, the rest start and end), with the arithmetic 13.0; at 16 rows
@@ -107,13 +107,12 @@ struct W4Args {
     int split_shift;         // log2 of the cluster's size
 };
 
-// NT: activation rows in eights; MT: weight rows per warp in sixteens; WARPS
-// per block; S: ring stages.
-template <int NT_, int MT_, int WARPS_, int S_>
+// NT: activation rows in eights; WARPS per block; S: ring stages.
+template <int NT_, int WARPS_, int S_>
 struct W4Cfg {
-    static constexpr int NT = NT_, MT = MT_, WARPS = WARPS_, S = S_;
+    static constexpr int NT = NT_, WARPS = WARPS_, S = S_;
     static constexpr int THREADS = 32 * WARPS;
-    static constexpr int WROWS = 16 * MT;                  // weight rows per warp
+    static constexpr int WROWS = 16;                       // weight rows per warp
     static constexpr int ROWS = WROWS * WARPS;             // and per block
     static constexpr int SLOT_BYTES = WROWS * kW4StageRow;
     static constexpr int RING_BYTES = S * SLOT_BYTES;      // per warp
@@ -144,7 +143,7 @@ __device__ __forceinline__ float w4_high(uint32_t w) { return __uint_as_float(w 
 // U: 32-K steps per scale (G = 32 U; 8 also for larger groups).
 template <class Cfg, int U>
 __global__ void __launch_bounds__(Cfg::THREADS, Cfg::PER_SM) gemm_w4_kernel(W4Args a) {
-    constexpr int NT = Cfg::NT, MT = Cfg::MT, S = Cfg::S, THREADS = Cfg::THREADS, WROWS = Cfg::WROWS;
+    constexpr int NT = Cfg::NT, S = Cfg::S, THREADS = Cfg::THREADS, WROWS = Cfg::WROWS;
     extern __shared__ __align__(128) uint8_t smem[];
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
     const int g = lane / 4, t = lane % 4;
@@ -161,17 +160,17 @@ __global__ void __launch_bounds__(Cfg::THREADS, Cfg::PER_SM) gemm_w4_kernel(W4Ar
     uint8_t *const x_smem = smem + Cfg::WARPS * Cfg::RING_BYTES;
     if (!a.zeros) {     // zeros of 8 in every slot, once
         for (int i = lane; i < S * WROWS; i += 32)
-            *reinterpret_cast<uint2 *>(ring + (i / WROWS) * Cfg::SLOT_BYTES + WROWS * (kW4Pitch + 16) + 8 * (i % WROWS)) =
-                make_uint2(0x08080808u, 0x08080808u);
+            *reinterpret_cast<uint2 *>(ring + (i / WROWS) * Cfg::SLOT_BYTES + WROWS * (kW4Pitch + 16) +
+                                       8 * (i % WROWS)) = make_uint2(0x08080808u, 0x08080808u);
     }
 
     // What this lane copies of each stage: 16 bytes (32 codes) of every fourth
     // row, and one row's scales and zeros.  Rows past N repeat the last row
     // (their sums are not stored), so that only the end of K needs a test.
     const int64_t n_warp = n0 + warp * WROWS;
-    const uint8_t *codes[4 * MT];
+    const uint8_t *codes[4];
 #pragma unroll
-    for (int i = 0; i < 4 * MT; ++i)
+    for (int i = 0; i < 4; ++i)
         codes[i] = a.b + min(n_warp + (lane >> 3) + 4 * i, a.N - 1) * a.ldb + 16 * (lane & 7);
     const uint32_t codes_dst = smem_addr(ring) + (lane >> 3) * kW4Pitch + 16 * (lane & 7);
     const int64_t side_row = min(n_warp + lane % WROWS, a.N - 1) * a.lds;
@@ -187,7 +186,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, Cfg::PER_SM) gemm_w4_kernel(W4Ar
             // slot held: any code is finite, and its activations are zero.
             if (st * (kW4K / 32) + (lane & 7) < k_steps) {
 #pragma unroll
-                for (int i = 0; i < 4 * MT; ++i)
+                for (int i = 0; i < 4; ++i)
                     w4_copy<16>(codes_dst + fill + 4 * i * kW4Pitch, codes[i] + st * (kW4K / 2));
             }
             // per row the stage's scales and zeros, each in one copy from a
@@ -258,7 +257,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, Cfg::PER_SM) gemm_w4_kernel(W4Ar
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) x_row[nt] = min(8 * nt + g, tokens - 1) * kW4XPitch + 16 * t;
 
-    float acc[MT][NT][4] = {};
+    float acc[NT][4] = {};
     uint32_t read = 0;                    // ring slot (byte offset) to read
     uint32_t x_read = 0;                  // and activation buffer
     load_x(s_begin);
@@ -276,40 +275,36 @@ __global__ void __launch_bounds__(Cfg::THREADS, Cfg::PER_SM) gemm_w4_kernel(W4Ar
         // the stage's scales and zeros of this lane's rows: 8 / U groups from g_low on
         const uint32_t g_low = U == 8 ? st >> (a.group_shift - 8) : U == 4 ? 2 * st : 0u;
         constexpr int GROUPS = 8 / U;
-        float scale[MT][2][GROUPS];
-        uint32_t zero[MT][2][(GROUPS + 3) / 4];
+        float scale[2][GROUPS];
+        uint32_t zero[2][(GROUPS + 3) / 4];
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
+        for (int h = 0; h < 2; ++h) {
+            const int row = 8 * h + g;
+            const uint8_t *sc = src + WROWS * kW4Pitch + 16 * row;
+            if constexpr (U == 8) {
+                scale[h][0] = w4_low(*reinterpret_cast<const uint16_t *>(sc + 2 * (g_low & 1)));
+            } else {
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int row = 16 * mt + 8 * h + g;
-                const uint8_t *sc = src + WROWS * kW4Pitch + 16 * row;
-                if constexpr (U == 8) {
-                    scale[mt][h][0] = w4_low(*reinterpret_cast<const uint16_t *>(sc + 2 * (g_low & 1)));
-                } else {
-#pragma unroll
-                    for (int i = 0; i < GROUPS / 2; ++i) {
-                        const uint32_t w = reinterpret_cast<const uint32_t *>(sc)[i];
-                        scale[mt][h][2 * i] = w4_low(w);
-                        scale[mt][h][2 * i + 1] = w4_high(w);
-                    }
+                for (int i = 0; i < GROUPS / 2; ++i) {
+                    const uint32_t w = reinterpret_cast<const uint32_t *>(sc)[i];
+                    scale[h][2 * i] = w4_low(w);
+                    scale[h][2 * i + 1] = w4_high(w);
                 }
-                const uint8_t *zr = src + WROWS * (kW4Pitch + 16) + 8 * row;
-#pragma unroll
-                for (int i = 0; i < (GROUPS + 3) / 4; ++i)
-                    zero[mt][h][i] = (reinterpret_cast<const uint32_t *>(zr)[i] & 0x0F0F0F0Fu) >> (8 * (g_low & 3));
             }
+            const uint8_t *zr = src + WROWS * (kW4Pitch + 16) + 8 * row;
+#pragma unroll
+            for (int i = 0; i < (GROUPS + 3) / 4; ++i)
+                zero[h][i] = (reinterpret_cast<const uint32_t *>(zr)[i] & 0x0F0F0F0Fu) >> (8 * (g_low & 3));
+        }
 #pragma unroll
         for (int grp = 0; grp < GROUPS; ++grp) {
             // The two MMAs of a step add to one sum only where other sums stand
             // between them: a dependent MMA waits some 20 cycles.
             constexpr int CHAINS = NT <= 2 ? 2 : 1;
-            float part[CHAINS][MT][NT][4];
-            uint32_t minus[MT][2];
+            float part[CHAINS][NT][4];
+            uint32_t minus[2];
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-                for (int h = 0; h < 2; ++h) minus[mt][h] = w4_minus(zero[mt][h][grp / 4], grp % 4);
+            for (int h = 0; h < 2; ++h) minus[h] = w4_minus(zero[h][grp / 4], grp % 4);
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 const int j = grp * U + u;
@@ -322,44 +317,34 @@ __global__ void __launch_bounds__(Cfg::THREADS, Cfg::PER_SM) gemm_w4_kernel(W4Ar
                     x[nt][2] = v.z;
                     x[nt][3] = v.w;
                 }
+                const uint8_t *w = src + g * kW4Pitch + 16 * j + 4 * t;
+                const uint32_t lo = *reinterpret_cast<const uint32_t *>(w);
+                const uint32_t hi = *reinterpret_cast<const uint32_t *>(w + 8 * kW4Pitch);
+                const uint32_t a0[4] = {w4_codes<0>(lo, minus[0]), w4_codes<0>(hi, minus[1]),
+                                        w4_codes<1>(lo, minus[0]), w4_codes<1>(hi, minus[1])};
+                const uint32_t a1[4] = {w4_codes<0>(lo >> 8, minus[0]), w4_codes<0>(hi >> 8, minus[1]),
+                                        w4_codes<1>(lo >> 8, minus[0]), w4_codes<1>(hi >> 8, minus[1])};
 #pragma unroll
-                for (int mt = 0; mt < MT; ++mt) {
-                    const uint8_t *w = src + (16 * mt + g) * kW4Pitch + 16 * j + 4 * t;
-                    const uint32_t lo = *reinterpret_cast<const uint32_t *>(w);
-                    const uint32_t hi = *reinterpret_cast<const uint32_t *>(w + 8 * kW4Pitch);
-                    uint32_t a0[4], a1[4];
-                    a0[0] = w4_codes<0>(lo, minus[mt][0]);
-                    a0[1] = w4_codes<0>(hi, minus[mt][1]);
-                    a0[2] = w4_codes<1>(lo, minus[mt][0]);
-                    a0[3] = w4_codes<1>(hi, minus[mt][1]);
-                    a1[0] = w4_codes<0>(lo >> 8, minus[mt][0]);
-                    a1[1] = w4_codes<0>(hi >> 8, minus[mt][1]);
-                    a1[2] = w4_codes<1>(lo >> 8, minus[mt][0]);
-                    a1[3] = w4_codes<1>(hi >> 8, minus[mt][1]);
+                for (int nt = 0; nt < NT; ++nt) {
+                    float (&p)[4] = part[0][nt];
+                    if (u == 0) w4_mma(p, a0, x[nt][0], x[nt][1], 0.0f, 0.0f, 0.0f, 0.0f);
+                    else w4_mma(p, a0, x[nt][0], x[nt][1], p[0], p[1], p[2], p[3]);
+                }
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        float (&p)[4] = part[0][mt][nt];
-                        if (u == 0) w4_mma(p, a0, x[nt][0], x[nt][1], 0.0f, 0.0f, 0.0f, 0.0f);
-                        else w4_mma(p, a0, x[nt][0], x[nt][1], p[0], p[1], p[2], p[3]);
-                    }
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        float (&p)[4] = part[CHAINS - 1][mt][nt];
-                        if (u == 0 && CHAINS == 2) w4_mma(p, a1, x[nt][2], x[nt][3], 0.0f, 0.0f, 0.0f, 0.0f);
-                        else w4_mma(p, a1, x[nt][2], x[nt][3], p[0], p[1], p[2], p[3]);
-                    }
+                for (int nt = 0; nt < NT; ++nt) {
+                    float (&p)[4] = part[CHAINS - 1][nt];
+                    if (u == 0 && CHAINS == 2) w4_mma(p, a1, x[nt][2], x[nt][3], 0.0f, 0.0f, 0.0f, 0.0f);
+                    else w4_mma(p, a1, x[nt][2], x[nt][3], p[0], p[1], p[2], p[3]);
                 }
             }
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt)
+            for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        float p = part[0][mt][nt][r];
-                        if (CHAINS == 2) p += part[1][mt][nt][r];
-                        acc[mt][nt][r] += scale[mt][r / 2][grp] * p;
-                    }
+                for (int r = 0; r < 4; ++r) {
+                    float p = part[0][nt][r];
+                    if (CHAINS == 2) p += part[1][nt][r];
+                    acc[nt][r] += scale[r / 2][grp] * p;
+                }
         }
     }
     asm volatile("cp.async.wait_group 0;" ::: "memory");
@@ -368,13 +353,10 @@ __global__ void __launch_bounds__(Cfg::THREADS, Cfg::PER_SM) gemm_w4_kernel(W4Ar
     // partial sums [token][row] over the rings
     float *red = reinterpret_cast<float *>(smem);
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
+    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int r = 0; r < 4; ++r)
-                red[(8 * nt + 2 * t + (r & 1)) * Cfg::RED_PITCH + warp * WROWS + 16 * mt + g + 8 * (r / 2)] =
-                    acc[mt][nt][r];
+        for (int r = 0; r < 4; ++r)
+            red[(8 * nt + 2 * t + (r & 1)) * Cfg::RED_PITCH + warp * WROWS + g + 8 * (r / 2)] = acc[nt][r];
     if (split > 1) cluster_sync_all();
     else __syncthreads();
     // Rank r writes its share of the rows, summed in rank order; the shares of

@@ -465,12 +465,15 @@ gemm_status_t gemm_bf16_w4(const void *A, const uint8_t *B, const void *scales, 
     a.groups = groups;
     a.group_shift = shift;
     a.out = c_type == GEMM_OUT_F32 ? kF32 : kBF16;
-    if (M <= 8) return dispatch_w4<b200::W4Cfg<1, 1, 8, 4>>(dev, sm_count, a, stream);
-    if (M <= 16) return dispatch_w4<b200::W4Cfg<2, 1, 8, 3>>(dev, sm_count, a, stream);
-    if (M <= 24) return dispatch_w4<b200::W4Cfg<3, 1, 8, 3>>(dev, sm_count, a, stream);
-    if (M <= 32) return dispatch_w4<b200::W4Cfg<4, 1, 8, 2>>(dev, sm_count, a, stream);
-    if (M <= 48) return dispatch_w4<b200::W4Cfg<6, 1, 8, 3>>(dev, sm_count, a, stream);
-    return dispatch_w4<b200::W4Cfg<8, 1, 8, 2>>(dev, sm_count, a, stream);
+    // a kernel for each size of batch (its sums and activations stay in
+    // registers and shared memory); ring stages as shared memory allows with
+    // two blocks per SM, or one from 33 rows on
+    if (M <= 8) return dispatch_w4<b200::W4Cfg<1, 8, 4>>(dev, sm_count, a, stream);
+    if (M <= 16) return dispatch_w4<b200::W4Cfg<2, 8, 3>>(dev, sm_count, a, stream);
+    if (M <= 24) return dispatch_w4<b200::W4Cfg<3, 8, 3>>(dev, sm_count, a, stream);
+    if (M <= 32) return dispatch_w4<b200::W4Cfg<4, 8, 2>>(dev, sm_count, a, stream);
+    if (M <= 48) return dispatch_w4<b200::W4Cfg<6, 8, 3>>(dev, sm_count, a, stream);
+    return dispatch_w4<b200::W4Cfg<8, 8, 2>>(dev, sm_count, a, stream);
 }
 
 }  // extern "C"
