@@ -215,11 +215,11 @@ gemm_status_t launch_quantize(int dev, int sm_count, const void *X, uint8_t *Q, 
                               int64_t ldx, int64_t ldq, gemm_layout_t layout, cudaStream_t stream) {
     gemm_status_t s;
     if (layout == GEMM_LAYOUT_MNMAJOR) {
-        const int64_t k_tiles = (K + 127) / 128, blocks = k_tiles * ((M + 63) / 64);
+        const int64_t i_tiles = (M + 63) / 64, blocks = i_tiles * ((K + 127) / 128);
         if (blocks > kMaxDim) return GEMM_ERR_TOO_LARGE;
         if ((s = b200::host::prepare<b200::mx_quantize_mn_kernel<XT>>(dev, 0, stream)) != GEMM_OK) return s;
         return launch(b200::mx_quantize_mn_kernel<XT>, dim3(static_cast<unsigned>(blocks)), dim3(128), 0, stream, 1, X,
-                      Q, sf, M, K, ldx, ldq, k_tiles);
+                      Q, sf, M, K, ldx, ldq, i_tiles);
     }
     // Four eights per thread; eight of bf16 where there are many rows: a block
     // then has as many bytes in flight as with fp32 (8192 x 8192 bf16: 32.1
