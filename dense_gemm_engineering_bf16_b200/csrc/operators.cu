@@ -148,15 +148,21 @@ static_assert(kPartialRows <= 320, "rmsnorm_dw_kernel adds up to 320 shares");
 template <int YT, int HT, int DT, int VPT>
 gemm_status_t launch_back(int dev, int sm_count, b200::RmsnormBackArgs a, dim3 block, float *dw, float *ws,
                           cudaStream_t stream) {
-    // rows in shared memory: as many (2 to 4) as leave room for two blocks per
-    // SM, or else for one
-    const int piece_bytes = static_cast<int>(VPT * 16 * block.x * block.y);
-    a.stage_dr = VPT < 4 || 2 * b200::back_pieces<YT, HT, DT>(true) * piece_bytes <= kSmemPerSm;
-    const int row_bytes = b200::back_pieces<YT, HT, DT>(a.stage_dr) * piece_bytes;
-    const int64_t per_sm = block.x * block.y <= 256 && 4 * row_bytes <= kSmemPerSm ? 2 : 1;
-    a.ring = VPT == 0 ? 0 : static_cast<int>(std::min<int64_t>(4, kSmemPerSm / (per_sm * row_bytes)));
+    // One block per SM (its registers allow 512 threads): as many rows as that
+    // holds at a time, and two to four in shared memory for each.
+    const auto row_bytes = [&](bool stage_dr) {
+        return static_cast<int>(VPT * 16 * block.x) * b200::back_pieces<YT, HT, DT>(stage_dr);
+    };
+    a.stage_dr = VPT < 4 || 2 * row_bytes(true) <= kSmemPerSm;
+    if (VPT > 0) {
+        const int64_t share = (a.M + sm_count - 1) / sm_count;      // rows per SM
+        block.y = static_cast<unsigned>(std::min<int64_t>({b200::kMaxRows, 512 / block.x, share,
+                                                           kSmemPerSm / (2 * row_bytes(a.stage_dr))}));
+        a.ring = std::min(4, kSmemPerSm / (row_bytes(a.stage_dr) * static_cast<int>(block.y)));
+    }
+    const int smem = a.ring * row_bytes(a.stage_dr) * static_cast<int>(block.y);
     const int64_t rows = (a.M + block.y - 1) / block.y;
-    const int64_t blocks = std::min({rows, per_sm * sm_count, kPartialRows});
+    const int64_t blocks = std::min({rows, static_cast<int64_t>(sm_count), kPartialRows});
     const dim3 grid(static_cast<unsigned>(blocks));
     // one block's share of dw is dw itself
     if (dw) a.partial = blocks == 1 ? dw : ws;
@@ -168,25 +174,25 @@ gemm_status_t launch_back(int dev, int sm_count, b200::RmsnormBackArgs a, dim3 b
     } else {
         if ((s = b200::host::prepare<b200::rmsnorm_back_kernel<YT, HT, DT, VPT>>(dev, kSmemPerSm, stream)) != GEMM_OK)
             return s;
-        s = launch(b200::rmsnorm_back_kernel<YT, HT, DT, VPT>, grid, block, a.ring * row_bytes, stream, 1, a);
+        s = launch(b200::rmsnorm_back_kernel<YT, HT, DT, VPT>, grid, block, smem, stream, 1, a);
     }
     if (s != GEMM_OK || !dw || blocks == 1) return s;
     return launch(b200::rmsnorm_dw_kernel, dim3(static_cast<unsigned>((a.K + 31) / 32)), dim3(1024), 0, stream, 1, ws,
                   dw, blocks, a.K);
 }
 
-// Rows of up to 1024 elements take a warp each (one, two or four vectors per
-// thread); longer ones a block with two vectors per thread, as far as 512
-// threads go, then four: what a thread does once per row (addresses, the sum
-// across the block) is spread over more elements than with one.
+// Rows of up to 1024 elements take a warp each (one, two or four eights per
+// thread); longer ones up to 512 threads with two eights each, then four: what a
+// thread does once per row (addresses, the sum across the warps) is spread
+// over more elements than with one.
 template <int YT, int HT, int DT>
 gemm_status_t dispatch_back(int dev, int sm_count, const b200::RmsnormBackArgs &a, float *dw, float *ws,
                             cudaStream_t stream) {
     const int64_t vecs = (a.K + 7) / 8;
     const auto block = [&](int vpt) { return dim3(static_cast<unsigned>(round_up((vecs + vpt - 1) / vpt, 32))); };
-    if (vecs <= 32) return launch_back<YT, HT, DT, 1>(dev, sm_count, a, dim3(32, 8), dw, ws, stream);
-    if (vecs <= 64) return launch_back<YT, HT, DT, 2>(dev, sm_count, a, dim3(32, 8), dw, ws, stream);
-    if (vecs <= 128) return launch_back<YT, HT, DT, 4>(dev, sm_count, a, dim3(32, 8), dw, ws, stream);
+    if (vecs <= 32) return launch_back<YT, HT, DT, 1>(dev, sm_count, a, dim3(32), dw, ws, stream);
+    if (vecs <= 64) return launch_back<YT, HT, DT, 2>(dev, sm_count, a, dim3(32), dw, ws, stream);
+    if (vecs <= 128) return launch_back<YT, HT, DT, 4>(dev, sm_count, a, dim3(32), dw, ws, stream);
     if (vecs <= 1024) return launch_back<YT, HT, DT, 2>(dev, sm_count, a, block(2), dw, ws, stream);
     if (vecs <= 2048 && 2 * 16 * b200::back_pieces<YT, HT, DT>(false) * 4 * block(4).x <= kSmemPerSm)
         return launch_back<YT, HT, DT, 4>(dev, sm_count, a, block(4), dw, ws, stream);

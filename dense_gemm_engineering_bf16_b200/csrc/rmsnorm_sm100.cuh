@@ -15,22 +15,19 @@
 
 namespace b200 {
 
-// Sum over the threads of a row.  With more than one warp per row the block
-// holds one row only; `red` has two halves that alternate by `phase`, so that
-// one barrier per sum is enough.
-template <int N>
-__device__ __forceinline__ void row_sum(float (&s)[N], float (*red)[N][32], int phase) {
-#pragma unroll
-    for (int i = 0; i < N; ++i) s[i] = warp_sum(s[i]);
-    if (blockDim.x == 32) return;
+// Sum over the blockDim.x threads of a row.  With more than one warp per row
+// the warps of a row meet at a barrier of their own (1 + threadIdx.y; rows of
+// three warps and more are at most five to a block), and `red`, their row's, has
+// two halves that alternate by `phase`, so that one barrier per sum is enough.
+constexpr int kMaxRows = 16;
+
+__device__ __forceinline__ float row_sum(float s, float (*red)[32], int phase) {
+    s = warp_sum(s);
+    if (blockDim.x == 32) return s;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, warps = blockDim.x / 32;
-    if (lane == 0) {
-#pragma unroll
-        for (int i = 0; i < N; ++i) red[phase][i][warp] = s[i];
-    }
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < N; ++i) s[i] = warp_sum(lane < warps ? red[phase][i][lane] : 0.0f);
+    if (lane == 0) red[phase][warp] = s;
+    asm volatile("bar.sync %0, %1;" ::"r"(1 + threadIdx.y), "r"(blockDim.x) : "memory");
+    return warp_sum(lane < warps ? red[phase][lane] : 0.0f);
 }
 
 struct RmsnormArgs {
@@ -60,7 +57,7 @@ __device__ __forceinline__ void rmsnorm_write(const RmsnormArgs &a, int64_t row,
 template <int XT, int HT, int VPT>
 __global__ void __launch_bounds__(VPT == 1 ? 1024 : 512) rmsnorm_kernel(RmsnormArgs a) {
     constexpr bool SPLIT = XT == kF32 || HT == kF32;
-    __shared__ float red[2][1][32];
+    __shared__ float red[2][32];
     wait_for_stream();
     const int64_t row = static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y;
     if (row >= a.M) return;   // whole warps, and only where a row has one warp
@@ -95,13 +92,13 @@ __global__ void __launch_bounds__(VPT == 1 ? 1024 : 512) rmsnorm_kernel(RmsnormA
     }
     // with one eight per thread (few rows) the weights' latency overlaps the sum
     if constexpr (VPT == 1) load8<kF32, SPLIT>(a.w, first8<SPLIT>(threadIdx.x, 0, blockDim.x), a.K, w);
-    float s[1] = {0.0f};
+    float s = 0.0f;
 #pragma unroll
     for (int i = 0; i < VPT; ++i)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) s[0] += v[i][j] * v[i][j];
-    row_sum<1>(s, red, 0);
-    const float rstd = 1.0f / sqrtf(s[0] / static_cast<float>(a.K) + a.eps);
+        for (int j = 0; j < 8; ++j) s += v[i][j] * v[i][j];
+    s = row_sum(s, red, 0);
+    const float rstd = 1.0f / sqrtf(s / static_cast<float>(a.K) + a.eps);
     if (a.rstd && threadIdx.x == 0) a.rstd[row] = rstd;
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
@@ -117,7 +114,7 @@ __global__ void __launch_bounds__(VPT == 1 ? 1024 : 512) rmsnorm_kernel(RmsnormA
 template <int XT, int HT>
 __global__ void __launch_bounds__(1024) rmsnorm_long_kernel(RmsnormArgs a) {
     constexpr bool SPLIT = XT == kF32 || HT == kF32;
-    __shared__ float red[2][1][32];
+    __shared__ float red[2][32];
     wait_for_stream();
     const int64_t row = blockIdx.x;
     const uint8_t *x = static_cast<const uint8_t *>(a.x) + row * a.ldx * elem_bytes<XT>;
@@ -134,7 +131,7 @@ __global__ void __launch_bounds__(1024) rmsnorm_long_kernel(RmsnormArgs a) {
             round8<HT>(v);
         }
     };
-    float s[1] = {0.0f};
+    float s = 0.0f;
     for (int64_t i = 0; i < steps; ++i) {
         const int64_t e = 8192 * i + first8<SPLIT>(threadIdx.x, 0, 1024);
         float v[8];
@@ -145,10 +142,10 @@ __global__ void __launch_bounds__(1024) rmsnorm_long_kernel(RmsnormArgs a) {
         float p = 0.0f;
 #pragma unroll
         for (int j = 0; j < 8; ++j) p += v[j] * v[j];
-        s[0] += p;
+        s += p;
     }
-    row_sum<1>(s, red, 0);
-    const float rstd = 1.0f / sqrtf(s[0] / static_cast<float>(a.K) + a.eps);
+    s = row_sum(s, red, 0);
+    const float rstd = 1.0f / sqrtf(s / static_cast<float>(a.K) + a.eps);
     if (a.rstd && threadIdx.x == 0) a.rstd[row] = rstd;
     for (int64_t i = 0; i < steps; ++i) {
         const int64_t e = 8192 * i + first8<SPLIT>(threadIdx.x, 0, 1024);
@@ -234,6 +231,7 @@ constexpr int back_pieces(bool stage_dr) {
 // Persistent blocks: block b takes rows b, b + gridDim.x, ... (times
 // blockDim.y) and keeps its share of dw in registers, written out once at
 // the end and summed over the blocks by rmsnorm_dw_kernel in block order.
+// Short rows share a block of 512 threads, each with a barrier of its own.
 // The next rows are on their way into shared memory while one is summed and
 // written (the barrier in the middle of each row would leave memory idle
 // otherwise), and what a row's second half needs is read from there again,
@@ -244,7 +242,7 @@ constexpr int back_pieces(bool stage_dr) {
 template <int YT, int HT, int DT, int VPT>
 __global__ void __launch_bounds__(512) rmsnorm_back_kernel(RmsnormBackArgs a) {
     constexpr bool SPLIT = YT == kF32 || HT == kF32 || DT == kF32;
-    __shared__ float red[2][1][32];
+    __shared__ float red[kMaxRows][2][32];
     wait_for_stream();
     extern __shared__ __align__(16) uint8_t dyn[];
     constexpr int kY = YT == kF32 ? 2 : 1, kH = HT == kF32 ? 2 : 1, kD = DT == kF32 ? 2 : 1;
@@ -307,7 +305,7 @@ __global__ void __launch_bounds__(512) rmsnorm_back_kernel(RmsnormBackArgs a) {
         else asm volatile("cp.async.wait_group 0;" ::: "memory");
         load_row();     // into the slot this thread read in the previous iteration
         const float next_rstd = row + stride < a.M ? a.rstd[row + stride] : 0.0f;
-        float s[1] = {0.0f};
+        float s = 0.0f;
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
             const uint8_t *p = mine + slot + i * pieces * pitch;
@@ -318,13 +316,13 @@ __global__ void __launch_bounds__(512) rmsnorm_back_kernel(RmsnormBackArgs a) {
             for (int j = 0; j < 8; ++j) {
                 const float p = y[j] * v[j];        // dy h: times rstd for dw, times w for the sum
                 dw[i][j] += p * rstd;
-                s[0] += p * w[i][j];
+                s += p * w[i][j];
             }
         }
-        row_sum<1>(s, red, phase);
+        s = row_sum(s, red[threadIdx.y], phase);
         phase ^= 1;
         // n mean(g n) = h c with c = rstd^2 sum(dy h w) / K
-        const float c = rstd * rstd * (s[0] * a.inv_k);
+        const float c = rstd * rstd * (s * a.inv_k);
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
             const int e = e0 + 8 * i * static_cast<int>(blockDim.x);
@@ -354,27 +352,26 @@ __global__ void __launch_bounds__(512) rmsnorm_back_kernel(RmsnormBackArgs a) {
     }
     asm volatile("cp.async.wait_group 0;" ::: "memory");
     if (!a.partial) return;
-    // the rows of one block (short rows: one warp each) in threadIdx.y order
+    // the sums of a block's rows meet in shared memory and are added in threadIdx.y order
     if (blockDim.y > 1) {
+        const int T = static_cast<int>(blockDim.x), sums = VPT * 8 * T, threads = T * static_cast<int>(blockDim.y);
         float *acc = reinterpret_cast<float *>(dyn);
         __syncthreads();
-        for (unsigned r = 0; r < blockDim.y; ++r) {
-            if (threadIdx.y == r) {
 #pragma unroll
-                for (int i = 0; i < VPT; ++i)
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        float *p = &acc[(i * 8 + j) * 32 + threadIdx.x];
-                        *p = r ? *p + dw[i][j] : dw[i][j];
-                    }
-            }
-            __syncthreads();
+        for (int i = 0; i < VPT; ++i) {
+            const int at = threadIdx.y * sums + 8 * (i * T + static_cast<int>(threadIdx.x));
+            float4 *d = reinterpret_cast<float4 *>(acc + at);
+            d[0] = make_float4(dw[i][0], dw[i][1], dw[i][2], dw[i][3]);
+            d[1] = make_float4(dw[i][4], dw[i][5], dw[i][6], dw[i][7]);
         }
-        if (threadIdx.y != 0) return;
-#pragma unroll
-        for (int i = 0; i < VPT; ++i)
-#pragma unroll
-            for (int j = 0; j < 8; ++j) dw[i][j] = acc[(i * 8 + j) * 32 + threadIdx.x];
+        __syncthreads();
+        for (int at = static_cast<int>(threadIdx.y) * T + static_cast<int>(threadIdx.x); at < sums; at += threads) {
+            float v = 0.0f;
+            for (unsigned r = 0; r < blockDim.y; ++r) v += acc[r * sums + at];
+            const int64_t col = first8<SPLIT>(at / 8, 0, T) + at8<SPLIT>(at % 8);
+            if (col < K) a.partial[static_cast<int64_t>(blockIdx.x) * a.K + col] = v;
+        }
+        return;
     }
     // rows of `partial` are K floats apart: 16-byte aligned where K is a multiple of four
     float *p = a.partial + static_cast<int64_t>(blockIdx.x) * a.K;
@@ -396,7 +393,7 @@ __global__ void __launch_bounds__(512) rmsnorm_back_kernel(RmsnormBackArgs a) {
 template <int YT, int HT, int DT>
 __global__ void __launch_bounds__(1024) rmsnorm_back_long_kernel(RmsnormBackArgs a) {
     constexpr bool SPLIT = YT == kF32 || HT == kF32 || DT == kF32;
-    __shared__ float red[2][1][32];
+    __shared__ float red[2][32];
     wait_for_stream();
     int phase = 0;
     const int64_t steps = (a.K + 8191) / 8192;
@@ -407,7 +404,7 @@ __global__ void __launch_bounds__(1024) rmsnorm_back_long_kernel(RmsnormBackArgs
         const uint8_t *dr = static_cast<const uint8_t *>(a.dr) + row * a.lddr * elem_bytes<DT>;
         uint8_t *dh = static_cast<uint8_t *>(a.dh) + row * a.lddh * elem_bytes<DT>;
         const float rstd = a.rstd[row];
-        float s[1] = {0.0f};
+        float s = 0.0f;
         for (int64_t i = 0; i < steps; ++i) {
             const int64_t e = 8192 * i + first8<SPLIT>(threadIdx.x, 0, 1024);
             float y[8], v[8], w[8], p = 0.0f;
@@ -416,11 +413,11 @@ __global__ void __launch_bounds__(1024) rmsnorm_back_long_kernel(RmsnormBackArgs
             load8<kF32, SPLIT>(a.w, e, a.K, w);
 #pragma unroll
             for (int j = 0; j < 8; ++j) p += y[j] * w[j] * (v[j] * rstd);
-            s[0] += p;
+            s += p;
         }
-        row_sum<1>(s, red, phase);
+        s = row_sum(s, red, phase);
         phase ^= 1;
-        const float mean = s[0] / static_cast<float>(a.K);
+        const float mean = s / static_cast<float>(a.K);
         for (int64_t i = 0; i < steps; ++i) {
             const int64_t e = 8192 * i + first8<SPLIT>(threadIdx.x, 0, 1024);
             float y[8], v[8], w[8], d[8];
