@@ -16,17 +16,20 @@
 namespace b200 {
 
 // Sum over the blockDim.x threads of a row.  With more than one warp per row
-// the warps of a row meet at a barrier of their own (1 + threadIdx.y; rows of
-// three warps and more are at most five to a block), and `red`, their row's, has
+// the warps of a row meet at a barrier of their own (1 + threadIdx.y, at most
+// 8: rows of two warps are up to eight to a block), and `red`, their row's, has
 // two halves that alternate by `phase`, so that one barrier per sum is enough.
+// SHARED: several rows of more than one warp may share the block.
 constexpr int kMaxRows = 16;
 
+template <bool SHARED>
 __device__ __forceinline__ float row_sum(float s, float (*red)[32], int phase) {
     s = warp_sum(s);
     if (blockDim.x == 32) return s;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, warps = blockDim.x / 32;
     if (lane == 0) red[phase][warp] = s;
-    asm volatile("bar.sync %0, %1;" ::"r"(1 + threadIdx.y), "r"(blockDim.x) : "memory");
+    if constexpr (SHARED) asm volatile("bar.sync %0, %1;" ::"r"(1 + threadIdx.y), "r"(blockDim.x) : "memory");
+    else __syncthreads();
     return warp_sum(lane < warps ? red[phase][lane] : 0.0f);
 }
 
@@ -52,7 +55,7 @@ __device__ __forceinline__ void rmsnorm_write(const RmsnormArgs &a, int64_t row,
 }
 
 // One row in registers: VPT eights per thread.  8192 x 8192 with a bf16 residual,
-// codes out: 75.2 us, 96 % of the copy rate; 4000 x 3000 with an fp32 stream: 24.3
+// codes out: 75.3 us, 96 % of the copy rate; 4000 x 3000 with an fp32 stream: 24.1
 // us, 91 %; one row of 8192: 2.8 us, all of it launch and two trips to memory.
 template <int XT, int HT, int VPT>
 __global__ void __launch_bounds__(VPT == 1 ? 1024 : 512) rmsnorm_kernel(RmsnormArgs a) {
@@ -97,7 +100,7 @@ __global__ void __launch_bounds__(VPT == 1 ? 1024 : 512) rmsnorm_kernel(RmsnormA
     for (int i = 0; i < VPT; ++i)
 #pragma unroll
         for (int j = 0; j < 8; ++j) s += v[i][j] * v[i][j];
-    s = row_sum(s, red, 0);
+    s = row_sum<false>(s, red, 0);
     const float rstd = 1.0f / sqrtf(s / static_cast<float>(a.K) + a.eps);
     if (a.rstd && threadIdx.x == 0) a.rstd[row] = rstd;
 #pragma unroll
@@ -144,7 +147,7 @@ __global__ void __launch_bounds__(1024) rmsnorm_long_kernel(RmsnormArgs a) {
         for (int j = 0; j < 8; ++j) p += v[j] * v[j];
         s += p;
     }
-    s = row_sum(s, red, 0);
+    s = row_sum<false>(s, red, 0);
     const float rstd = 1.0f / sqrtf(s / static_cast<float>(a.K) + a.eps);
     if (a.rstd && threadIdx.x == 0) a.rstd[row] = rstd;
     for (int64_t i = 0; i < steps; ++i) {
@@ -235,10 +238,10 @@ constexpr int back_pieces(bool stage_dr) {
 // The next rows are on their way into shared memory while one is summed and
 // written (the barrier in the middle of each row would leave memory idle
 // otherwise), and what a row's second half needs is read from there again,
-// which keeps registers free.  8192 x 8192 bf16 with a residual's gradient: 95.2 us,
+// which keeps registers free.  8192 x 8192 bf16 with a residual's gradient: 95.8 us,
 // 86 % of the copy rate (a barrier and ten shuffles per row are what is left, with
-// one block of 16 warps per SM); 4000 x 3000 fp32: 32.3 us, 79 %; 1000 x 2000
-// bf16: 8.4 us, two launches and few rows per block.
+// one block of 16 warps per SM); 4000 x 3000 fp32: 33.4 us, 77 %; 1000 x 2000
+// bf16: 8.2 us, two launches and seven rows per block.
 template <int YT, int HT, int DT, int VPT>
 __global__ void __launch_bounds__(512) rmsnorm_back_kernel(RmsnormBackArgs a) {
     constexpr bool SPLIT = YT == kF32 || HT == kF32 || DT == kF32;
@@ -319,7 +322,7 @@ __global__ void __launch_bounds__(512) rmsnorm_back_kernel(RmsnormBackArgs a) {
                 s += p * w[i][j];
             }
         }
-        s = row_sum(s, red[threadIdx.y], phase);
+        s = row_sum<true>(s, red[threadIdx.y], phase);
         phase ^= 1;
         // n mean(g n) = h c with c = rstd^2 sum(dy h w) / K
         const float c = rstd * rstd * (s * a.inv_k);
@@ -415,7 +418,7 @@ __global__ void __launch_bounds__(1024) rmsnorm_back_long_kernel(RmsnormBackArgs
             for (int j = 0; j < 8; ++j) p += y[j] * w[j] * (v[j] * rstd);
             s += p;
         }
-        s = row_sum(s, red, phase);
+        s = row_sum<false>(s, red, phase);
         phase ^= 1;
         const float mean = s / static_cast<float>(a.K);
         for (int64_t i = 0; i < steps; ++i) {
