@@ -260,9 +260,10 @@ bool overlaps(const void *p, int64_t rows, int64_t cols, int64_t ld, int64_t esi
     return a0 < b1 && b0 < a1;
 }
 
-bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
+using b200::host::aligned16;
+using b200::host::extent_ok;
 using b200::host::kMaxDim;
+using b200::host::pitch16;
 
 // Checks shared by every entry point.  elem sizes in bytes; a_mn / b_mn:
 // A stored K x M, B stored K x N (else M x K and N x K).
@@ -274,20 +275,21 @@ gemm_status_t check_args(const void *A, const void *B, const void *C, int64_t M,
     if (M == 0 || N == 0) return GEMM_OK;
     if (!C) return GEMM_ERR_INVALID_VALUE;
     if (ldc < N) return GEMM_ERR_INVALID_VALUE;
+    const bool c_ok = extent_ok(M, ldc, ec);   // C's byte range is only formed where it does not wrap
     if (K > 0) {
         const int64_t a_rows = a_mn ? K : M, a_cols = a_mn ? M : K;
         const int64_t b_rows = b_mn ? K : N, b_cols = b_mn ? N : K;
         if (!A || !B) return GEMM_ERR_INVALID_VALUE;
         if (lda < a_cols || ldb < b_cols) return GEMM_ERR_INVALID_VALUE;
         if (!aligned16(A) || !aligned16(B)) return GEMM_ERR_MISALIGNED;
-        if ((lda * ea) % 16 || (ldb * eb) % 16) return GEMM_ERR_MISALIGNED;
-        if (lda * ea >= (int64_t(1) << 40) || ldb * eb >= (int64_t(1) << 40)) return GEMM_ERR_TOO_LARGE;
-        if (overlaps(C, M, N, ldc, ec, A, a_rows, a_cols, lda, ea) ||
-            overlaps(C, M, N, ldc, ec, B, b_rows, b_cols, ldb, eb))
+        if (!pitch16(lda, ea) || !pitch16(ldb, eb)) return GEMM_ERR_MISALIGNED;
+        if (!extent_ok(a_rows, lda, ea) || !extent_ok(b_rows, ldb, eb)) return GEMM_ERR_TOO_LARGE;
+        if (c_ok && (overlaps(C, M, N, ldc, ec, A, a_rows, a_cols, lda, ea) ||
+                     overlaps(C, M, N, ldc, ec, B, b_rows, b_cols, ldb, eb)))
             return GEMM_ERR_ALIAS;
     }
-    if (!aligned16(C) || (ldc * ec) % 16) return GEMM_ERR_MISALIGNED;
-    if (ldc * ec >= (int64_t(1) << 40)) return GEMM_ERR_TOO_LARGE;
+    if (!aligned16(C) || !pitch16(ldc, ec)) return GEMM_ERR_MISALIGNED;
+    if (!c_ok) return GEMM_ERR_TOO_LARGE;
     return GEMM_OK;
 }
 
@@ -1180,8 +1182,11 @@ gemm_status_t gemm_bf16_allgather(const void *A, const void *B, void *const *C_d
     for (int d = 0; d < n_dst; ++d) {
         if (!C_dst[d]) return GEMM_ERR_INVALID_VALUE;
         if (!aligned16(C_dst[d])) return GEMM_ERR_MISALIGNED;
-        slab[d] = static_cast<uint8_t *>(C_dst[d]) + row0 * ldc * ec;
+        // (a slab that no address space holds is taken as its C's first rows here, and refused below)
+        const bool slab_ok = M >= 0 && ldc >= 0 && extent_ok(row0 + M, ldc, ec);
+        slab[d] = static_cast<uint8_t *>(C_dst[d]) + (slab_ok ? row0 * ldc * ec : 0);
         if ((s = check_args(A, B, slab[d], M, N, K, lda, ldb, ldc, 2, 2, ec)) != GEMM_OK) return s;
+        if (M > 0 && N > 0 && !slab_ok) return GEMM_ERR_TOO_LARGE;
         for (int e = 0; e < d; ++e)   // two destinations may not share bytes of the slab
             if (overlaps(slab[d], M, N, ldc, ec, slab[e], M, N, ldc, ec)) return GEMM_ERR_ALIAS;
     }

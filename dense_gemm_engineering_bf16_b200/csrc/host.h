@@ -33,6 +33,20 @@ bool overlaps(const void *p, int64_t rows, int64_t cols, int64_t ld, int64_t esi
 
 inline bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
+// Whether a pitch of ld >= 0 elements is a multiple of 16 bytes.  The product
+// ld * esize may not be formed before extent_ok has bounded ld: it wraps for
+// pitches near 2^62 elements.
+inline bool pitch16(int64_t ld, int64_t esize) { return (ld % 16) * esize % 16 == 0; }
+
+// Whether a matrix of `rows` rows with pitch ld keeps within the limits that
+// every offset is computed under: a pitch below 2^40 bytes (the tensor maps'
+// limit), and at most 2^62 bytes from the first row to the last (far above any
+// address space), so that no byte offset wraps, here or in a kernel.
+inline bool extent_ok(int64_t rows, int64_t ld, int64_t esize) {
+    if (ld >= (int64_t(1) << 40) / esize) return false;
+    return rows <= 1 || ld == 0 || rows <= (int64_t(1) << 62) / (ld * esize);
+}
+
 // One-time set-up of a kernel on a device: loads it (lazy loading may not
 // happen inside a stream capture) and raises its dynamic shared memory limit.
 // `Kernel` gives each kernel flags of its own, one bit per device.

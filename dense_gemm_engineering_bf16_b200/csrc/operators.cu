@@ -20,8 +20,10 @@ using b200::kBF16;
 using b200::kF32;
 using b200::kNone;
 using b200::host::aligned16;
+using b200::host::extent_ok;
 using b200::host::kMaxDim;
 using b200::host::overlaps;
+using b200::host::pitch16;
 
 bool valid_type(gemm_out_t t) { return t == GEMM_OUT_F32 || t == GEMM_OUT_BF16; }
 int64_t size_of(gemm_out_t t) { return t == GEMM_OUT_F32 ? 4 : 2; }
@@ -32,11 +34,11 @@ struct Mat {
     int64_t rows, cols, ld, esize;
 };
 
-// Pointer, pitch and alignment of a matrix that the call touches.
+// Pointer, pitch, alignment and extent of a matrix that the call touches.
 gemm_status_t check_mat(const Mat &m) {
     if (!m.p || m.ld < m.cols) return GEMM_ERR_INVALID_VALUE;
-    if (!aligned16(m.p) || (m.ld * m.esize) % 16) return GEMM_ERR_MISALIGNED;
-    if (m.ld * m.esize >= (int64_t(1) << 40)) return GEMM_ERR_TOO_LARGE;
+    if (!aligned16(m.p) || !pitch16(m.ld, m.esize)) return GEMM_ERR_MISALIGNED;
+    if (!extent_ok(m.rows, m.ld, m.esize)) return GEMM_ERR_TOO_LARGE;
     return GEMM_OK;
 }
 

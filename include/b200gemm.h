@@ -75,7 +75,8 @@ typedef enum {
     GEMM_ERR_UNSUPPORTED_DEVICE = 4,/* no device, or not compute capability 10.0 */
     GEMM_ERR_LAUNCH = 5,            /* a CUDA runtime call failed (see gemm_last_cuda_error) */
     GEMM_ERR_TIMEOUT = 6,           /* a kernel's bounded wait expired (device watchdog) */
-    GEMM_ERR_TOO_LARGE = 7,         /* a dimension exceeds 2^31-1 (TMA coordinates are int32) */
+    GEMM_ERR_TOO_LARGE = 7,         /* a dimension exceeds 2^31-1 (TMA coordinates are int32), a pitch reaches 2^40
+                                       bytes, or a matrix spans more than 2^62 bytes */
     GEMM_ERR_CAPTURE = 8            /* one-time set-up requested inside a stream capture (below) */
 } gemm_status_t;
 
