@@ -34,8 +34,9 @@ def _sources():
 
 
 def _deps():
-    return _sources() + sorted(glob.glob(os.path.join(CSRC, "*.cuh"))) + \
-        sorted(glob.glob(os.path.join(INCLUDE, "*.h")))
+    headers = [h for folder, kind in ((CSRC, "*.cuh"), (CSRC, "*.h"), (INCLUDE, "*.h"))
+               for h in sorted(glob.glob(os.path.join(folder, kind)))]
+    return _sources() + headers
 
 
 def needs_build() -> bool:
