@@ -324,8 +324,9 @@ __global__ void __launch_bounds__(512) rmsnorm_back_kernel(RmsnormBackArgs a) {
         }
         s = row_sum<true>(s, red[threadIdx.y], phase);
         phase ^= 1;
-        // n mean(g n) = h c with c = rstd^2 sum(dy h w) / K
-        const float c = rstd * rstd * (s * a.inv_k);
+        // n mean(g n) = h c with c = rstd^2 sum(dy h w) / K; rstd^2 alone may pass
+        // fp32's range (a row of zeros with a subnormal eps) where c does not
+        const float c = rstd * (rstd * (s * a.inv_k));
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
             const int e = e0 + 8 * i * static_cast<int>(blockDim.x);
