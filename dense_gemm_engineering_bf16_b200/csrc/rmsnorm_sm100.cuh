@@ -317,16 +317,17 @@ __global__ void __launch_bounds__(512) rmsnorm_back_kernel(RmsnormBackArgs a) {
             staged8<HT>(p + kY * pitch, pitch, v);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                const float p = y[j] * v[j];        // dy h: times rstd for dw, times w for the sum
-                dw[i][j] += p * rstd;
+                // n first: dy h may leave fp32's range where dy n does not
+                const float p = y[j] * (v[j] * rstd);
+                dw[i][j] += p;
                 s += p * w[i][j];
             }
         }
         s = row_sum<true>(s, red[threadIdx.y], phase);
         phase ^= 1;
-        // n mean(g n) = h c with c = rstd^2 sum(dy h w) / K; rstd^2 alone may pass
-        // fp32's range (a row of zeros with a subnormal eps) where c does not
-        const float c = rstd * (rstd * (s * a.inv_k));
+        // n mean(g n) = h c with c = rstd mean(g n): no rstd^2, which passes fp32's
+        // range in a row of zeros with a subnormal eps
+        const float c = rstd * (s * a.inv_k);
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
             const int e = e0 + 8 * i * static_cast<int>(blockDim.x);

@@ -50,3 +50,11 @@ def test_rows_of_zeros_under_a_subnormal_eps(M, K):
     h = normal(1, M, K) * 1e-3
     h[::2] = 0
     check(M, K, h, normal(2, M, K), 1e-39)
+
+
+@pytest.mark.parametrize("M,K", SIZES)
+@pytest.mark.parametrize("h_scale,dy_scale,eps", [(1e16, 1e23, 1e-5), (1e-18, 1e-22, 1e-38)])
+def test_products_of_the_gradient_and_the_row_out_of_range(M, K, h_scale, dy_scale, eps):
+    """dy h is above fp32's largest value, or among its subnormals, where dy (h
+    rstd) is neither."""
+    check(M, K, normal(3, M, K) * h_scale, normal(4, M, K) * dy_scale, eps)
