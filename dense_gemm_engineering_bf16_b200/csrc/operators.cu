@@ -158,8 +158,9 @@ gemm_status_t launch_back(int dev, int sm_count, b200::RmsnormBackArgs a, dim3 b
     a.stage_dr = VPT < 4 || 2 * row_bytes(true) <= kSmemPerSm;
     if (VPT > 0) {
         const int64_t share = (a.M + sm_count - 1) / sm_count;      // rows per SM
-        block.y = static_cast<unsigned>(std::min<int64_t>({b200::kMaxRows, 512 / block.x, share,
-                                                           kSmemPerSm / (2 * row_bytes(a.stage_dr))}));
+        if (VPT < 4)    // with four eights per thread a row takes more than half of the threads
+            block.y = static_cast<unsigned>(std::min<int64_t>({b200::kMaxRows, 512 / block.x, share,
+                                                               kSmemPerSm / (2 * row_bytes(a.stage_dr))}));
         a.ring = std::min(4, kSmemPerSm / (row_bytes(a.stage_dr) * static_cast<int>(block.y)));
     }
     const int smem = a.ring * row_bytes(a.stage_dr) * static_cast<int>(block.y);

@@ -245,17 +245,20 @@ constexpr int back_pieces(bool stage_dr) {
 template <int YT, int HT, int DT, int VPT>
 __global__ void __launch_bounds__(512) rmsnorm_back_kernel(RmsnormBackArgs a) {
     constexpr bool SPLIT = YT == kF32 || HT == kF32 || DT == kF32;
-    __shared__ float red[kMaxRows][2][32];
+    // four eights per thread only where a row needs more than 256 threads
+    constexpr bool SHARED = VPT < 4;
+    __shared__ float red[SHARED ? kMaxRows : 1][2][32];
     wait_for_stream();
+    const unsigned sub = SHARED ? threadIdx.y : 0, subs = SHARED ? blockDim.y : 1;   // row of the block
     extern __shared__ __align__(16) uint8_t dyn[];
     constexpr int kY = YT == kF32 ? 2 : 1, kH = HT == kF32 ? 2 : 1, kD = DT == kF32 ? 2 : 1;
     const bool stage_dr = VPT < 4 || a.stage_dr;
     const int pieces = kY + kH + (stage_dr ? kD : 0);
-    const unsigned pitch = 16 * blockDim.x * blockDim.y;       // between a thread's pieces
+    const unsigned pitch = 16 * blockDim.x * subs;             // between a thread's pieces
     const unsigned row_pitch = VPT * pieces * pitch, ring_end = a.ring * row_pitch;
-    uint8_t *const mine = dyn + 16 * (threadIdx.y * blockDim.x + threadIdx.x);
-    const int64_t stride = static_cast<int64_t>(gridDim.x) * blockDim.y;
-    const int64_t first = static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y;
+    uint8_t *const mine = dyn + 16 * (sub * blockDim.x + threadIdx.x);
+    const int64_t stride = static_cast<int64_t>(gridDim.x) * subs;
+    const int64_t first = static_cast<int64_t>(blockIdx.x) * subs + sub;
     const int K = static_cast<int>(a.K);                       // at most 16384 here
     unsigned fill = 0;
     // the next row to load, and this thread's first vector of it
@@ -323,7 +326,7 @@ __global__ void __launch_bounds__(512) rmsnorm_back_kernel(RmsnormBackArgs a) {
                 s += p * w[i][j];
             }
         }
-        s = row_sum<true>(s, red[threadIdx.y], phase);
+        s = row_sum<SHARED>(s, red[sub], phase);
         phase ^= 1;
         // n mean(g n) = h c with c = rstd mean(g n): no rstd^2, which passes fp32's
         // range in a row of zeros with a subnormal eps
@@ -357,22 +360,22 @@ __global__ void __launch_bounds__(512) rmsnorm_back_kernel(RmsnormBackArgs a) {
     }
     asm volatile("cp.async.wait_group 0;" ::: "memory");
     if (!a.partial) return;
-    // the sums of a block's rows meet in shared memory and are added in threadIdx.y order
-    if (blockDim.y > 1) {
-        const int T = static_cast<int>(blockDim.x), sums = VPT * 8 * T, threads = T * static_cast<int>(blockDim.y);
+    // the sums of a block's rows meet in shared memory and are added in the rows' order
+    if (SHARED && subs > 1) {
+        const int T = static_cast<int>(blockDim.x), sums = VPT * 8 * T, threads = T * static_cast<int>(subs);
         float *acc = reinterpret_cast<float *>(dyn);
         __syncthreads();
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
-            const int at = threadIdx.y * sums + 8 * (i * T + static_cast<int>(threadIdx.x));
+            const int at = sub * sums + 8 * (i * T + static_cast<int>(threadIdx.x));
             float4 *d = reinterpret_cast<float4 *>(acc + at);
             d[0] = make_float4(dw[i][0], dw[i][1], dw[i][2], dw[i][3]);
             d[1] = make_float4(dw[i][4], dw[i][5], dw[i][6], dw[i][7]);
         }
         __syncthreads();
-        for (int at = static_cast<int>(threadIdx.y) * T + static_cast<int>(threadIdx.x); at < sums; at += threads) {
+        for (int at = static_cast<int>(sub) * T + static_cast<int>(threadIdx.x); at < sums; at += threads) {
             float v = 0.0f;
-            for (unsigned r = 0; r < blockDim.y; ++r) v += acc[r * sums + at];
+            for (unsigned r = 0; r < subs; ++r) v += acc[r * sums + at];
             const int64_t col = first8<SPLIT>(at / 8, 0, T) + at8<SPLIT>(at % 8);
             if (col < K) a.partial[static_cast<int64_t>(blockIdx.x) * a.K + col] = v;
         }
