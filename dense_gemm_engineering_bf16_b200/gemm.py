@@ -219,10 +219,11 @@ def _here(stream):
     return dev, _DTYPES["stream"](dev)
 
 
-def _operand(x, kind, dev, what: str):
+def _operand(x, kind, dev, what: str, packed: bool = False):
     """Device pointer of an operand: None, a raw pointer, or a tensor, which
     has to be on the current device (whose stream the call runs on) and to
-    hold the type that the call reads there."""
+    hold the type that the call reads there.  packed: the call has no pitch for
+    it (vectors, scales, a workspace), so the tensor must be contiguous."""
     if x is None or type(x) is int:
         return x
     if dev is None:
@@ -231,6 +232,8 @@ def _operand(x, kind, dev, what: str):
         raise GemmError(1, f"{what} is on {x.device}, the call runs on cuda:{dev}")
     if kind is not None and x.dtype not in _DTYPES.get(kind, ()):
         raise GemmError(1, f"{what} is {x.dtype}")
+    if packed and not x.is_contiguous():
+        raise GemmError(1, f"{what} is not contiguous")
     return x.data_ptr()
 
 
@@ -243,10 +246,10 @@ def gemm_rmsnorm(X, R, H, weight, Y, Q, sf, rstd, M: int, K: int, ldx: int, ldr:
     dev, queue = _here(stream)
     st = lib.gemm_rmsnorm(_operand(X, x_type, dev, "gemm_rmsnorm: X"), _operand(R, h_type, dev, "gemm_rmsnorm: R"),
                           _operand(H, h_type, dev, "gemm_rmsnorm: H"),
-                          _operand(weight, OUT_F32, dev, "gemm_rmsnorm: weight"),
+                          _operand(weight, OUT_F32, dev, "gemm_rmsnorm: weight", True),
                           _operand(Y, OUT_BF16, dev, "gemm_rmsnorm: Y"), _operand(Q, "codes", dev, "gemm_rmsnorm: Q"),
-                          _operand(sf, "scales", dev, "gemm_rmsnorm: sf"),
-                          _operand(rstd, OUT_F32, dev, "gemm_rmsnorm: rstd"), M, K, ldx, ldr, ldh, ldy, ldq,
+                          _operand(sf, "scales", dev, "gemm_rmsnorm: sf", True),
+                          _operand(rstd, OUT_F32, dev, "gemm_rmsnorm: rstd", True), M, K, ldx, ldr, ldh, ldy, ldq,
                           int(x_type), int(h_type), eps, queue)
     return _check(st, "gemm_rmsnorm", check)
 
@@ -269,12 +272,12 @@ def gemm_rmsnorm_backward(dY, H, weight, rstd, dR, dH, dW, workspace, M: int, K:
     dev, queue = _here(stream)
     st = lib.gemm_rmsnorm_backward(
         _operand(dY, dy_type, dev, "gemm_rmsnorm_backward: dY"), _operand(H, h_type, dev, "gemm_rmsnorm_backward: H"),
-        _operand(weight, OUT_F32, dev, "gemm_rmsnorm_backward: weight"),
-        _operand(rstd, OUT_F32, dev, "gemm_rmsnorm_backward: rstd"),
+        _operand(weight, OUT_F32, dev, "gemm_rmsnorm_backward: weight", True),
+        _operand(rstd, OUT_F32, dev, "gemm_rmsnorm_backward: rstd", True),
         _operand(dR, dh_type, dev, "gemm_rmsnorm_backward: dR"),
         _operand(dH, dh_type, dev, "gemm_rmsnorm_backward: dH"),
-        _operand(dW, OUT_F32, dev, "gemm_rmsnorm_backward: dW"),
-        _operand(workspace, None, dev, "gemm_rmsnorm_backward: workspace"), workspace_bytes, M, K, lddy, ldh, lddr,
+        _operand(dW, OUT_F32, dev, "gemm_rmsnorm_backward: dW", True),
+        _operand(workspace, None, dev, "gemm_rmsnorm_backward: workspace", True), workspace_bytes, M, K, lddy, ldh, lddr,
         lddh, int(dy_type), int(h_type), int(dh_type), queue)
     return _check(st, "gemm_rmsnorm_backward", check)
 
@@ -286,7 +289,7 @@ def gemm_mxfp8_quantize(X, Q, sf, M: int, K: int, ldx: int, ldq: int, x_type: in
     dev, queue = _here(stream)
     st = lib.gemm_mxfp8_quantize(_operand(X, x_type, dev, "gemm_mxfp8_quantize: X"),
                                  _operand(Q, "codes", dev, "gemm_mxfp8_quantize: Q"),
-                                 _operand(sf, "scales", dev, "gemm_mxfp8_quantize: sf"), M, K, ldx, ldq, int(x_type),
+                                 _operand(sf, "scales", dev, "gemm_mxfp8_quantize: sf", True), M, K, ldx, ldq, int(x_type),
                                  int(layout), queue)
     return _check(st, "gemm_mxfp8_quantize", check)
 
