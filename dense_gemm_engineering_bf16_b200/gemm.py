@@ -237,20 +237,32 @@ def _operand(x, kind, dev, what: str, packed: bool = False):
     return x.data_ptr()
 
 
+def _refused(e: GemmError, check: bool) -> int:
+    """An operand that `_operand` refused: raised, or with check=False returned
+    as its status, like the library's own refusals."""
+    if check:
+        raise e
+    return e.status
+
+
 def gemm_rmsnorm(X, R, H, weight, Y, Q, sf, rstd, M: int, K: int, ldx: int, ldr: int, ldh: int, ldy: int, ldq: int,
                  x_type: int = OUT_BF16, h_type: int = OUT_BF16, eps: float = 1e-5, stream=None,
                  check: bool = True) -> int:
     """h = X + R (stored to H), y = h / rms(h) * weight, written as bf16 to Y
     and / or as MXFP8 codes and scales to Q and sf; 1 / rms to rstd.  R, H, Y,
     Q with sf, and rstd may be None (see include/b200gemm.h, gemm_rmsnorm)."""
-    dev, queue = _here(stream)
-    st = lib.gemm_rmsnorm(_operand(X, x_type, dev, "gemm_rmsnorm: X"), _operand(R, h_type, dev, "gemm_rmsnorm: R"),
-                          _operand(H, h_type, dev, "gemm_rmsnorm: H"),
-                          _operand(weight, OUT_F32, dev, "gemm_rmsnorm: weight", True),
-                          _operand(Y, OUT_BF16, dev, "gemm_rmsnorm: Y"), _operand(Q, "codes", dev, "gemm_rmsnorm: Q"),
-                          _operand(sf, "scales", dev, "gemm_rmsnorm: sf", True),
-                          _operand(rstd, OUT_F32, dev, "gemm_rmsnorm: rstd", True), M, K, ldx, ldr, ldh, ldy, ldq,
-                          int(x_type), int(h_type), eps, queue)
+    try:
+        dev, queue = _here(stream)
+        st = lib.gemm_rmsnorm(_operand(X, x_type, dev, "gemm_rmsnorm: X"), _operand(R, h_type, dev, "gemm_rmsnorm: R"),
+                              _operand(H, h_type, dev, "gemm_rmsnorm: H"),
+                              _operand(weight, OUT_F32, dev, "gemm_rmsnorm: weight", True),
+                              _operand(Y, OUT_BF16, dev, "gemm_rmsnorm: Y"),
+                              _operand(Q, "codes", dev, "gemm_rmsnorm: Q"),
+                              _operand(sf, "scales", dev, "gemm_rmsnorm: sf", True),
+                              _operand(rstd, OUT_F32, dev, "gemm_rmsnorm: rstd", True), M, K, ldx, ldr, ldh, ldy, ldq,
+                              int(x_type), int(h_type), eps, queue)
+    except GemmError as e:
+        return _refused(e, check)
     return _check(st, "gemm_rmsnorm", check)
 
 
@@ -269,16 +281,20 @@ def gemm_rmsnorm_backward(dY, H, weight, rstd, dR, dH, dW, workspace, M: int, K:
     if workspace_bytes is None:
         workspace_bytes = 0 if workspace is None or isinstance(workspace, int) else \
             workspace.numel() * workspace.element_size()
-    dev, queue = _here(stream)
-    st = lib.gemm_rmsnorm_backward(
-        _operand(dY, dy_type, dev, "gemm_rmsnorm_backward: dY"), _operand(H, h_type, dev, "gemm_rmsnorm_backward: H"),
-        _operand(weight, OUT_F32, dev, "gemm_rmsnorm_backward: weight", True),
-        _operand(rstd, OUT_F32, dev, "gemm_rmsnorm_backward: rstd", True),
-        _operand(dR, dh_type, dev, "gemm_rmsnorm_backward: dR"),
-        _operand(dH, dh_type, dev, "gemm_rmsnorm_backward: dH"),
-        _operand(dW, OUT_F32, dev, "gemm_rmsnorm_backward: dW", True),
-        _operand(workspace, None, dev, "gemm_rmsnorm_backward: workspace", True), workspace_bytes, M, K, lddy, ldh, lddr,
-        lddh, int(dy_type), int(h_type), int(dh_type), queue)
+    try:
+        dev, queue = _here(stream)
+        st = lib.gemm_rmsnorm_backward(
+            _operand(dY, dy_type, dev, "gemm_rmsnorm_backward: dY"),
+            _operand(H, h_type, dev, "gemm_rmsnorm_backward: H"),
+            _operand(weight, OUT_F32, dev, "gemm_rmsnorm_backward: weight", True),
+            _operand(rstd, OUT_F32, dev, "gemm_rmsnorm_backward: rstd", True),
+            _operand(dR, dh_type, dev, "gemm_rmsnorm_backward: dR"),
+            _operand(dH, dh_type, dev, "gemm_rmsnorm_backward: dH"),
+            _operand(dW, OUT_F32, dev, "gemm_rmsnorm_backward: dW", True),
+            _operand(workspace, None, dev, "gemm_rmsnorm_backward: workspace", True), workspace_bytes, M, K, lddy, ldh,
+            lddr, lddh, int(dy_type), int(h_type), int(dh_type), queue)
+    except GemmError as e:
+        return _refused(e, check)
     return _check(st, "gemm_rmsnorm_backward", check)
 
 
@@ -286,11 +302,14 @@ def gemm_mxfp8_quantize(X, Q, sf, M: int, K: int, ldx: int, ldq: int, x_type: in
                         stream=None, check: bool = True) -> int:
     """E4M3 codes Q (M x ldq) and E8M0 scales sf (M x K/32) of X, stored M x K
     (KMAJOR) or K x M (MNMAJOR): an operand of gemm_mxfp8."""
-    dev, queue = _here(stream)
-    st = lib.gemm_mxfp8_quantize(_operand(X, x_type, dev, "gemm_mxfp8_quantize: X"),
-                                 _operand(Q, "codes", dev, "gemm_mxfp8_quantize: Q"),
-                                 _operand(sf, "scales", dev, "gemm_mxfp8_quantize: sf", True), M, K, ldx, ldq, int(x_type),
-                                 int(layout), queue)
+    try:
+        dev, queue = _here(stream)
+        st = lib.gemm_mxfp8_quantize(_operand(X, x_type, dev, "gemm_mxfp8_quantize: X"),
+                                     _operand(Q, "codes", dev, "gemm_mxfp8_quantize: Q"),
+                                     _operand(sf, "scales", dev, "gemm_mxfp8_quantize: sf", True), M, K, ldx, ldq,
+                                     int(x_type), int(layout), queue)
+    except GemmError as e:
+        return _refused(e, check)
     return _check(st, "gemm_mxfp8_quantize", check)
 
 
@@ -299,12 +318,16 @@ def gemm_bf16_w4(A, B, scales, zeros, C, M: int, N: int, K: int, lda: int, ldb: 
     """C = A.W^T with W[j][k] = scales[j][k/group] (q[j][k] - zeros[j][k/group]):
     bf16 A (M x K), 4-bit codes B (N x ldb bytes, two each, even k in the low
     half), bf16 scales and byte zeros (N x lds; zeros None: 8), C M x N."""
-    dev, queue = _here(stream)
-    st = lib.gemm_bf16_w4(_operand(A, OUT_BF16, dev, "gemm_bf16_w4: A"), _operand(B, "bytes", dev, "gemm_bf16_w4: B"),
-                          _operand(scales, OUT_BF16, dev, "gemm_bf16_w4: scales"),
-                          _operand(zeros, "bytes", dev, "gemm_bf16_w4: zeros"),
-                          _operand(C, c_type, dev, "gemm_bf16_w4: C"), M, N, K, lda, ldb, lds, ldc, group,
-                          int(c_type), queue)
+    try:
+        dev, queue = _here(stream)
+        st = lib.gemm_bf16_w4(_operand(A, OUT_BF16, dev, "gemm_bf16_w4: A"),
+                              _operand(B, "bytes", dev, "gemm_bf16_w4: B"),
+                              _operand(scales, OUT_BF16, dev, "gemm_bf16_w4: scales"),
+                              _operand(zeros, "bytes", dev, "gemm_bf16_w4: zeros"),
+                              _operand(C, c_type, dev, "gemm_bf16_w4: C"), M, N, K, lda, ldb, lds, ldc, group,
+                              int(c_type), queue)
+    except GemmError as e:
+        return _refused(e, check)
     return _check(st, "gemm_bf16_w4", check)
 
 

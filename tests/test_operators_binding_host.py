@@ -78,3 +78,15 @@ def test_a_matrix_with_a_pitch_may_be_a_slice():
     with pytest.raises(G.GemmError) as e:
         G.gemm_mxfp8_quantize(o["x"], o["q"], o["sf"], M, K, 2 * K, K)
     assert e.value.status == 4
+
+
+@pytest.mark.parametrize("name,what,bad", [
+    ("norm", "x", torch.float16), ("back", "ws", None), ("quantize", "q", torch.bfloat16), ("w4", "c", torch.bfloat16)])
+def test_without_check_a_refused_operand_is_a_status(name, what, bad):
+    """As for the library's own refusals: check=False returns the status."""
+    o = operands()
+    assert CALLS[name](o, check=False) == 4
+    o[what] = torch.zeros(*o[what].shape, 2, dtype=o[what].dtype)[..., 0] if bad is None else o[what].to(bad)
+    assert CALLS[name](o, check=False) == 1
+    with pytest.raises(G.GemmError):
+        CALLS[name](o)
