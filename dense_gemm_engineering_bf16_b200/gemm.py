@@ -207,16 +207,29 @@ _DTYPES: dict = {}
 def _here(stream):
     """The current device (None: not asked for yet) and the call's stream
     handle.  Without a stream it is the device's current one, asked for
-    without building a Stream object, which would cost more than the launch."""
+    without building a Stream object, which would cost more than the launch;
+    where torch lacks those two functions its public ones answer."""
     if not _DTYPES:
         import torch
+        device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+        queue = getattr(torch._C, "_cuda_getCurrentRawStream",
+                        lambda dev: torch.cuda.current_stream(dev).cuda_stream)
         _DTYPES.update({OUT_F32: (torch.float32,), OUT_BF16: (torch.bfloat16,), "bytes": (torch.uint8,),
                         "codes": (torch.float8_e4m3fn, torch.uint8), "scales": (torch.float8_e8m0fnu, torch.uint8),
-                        "device": torch._C._cuda_getDevice, "stream": torch._C._cuda_getCurrentRawStream})
+                        "device": device, "stream": queue})
     if stream is not None:
         return None, _stream(stream)
-    dev = _DTYPES["device"]()
+    dev = _device()
     return dev, _DTYPES["stream"](dev)
+
+
+def _device() -> int:
+    """The current device; without CUDA, in the driver or in this torch, the
+    library's own status for that."""
+    try:
+        return _DTYPES["device"]()
+    except (AssertionError, RuntimeError) as e:
+        raise GemmError(4, str(e).split(".")[0]) from e
 
 
 def _operand(x, kind, dev, what: str, packed: bool = False):
@@ -227,7 +240,7 @@ def _operand(x, kind, dev, what: str, packed: bool = False):
     if x is None or type(x) is int:
         return x
     if dev is None:
-        dev = _DTYPES["device"]()
+        dev = _device()
     if x.get_device() != dev:
         raise GemmError(1, f"{what} is on {x.device}, the call runs on cuda:{dev}")
     if kind is not None and x.dtype not in _DTYPES.get(kind, ()):

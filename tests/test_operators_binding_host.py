@@ -90,3 +90,37 @@ def test_without_check_a_refused_operand_is_a_status(name, what, bad):
     assert CALLS[name](o, check=False) == 1
     with pytest.raises(G.GemmError):
         CALLS[name](o)
+
+
+def test_a_torch_without_the_private_functions(monkeypatch):
+    """The two functions that the binding asks for the current device and its
+    stream are torch's own; without them its public ones answer, and without
+    CUDA at all the status is the library's."""
+    for name in ("_cuda_getDevice", "_cuda_getCurrentRawStream"):
+        monkeypatch.delattr(torch._C, name)
+    monkeypatch.setattr(G, "_DTYPES", {})
+    asked = []
+
+    class Queue:
+        cuda_stream = 0
+
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: -1)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda dev: asked.append(dev) or Queue)
+    assert status("norm", operands())[0] == 4 and asked == [-1]
+
+    def no_cuda():
+        raise AssertionError("Torch not compiled with CUDA enabled")
+
+    monkeypatch.setattr(G, "_DTYPES", {})
+    monkeypatch.setattr(torch.cuda, "current_device", no_cuda)
+    for name in CALLS:
+        got, text = status(name, operands())
+        assert got == 4 and "Torch not compiled with CUDA enabled" in text
+        assert CALLS[name](operands(), check=False) == 4
+
+
+def test_no_driver_is_the_library_s_status(monkeypatch):
+    monkeypatch.setattr(G, "_DTYPES", {})
+    for name in CALLS:
+        got, text = status(name, operands())
+        assert got == 4 and "driver" in text
