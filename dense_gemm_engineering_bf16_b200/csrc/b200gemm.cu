@@ -118,7 +118,11 @@ typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t
                                   CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 EncodeTiledFn g_encode = nullptr;
 
+// Records a failed runtime call.  The runtime keeps its error for
+// cudaGetLastError as well, where the next launch of this library would find
+// it and report it as its own: it is taken from there.
 gemm_status_t cuda_fail(cudaError_t e) {
+    (void)cudaGetLastError();
     g_last_cuda_error = static_cast<int>(e);
     return GEMM_ERR_LAUNCH;
 }
@@ -201,7 +205,7 @@ bool capturing(cudaStream_t stream) {
 gemm_status_t current_device(int &dev, DeviceState *&st, cudaStream_t stream) {
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess || dev < 0 || dev >= kMaxDevices) {
-        g_last_cuda_error = static_cast<int>(e);
+        (void)cuda_fail(e);
         return GEMM_ERR_UNSUPPORTED_DEVICE;
     }
     std::lock_guard<std::mutex> lock(g_mutex);
@@ -211,6 +215,7 @@ gemm_status_t current_device(int &dev, DeviceState *&st, cudaStream_t stream) {
         int major = 0, minor = 0;
         if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
             cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess) {
+            (void)cudaGetLastError();
             return GEMM_ERR_UNSUPPORTED_DEVICE;
         }
         st->supported = (major == 10 && minor == 0);
