@@ -194,7 +194,6 @@ gemm_status_t dispatch_back(int dev, int sm_count, const b200::RmsnormBackArgs &
     const int64_t vecs = (a.K + 7) / 8;
     const auto block = [&](int vpt) { return dim3(static_cast<unsigned>(round_up((vecs + vpt - 1) / vpt, 32))); };
     if (vecs <= 32) return launch_back<YT, HT, DT, 1>(dev, sm_count, a, dim3(32), dw, ws, stream);
-    if (vecs <= 64) return launch_back<YT, HT, DT, 2>(dev, sm_count, a, dim3(32), dw, ws, stream);
     if (vecs <= 1024) return launch_back<YT, HT, DT, 2>(dev, sm_count, a, block(2), dw, ws, stream);
     if (vecs <= 2048 && 2 * 16 * b200::back_pieces<YT, HT, DT>(false) * 4 * block(4).x <= kSmemPerSm)
         return launch_back<YT, HT, DT, 4>(dev, sm_count, a, block(4), dw, ws, stream);
@@ -232,7 +231,8 @@ gemm_status_t launch_quantize(int dev, int sm_count, const void *X, uint8_t *Q, 
     // Four eights per thread; eight of bf16 where there are many rows: a block
     // then has as many bytes in flight as with fp32 (8192 x 8192 bf16: 32.1
     // against 35.6 us; 1000 x 8192: 4.9 against 4.7).
-    if (XT == kBF16 && M >= 16 * sm_count) return launch_quantize_rows<XT, 8>(dev, X, Q, sf, M, K, ldx, ldq, stream);
+    if constexpr (XT == kBF16)
+        if (M >= 16 * sm_count) return launch_quantize_rows<XT, 8>(dev, X, Q, sf, M, K, ldx, ldq, stream);
     return launch_quantize_rows<XT, 4>(dev, X, Q, sf, M, K, ldx, ldq, stream);
 }
 
