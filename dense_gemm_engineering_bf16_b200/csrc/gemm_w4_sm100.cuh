@@ -25,12 +25,24 @@
 // memory and are added in a fixed order: no workspace, and the same result
 // every time.
 //
-// What bounds it: at 1 x 8192 x 8192 the copies alone take 8.1 us (5.3 is the
-// bytes' floor, the rest start and end), with the arithmetic 13.0; at 16 rows
-// 17.0.  Per 16 x 32 weights a warp issues 53 instructions, 20 of them bit
-// operations, which run at half rate, and an MMA takes some 6 of its 8 cycles
-// from them (measured: 8 multiply-adds and 8 bit operations 16.3 cycles, with an
-// MMA 22.7).  Each further 8 rows of a batch cost 4 to 5 us at this size.
+// What bounds it: the steps from codes to sums, as far as the copies do not hide
+// them.  At 1 x 8192 x 8192 the copies alone take 8.1 us
+// (5.3 is the bytes' floor, the rest start and end), with the arithmetic 12.8
+// (13.3 with weights from memory rather than L2); at 16 rows 17.0 (17.2).  Per 16
+// x 32 weights of 16 rows a warp issues 53 instructions (counted by ncu, groups
+// of 128, zeros): 19 in the integer and bit pipe, ten of which unpack codes and
+// the rest address, select and permute; 18 multiply-adds; 8 loads and stores; 4
+// MMAs.  No pipe is near its rate (tensor 25 %, bits about as much): what is left is
+// latency, with 16 warps per SM and a block-wide barrier per stage.  Each
+// further 8 rows of a batch cost 2 to 6 us at this size: 25 us at 32, 42.5 at 64 with
+// groups of 128, where a bf16 copy of the weights through gemm_bf16 takes 33.
+//
+// Registers: at 9 to 32 rows the bound of 128 (two blocks per SM) spills up to 48
+// bytes, at 9 to 16 rows with groups of 64 only, at 17 to 32 rows with groups of 32,
+// 64 and 128; from 33 rows on (255) groups of 32 spill 40 to 84 bytes and groups of
+// 64, from 49 rows on, 100.  Groups of 256 and more spill nowhere.  16 x 8192 x 8192
+// with groups of 64 takes 19.8 us, of 32 19.3, of 128 17.0; 64 x 8192 x 8192 53.3,
+// 56.4 and 42.5.
 #pragma once
 #include <cuda_bf16.h>
 
@@ -72,9 +84,8 @@ __device__ __forceinline__ void w4_mma(float (&d)[4], const uint32_t (&a)[4], ui
 // the pair -z / 64.  The AND leaves q 16^I in each half, as a bf16 the
 // subnormal q 16^I 2^-133 (bf16 patterns below 0x0100 grow linearly through the
 // subnormals and the first binade), and one fused multiply-add by 2^127 or
-// 2^123 makes q / 64 - z / 64 of it, exactly.  Bit operations run at half the
-// rate of multiply-adds here and bound this kernel, so their number counts:
-// five per word (without the subnormals it takes seven).
+// 2^123 makes q / 64 - z / 64 of it, exactly.  Five bit operations per word;
+// without the subnormals it takes seven (16 x 8192 x 8192: 18.5 against 19.0 us).
 template <int I>
 __device__ __forceinline__ uint32_t w4_codes(uint32_t word, uint32_t minus) {
     uint32_t d;

@@ -8,8 +8,8 @@ namespace b200 {
 
 // X stored K-major (M rows of K): VPT eights per thread.  A row takes
 // blockDim.x threads in each of `parts` blocks; short rows share a block
-// (blockDim.y).  8192 x 8192: 32.1 us from bf16 (97 % of the copy rate), 50.7 from
-// fp32; 1000 x 8192 bf16: 4.9 us, which is L2's rate and the launch.
+// (blockDim.y).  8192 x 8192: 34.2 us from bf16 (91 % of the copy rate), 50.9 from
+// fp32 (101 %); 1000 x 8192 bf16: 5.0 us, which is L2's rate and the launch.
 template <int XT, int VPT>
 __global__ void __launch_bounds__(256) mx_quantize_kernel(const void *x, uint8_t *q, uint8_t *sf, int64_t M, int64_t K,
                                                           int64_t ldx, int64_t ldq, unsigned parts) {
@@ -40,7 +40,8 @@ __global__ void __launch_bounds__(256) mx_quantize_kernel(const void *x, uint8_t
 // together.  Neighbouring blocks read neighbouring pieces of the same rows of X.
 // 8192 x 8192 bf16: 33.1 us, 94 % of the copy rate (35.0 with neighbours along K;
 // written straight from the lanes, 32 bytes of a row each and single scale
-// bytes, 58); the registers are held to seven blocks per SM (eight spill: 43.1).
+// bytes, 58); the registers are held to seven blocks per SM (72, with 12 bytes
+// spilled; eight blocks spill more: 43.1).  From fp32, five blocks: 50.8 us, 101 %.
 template <int XT>
 __global__ void __launch_bounds__(128, XT == kF32 ? 5 : 7) mx_quantize_mn_kernel(const void *x, uint8_t *q, uint8_t *sf, int64_t M,
                                                              int64_t K, int64_t ldx, int64_t ldq, unsigned i_tiles) {

@@ -93,9 +93,13 @@ int round_up(int64_t n, int m) { return static_cast<int>((n + m - 1) / m * m); }
 // row, and eight rows share a block.  Longer rows take a block each: with
 // fewer rows than would fill the SMs, one eight per thread (the shortest chain
 // of loads); else four of bf16 or, with an fp32 operand, two, about the same
-// bytes in flight (8192 x 8192 bf16: 75.8 us with four, 79.6 with two; 4000 x
-// 3000 with an fp32 stream: 26.3 and 24.9).  VPT 0: the row does not fit into
-// registers.
+// bytes in flight.  Measured with four and with two, 4000 rows, bf16 out: fp32
+// stream 12.7 and 11.3 us at 1100 elements, 25.7 and 24.2 at 3000, 61.8 and 59.8 at
+// 8192; bf16 without a stream 7.2 and 5.9 at 1120, 12.9 and 12.7 at 3008, 21.5 and
+// 23.0 at 6016, 26.7 and 30.3 at 8192; bf16 stream 10.7 and 8.6, 19.2 and 17.9, 33.4
+// and 31.7, 42.8 and 41.6, but 75.2 and 79.4 with codes out at 8192 x 8192: for bf16
+// four is the better one of long rows, and gives up to 20 % away on short ones.
+// VPT 0: the row does not fit into registers.
 struct RowShape {
     int vpt;
     dim3 block;
@@ -142,7 +146,9 @@ gemm_status_t dispatch_norm_h(int dev, int sm_count, const b200::RmsnormArgs &a,
                       : dispatch_norm<XT, kBF16>(dev, sm_count, a, stream);
 }
 
-// Blocks of the backward pass, at most: the rows of its workspace (two per SM).
+// Rows of the backward pass's workspace, and so its blocks at most: a documented
+// size that does not depend on the device.  A launch has one block per SM, 148 on
+// this one.
 constexpr int64_t kPartialRows = 296;
 static_assert(kPartialRows <= 320, "rmsnorm_dw_kernel adds up to 320 shares");
 
@@ -185,9 +191,11 @@ gemm_status_t launch_back(int dev, int sm_count, b200::RmsnormBackArgs a, dim3 b
 }
 
 // One eight per thread up to 256 elements (a warp), two as far as 512 threads
-// go, then four: what a thread does once per row (addresses, the sum across the
-// warps) is spread over more elements than with one (8000 x 1000 bf16: 18.7 us with
-// two, 25.7 with one, 23.3 with four in one warp).
+// go (8192 elements), then four, as far as 512 threads go and shared memory holds
+// two rows of dy and h (16384 elements; 13312 with both in fp32); past that two
+// passes per row.  More than one eight spreads what a thread does once per row
+// (addresses, the sum across the warps) over more elements (8000 x 1000 bf16: 18.9
+// us with two, 25.7 with one, 23.3 with four in one warp).
 template <int YT, int HT, int DT>
 gemm_status_t dispatch_back(int dev, int sm_count, const b200::RmsnormBackArgs &a, float *dw, float *ws,
                             cudaStream_t stream) {
@@ -229,7 +237,7 @@ gemm_status_t launch_quantize(int dev, int sm_count, const void *X, uint8_t *Q, 
                       Q, sf, M, K, ldx, ldq, i_tiles);
     }
     // Four eights per thread; eight of bf16 where there are many rows: a block
-    // then has as many bytes in flight as with fp32 (8192 x 8192 bf16: 32.1
+    // then has as many bytes in flight as with fp32 (8192 x 8192 bf16: 34.2
     // against 35.6 us; 1000 x 8192: 4.9 against 4.7).
     if constexpr (XT == kBF16)
         if (M >= 16 * sm_count) return launch_quantize_rows<XT, 8>(dev, X, Q, sf, M, K, ldx, ldq, stream);
@@ -473,9 +481,10 @@ gemm_status_t gemm_bf16_w4(const void *A, const uint8_t *B, const void *scales, 
     a.groups = groups;
     a.group_shift = shift;
     a.out = c_type == GEMM_OUT_F32 ? kF32 : kBF16;
-    // a kernel for each size of batch (its sums and activations stay in
-    // registers and shared memory); ring stages as shared memory allows with
-    // two blocks per SM, or one from 33 rows on
+    // A kernel for each size of batch: its sums stay in registers, its activations
+    // pass through shared memory.  Up to 32 rows two blocks share an SM, with as
+    // many ring stages as their shared memory allows; from 33 rows on the sums'
+    // registers leave room for one block, which takes about half of it.
     if (M <= 8) return dispatch_w4<b200::W4Cfg<1, 8, 4>>(dev, sm_count, a, stream);
     if (M <= 16) return dispatch_w4<b200::W4Cfg<2, 8, 3>>(dev, sm_count, a, stream);
     if (M <= 24) return dispatch_w4<b200::W4Cfg<3, 8, 3>>(dev, sm_count, a, stream);

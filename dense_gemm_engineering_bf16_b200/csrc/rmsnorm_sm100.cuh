@@ -8,8 +8,8 @@
 // Both are bound by memory: a row is read once, stays in registers between
 // the sum over it and its use, and is written once.  A row belongs to
 // blockDim.x threads (a multiple of 32), each holding one or more eights of
-// elements; short rows take one warp each, and
-// blockDim.y of them share a block.  All sums are fp32, in a fixed order.
+// elements; blockDim.y short rows share a block (one warp each in the forward
+// pass).  All sums are fp32, in a fixed order.
 #pragma once
 #include "rows.cuh"
 
@@ -55,8 +55,8 @@ __device__ __forceinline__ void rmsnorm_write(const RmsnormArgs &a, int64_t row,
 }
 
 // One row in registers: VPT eights per thread.  8192 x 8192 with a bf16 residual,
-// codes out: 75.3 us, 96 % of the copy rate; 4000 x 3000 with an fp32 stream: 24.1
-// us, 91 %; one row of 8192: 2.8 us, all of it launch and two trips to memory.
+// codes out: 75.3 us, 96 % of the copy rate; 4000 x 3000 with an fp32 stream: 24.3
+// us, 90 %; one row of 8192: 2.6 us, all of it launch and two trips to memory.
 template <int XT, int HT, int VPT>
 __global__ void __launch_bounds__(VPT == 1 ? 1024 : 512) rmsnorm_kernel(RmsnormArgs a) {
     constexpr bool SPLIT = XT == kF32 || HT == kF32;
@@ -111,8 +111,9 @@ __global__ void __launch_bounds__(VPT == 1 ? 1024 : 512) rmsnorm_kernel(RmsnormA
     }
 }
 
-// Rows too long for registers: a second pass reads them again (from L2, where
-// they fit).  It reads h where h was stored (r may be the same buffer, and
+// Rows too long for registers (past 16384 elements): a second pass reads them
+// again (from L2, where they fit; 2000 x 20000 bf16 with a residual: 68.8 us, 71 % of
+// the copy rate).  It reads h where h was stored (r may be the same buffer, and
 // then holds h by now: each thread reads back what it wrote itself).
 template <int XT, int HT>
 __global__ void __launch_bounds__(1024) rmsnorm_long_kernel(RmsnormArgs a) {
@@ -238,10 +239,12 @@ constexpr int back_pieces(bool stage_dr) {
 // The next rows are on their way into shared memory while one is summed and
 // written (the barrier in the middle of each row would leave memory idle
 // otherwise), and what a row's second half needs is read from there again,
-// which keeps registers free.  8192 x 8192 bf16 with a residual's gradient: 95.8 us,
-// 86 % of the copy rate (a barrier and ten shuffles per row are what is left, with
-// one block of 16 warps per SM); 4000 x 3000 fp32: 33.4 us, 77 %; 1000 x 2000
-// bf16: 8.2 us, two launches and seven rows per block.
+// which keeps registers free.  With a residual's gradient: 8192 x 8192 bf16 97.5
+// us, 84 % of the copy rate (a barrier and ten shuffles per row are what is left,
+// with one block of 16 warps per SM); 4000 x 3000 fp32 33.5 us, 77 %; with four
+// eights per thread, two rows in shared memory and 96 to 128 registers, 2000 x
+// 16384 bf16 63 us, 63 %, and 2000 x 12000 fp32 89 us, 66 %.  1000 x 2000 bf16
+// without one: 8.3 us, two launches and seven rows per block.
 template <int YT, int HT, int DT, int VPT>
 __global__ void __launch_bounds__(512) rmsnorm_back_kernel(RmsnormBackArgs a) {
     constexpr bool SPLIT = YT == kF32 || HT == kF32 || DT == kF32;
@@ -396,8 +399,12 @@ __global__ void __launch_bounds__(512) rmsnorm_back_kernel(RmsnormBackArgs a) {
     }
 }
 
-// Rows too long for registers: two passes over each row, and the block's share
-// of dw kept in `partial` itself (each thread owns its columns there).
+// Rows of which shared memory does not hold two (from 13313 elements on with dy
+// and h both fp32) or registers one (past 16384): two passes over each row, and the
+// block's share of dw kept in `partial` itself (each thread owns its columns
+// there), read and written once per row, which is what bounds it: with a
+// residual's gradient 2000 x 13320 fp32 150 us, 43 % of the copy rate (at 13312, on the
+// kernel above, 92 us), 2000 x 20000 bf16 255 us, 19 %.
 template <int YT, int HT, int DT>
 __global__ void __launch_bounds__(1024) rmsnorm_back_long_kernel(RmsnormBackArgs a) {
     constexpr bool SPLIT = YT == kF32 || HT == kF32 || DT == kF32;
@@ -450,7 +457,8 @@ __global__ void __launch_bounds__(1024) rmsnorm_back_long_kernel(RmsnormBackArgs
 
 // dw[k] = sum over the blocks' shares: 32 columns per block, each of its 32
 // warps adds every 32nd share, then warp w adds the 32 sums of column w: a fixed
-// order, and all of a warp's loads (at most ten) are in flight together.
+// order, and all of a warp's loads (at most ten; five of them for the 148 shares
+// of a device with 148 SMs) are in flight together.
 __global__ void __launch_bounds__(1024) rmsnorm_dw_kernel(const float *__restrict__ partial, float *dw, int rows,
                                                           int64_t K) {
     __shared__ float part[32][33];

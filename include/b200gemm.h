@@ -359,7 +359,8 @@ B200GEMM_API gemm_status_t gemm_bf16_noalloc(const void *A, const void *B, void 
  *   eps     > 0
  * At least one of Y and Q is given.  Outputs may not overlap one another nor
  * an input (H == R aside).  M == 0 or K == 0: nothing to do.  One kernel.
- * The sum of squares is fp32: a row whose squares pass 3.4e38 gives zeros.
+ * The sum of squares is fp32: a row whose squares pass 3.4e38 gives zeros (and
+ * rstd 0, with which the backward pass adds nothing).
  */
 B200GEMM_API gemm_status_t gemm_rmsnorm(const void *X, const void *R, void *H, const float *weight, void *Y, uint8_t *Q,
                                         uint8_t *sf, float *rstd, int64_t M, int64_t K, int64_t ldx, int64_t ldr,
@@ -433,10 +434,12 @@ B200GEMM_API gemm_status_t gemm_mxfp8_quantize(const void *X, uint8_t *Q, uint8_
  *   group   a power of two >= 32; from K on: one scale per row
  * K must be a multiple of 32, ldb (bytes) and lds of 16, lds >= ceil(K / group).
  * Products are exact, sums fp32 and in a fixed order, the result rounded once.
- * The kernel is built for M <= 64.  More rows (up to 64 * 65535, beyond that
- * GEMM_ERR_TOO_LARGE) are taken 64 at a time, each time over all weights, and
- * are bound by the warp-level tensor instruction: for long prompts, keep a
- * bf16 copy of the weights and use gemm_bf16.
+ * The kernel is built for few rows.  Up to 32 it is faster than gemm_bf16 on a
+ * bf16 copy of the weights (8192 x 8192, groups of 128, weights from memory: 13.3
+ * against 29.8 us at one row, 25 against 35 at 32), at 64 it is not (42.5 against
+ * 33).  More than 64 rows (up to 64 * 65535, beyond that GEMM_ERR_TOO_LARGE) are
+ * taken 64 at a time, each time over all weights: for long prompts, keep a bf16
+ * copy of the weights and use gemm_bf16.
  * C may not overlap an input.  M == 0 or N == 0: nothing to do; K == 0: C = 0.
  * One kernel.
  */
