@@ -300,14 +300,17 @@ gemm_status_t check_args(const void *A, const void *B, const void *C, int64_t M,
 
 // ------------------------------------------------------------ tensor maps --
 
-gemm_status_t encode_2d(CUtensorMap *map, CUtensorMapDataType dtype, const void *ptr, int64_t inner,
-                        int64_t outer, int64_t ld_bytes, uint32_t box_inner, uint32_t box_outer,
-                        CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B) {
-    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(inner), static_cast<cuuint64_t>(outer)};
-    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld_bytes)};
-    const cuuint32_t box[2] = {box_inner, box_outer};
-    const cuuint32_t estr[2] = {1, 1};
-    CUresult r = g_encode(map, dtype, 2, const_cast<void *>(ptr), dims, strides, box, estr,
+gemm_status_t encode_map(CUtensorMap *map, CUtensorMapDataType dtype, const void *ptr, int rank, const int64_t *dims,
+                         const int64_t *strides, const uint32_t *box, CUtensorMapSwizzle swizzle) {
+    cuuint64_t d[3], st[2];
+    cuuint32_t bx[3];
+    const cuuint32_t estr[3] = {1, 1, 1};
+    for (int i = 0; i < rank; ++i) {
+        d[i] = static_cast<cuuint64_t>(dims[i]);
+        bx[i] = box[i];
+        if (i > 0) st[i - 1] = static_cast<cuuint64_t>(strides[i - 1]);
+    }
+    CUresult r = g_encode(map, dtype, static_cast<cuuint32_t>(rank), const_cast<void *>(ptr), d, st, bx, estr,
                           CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
                           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS) {
@@ -315,6 +318,14 @@ gemm_status_t encode_2d(CUtensorMap *map, CUtensorMapDataType dtype, const void 
         return GEMM_ERR_LAUNCH;
     }
     return GEMM_OK;
+}
+
+gemm_status_t encode_2d(CUtensorMap *map, CUtensorMapDataType dtype, const void *ptr, int64_t inner,
+                        int64_t outer, int64_t ld_bytes, uint32_t box_inner, uint32_t box_outer,
+                        CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B) {
+    const int64_t dims[2] = {inner, outer};
+    const uint32_t box[2] = {box_inner, box_outer};
+    return encode_map(map, dtype, ptr, 2, dims, &ld_bytes, box, swizzle);
 }
 
 // --------------------------------------------------------------- launches --
@@ -1102,6 +1113,23 @@ gemm_status_t device(int &dev, int &sm_count, cudaStream_t stream) {
     const gemm_status_t s = current_device(dev, st, stream);
     if (s == GEMM_OK) sm_count = st->sm_count;
     return s;
+}
+
+gemm_status_t device_with_status(int &dev, int &sm_count, DeviceStatus *&status, cudaStream_t stream) {
+    DeviceState *st = nullptr;
+    const gemm_status_t s = current_device_alloc(dev, st, stream);
+    if (s == GEMM_OK) {
+        sm_count = st->sm_count;
+        status = st->status;
+    }
+    return s;
+}
+
+uint64_t watchdog_ns(int64_t K) { return ::watchdog_ns(K); }
+
+gemm_status_t encode_map(CUtensorMap *map, CUtensorMapDataType dtype, const void *ptr, int rank, const int64_t *dims,
+                         const int64_t *strides, const uint32_t *box, CUtensorMapSwizzle swizzle) {
+    return ::encode_map(map, dtype, ptr, rank, dims, strides, box, swizzle);
 }
 
 bool capturing(cudaStream_t stream) { return ::capturing(stream); }

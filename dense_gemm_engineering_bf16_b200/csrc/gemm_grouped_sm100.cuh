@@ -1,0 +1,409 @@
+// Products grouped by expert, on rows sorted by expert whose extents only the
+// device knows (ends[e]: where expert e's rows end):
+//
+//   rows       C[r] = A[r] . B_e            for the rows r of expert e
+//   gradient   dB_e = sum over its rows r of dC[r]^T A[r]   (+ beta dB_e)
+//
+// One persistent, warp-specialised kernel with two operands: P, whose index runs
+// along a row of the output and along the MMA's M (128 a CTA, TMEM lanes), and
+// Q, whose index runs along its columns and the MMA's N.  N is chosen per tile
+// in the instruction descriptor, in steps of 16 (32 for a pair of CTAs), so the
+// ragged side costs what it has: an expert with 300 rows is two tiles of 150
+// (160), one with three rows a tile of 16.
+//   rows       P = B_e (rows of N, K- or MN-major), Q = A, reduced over K
+//   gradient   P, Q = A, dC or the other way round, both MN-major, reduced over
+//              the expert's rows
+//
+// Warps of a CTA:
+//   0          TMA producer
+//   1          MMA issuer (of the pair's leader), owner of TMEM
+//   2          gradient only: an expert's last block of 64 rows ends inside rows
+//              of the next expert, which must not count, not even as 0 * NaN.
+//              Such a block's bytes arrive on a barrier of its own; this warp
+//              zeroes the foreign rows up to the MMA's next step of 16 in both
+//              operands and hands the block on.
+//   the rest   epilogue: TMEM to registers to global memory (columns_out.cuh),
+//              double-buffered against the next tile's MMAs
+//
+// Every CTA works out the tiles from `ends` itself: the numbers of tiles up to
+// each expert in shared memory, a binary search per tile.  Rows outside every
+// expert are neither computed nor written.
+#pragma once
+#include <cstdint>
+
+#include "columns_out.cuh"
+#include "gemm_bf16_sm100.cuh"
+#include "ptx.cuh"
+#include "rows.cuh"
+
+namespace b200 {
+
+constexpr int kMaxGroups = 1024;      // two words of shared memory each
+constexpr int kRoleFix = 6;           // watchdog codes of the gradient's second warp
+constexpr int kBarFix = 12;
+
+// What a kernel computes: rows of C, or an expert's gradient.
+enum : int { kGroupedRows = 0, kGroupedGrad = 1 };
+
+template <int MODE_, bool PMN_, int CG_, int BQ_, int STAGES_>
+struct GroupedCfg {
+    static constexpr int MODE = MODE_;
+    static constexpr bool PMN = PMN_ || MODE_ == kGroupedGrad;   // P stored MN-major
+    static constexpr bool QMN = MODE_ == kGroupedGrad;
+    static constexpr int CG = CG_;
+    static constexpr int BP_CTA = 128;               // P indexes (TMEM lanes) per CTA
+    static constexpr int BP = BP_CTA * CG;
+    static constexpr int BQ = BQ_;                   // largest Q extent of a tile
+    static constexpr int STAGES = STAGES_;
+    static constexpr int BK = 64;
+    static constexpr int N_STEP = 16 * CG;           // MMA N is a multiple of this
+    static constexpr int Q_CTA = BQ / CG;            // Q indexes this CTA loads at most
+    static constexpr int QBOX = QMN ? 64 : BQ >= 128 ? 32 : 16;   // Q indexes per TMA box
+    static constexpr int P_BYTES = BP_CTA * BK * 2;
+    static constexpr int Q_BYTES = Q_CTA * BK * 2;
+    static constexpr int STAGE_BYTES = P_BYTES + Q_BYTES;
+    static constexpr int EPI_WARPS = BQ >= 128 ? 8 : 4;
+    static constexpr int EPI0 = MODE == kGroupedGrad ? 3 : 2;    // first epilogue warp
+    static constexpr int THREADS = 32 * (EPI0 + EPI_WARPS);
+    // full[S], empty[S], fix[S] (gradient), tmem_full[2], tmem_empty[2]
+    static constexpr int NUM_BARS = (MODE == kGroupedGrad ? 3 : 2) * STAGES + 4;
+    static constexpr int BAR_OFF = STAGES * STAGE_BYTES;
+    static constexpr int TABLE_OFF = BAR_OFF + NUM_BARS * 8 + 16;    // + TMEM address, abort flag
+    static constexpr int TMEM_COLS = pow2_at_least(2 * BQ, 32);
+    static constexpr int smem_bytes(int groups) { return 1024 + TABLE_OFF + 8 * groups; }
+
+    static_assert(Q_CTA % QBOX == 0 && Q_BYTES % 1024 == 0, "whole boxes and swizzle atoms");
+    static_assert(BQ >= 32 && BQ <= 256, "the epilogue reads 32 columns at a time");
+    static_assert(smem_bytes(kMaxGroups) <= 232448, "dynamic shared memory per CTA on sm_100");
+};
+
+struct GroupedArgs {
+    const int32_t *ends;
+    void *out;
+    int64_t ld, out_stride;     // of the output; gradient: between experts
+    int groups, M;              // rows of A and of dC
+    int P, Q, K;                // P's extent (columns of the output); gradient: Q's (its rows); rows: K
+    float beta;                 // gradient
+    bool f32;                   // type of the output
+    DeviceStatus *status;
+    uint64_t timeout_ns;
+};
+
+// One tile: P indexes from p0, Q indexes [q0, q0 + count) (rows: of A and C;
+// gradient: rows of the output), `n` the MMA's N, reduction from k0 over k_len.
+struct GroupedTile {
+    int group, p0, q0, count, n, k0, k_len;
+};
+
+template <class Cfg>
+__device__ __forceinline__ GroupedTile grouped_tile(int tile, const GroupedArgs &a, const int *ends, const int *tiles) {
+    GroupedTile t;
+    int local, extent;
+    if constexpr (Cfg::MODE == kGroupedRows) {
+        int lo = 0, hi = a.groups - 1;      // the first group whose tiles reach past `tile`
+        while (lo < hi) {
+            const int mid = (lo + hi) / 2;
+            if (tiles[mid] > tile) hi = mid;
+            else lo = mid + 1;
+        }
+        t.group = lo;
+        local = tile - (lo ? tiles[lo - 1] : 0);
+        t.q0 = lo ? ends[lo - 1] : 0;
+        extent = ends[lo] - t.q0;
+        t.k0 = 0;
+        t.k_len = a.K;
+    } else {
+        const int per = ((a.P + Cfg::BP - 1) / Cfg::BP) * ((a.Q + Cfg::BQ - 1) / Cfg::BQ);
+        t.group = tile / per;
+        local = tile - t.group * per;
+        t.q0 = 0;
+        extent = a.Q;
+        t.k0 = t.group ? ends[t.group - 1] : 0;
+        t.k_len = max(ends[t.group] - t.k0, 0);
+    }
+    // Q in tiles of one size (the last may be smaller), in bands of eight so
+    // that clusters running at the same time share both operands in L2
+    const int tiles_p = (a.P + Cfg::BP - 1) / Cfg::BP, tiles_q = (extent + Cfg::BQ - 1) / Cfg::BQ;
+    const int width = ((extent + tiles_q - 1) / tiles_q + Cfg::N_STEP - 1) / Cfg::N_STEP * Cfg::N_STEP;
+    int tq, tp;
+    raster_tile(local, tiles_q, tiles_p, 8, tq, tp);
+    t.p0 = tp * Cfg::BP;
+    t.q0 += tq * width;
+    t.count = min(width, extent - tq * width);
+    t.n = (t.count + Cfg::N_STEP - 1) / Cfg::N_STEP * Cfg::N_STEP;
+    return t;
+}
+
+template <class Cfg>
+__global__ void __launch_bounds__(Cfg::THREADS, 1)
+gemm_grouped_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ CUtensorMap tmQ, GroupedArgs a) {
+    constexpr int CG = Cfg::CG, STAGES = Cfg::STAGES;
+    constexpr bool GRAD = Cfg::MODE == kGroupedGrad;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = smem_addr(smem_raw);
+    uint8_t *smem = smem_raw + ((1024u - (raw & 1023u)) & 1023u);
+    const uint32_t base = smem_addr(smem);
+    const uint32_t warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const uint32_t rank = CG == 2 ? cluster_cta_rank() : 0u;
+
+    const uint32_t bar0 = base + Cfg::BAR_OFF;
+    auto full_bar = [&](uint32_t s) { return bar0 + 8u * s; };
+    auto empty_bar = [&](uint32_t s) { return bar0 + 8u * (STAGES + s); };
+    auto tfull_bar = [&](uint32_t b) { return bar0 + 8u * (2 * STAGES + b); };
+    auto tempty_bar = [&](uint32_t b) { return bar0 + 8u * (2 * STAGES + 2 + b); };
+    auto fix_bar = [&](uint32_t s) { return bar0 + 8u * (2 * STAGES + 4 + s); };
+    const uint32_t tmem_slot = bar0 + 8u * Cfg::NUM_BARS, abort_slot = tmem_slot + 4u;
+    volatile uint32_t *tmem_slot_ptr = reinterpret_cast<volatile uint32_t *>(smem + Cfg::BAR_OFF + 8 * Cfg::NUM_BARS);
+    volatile uint32_t *abort_flag = tmem_slot_ptr + 1;
+    int *ends = reinterpret_cast<int *>(smem + Cfg::TABLE_OFF), *tiles = ends + a.groups;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < STAGES; ++s) {
+            // gradient: each CTA of the pair says that its part of a block is there
+            mbar_init(full_bar(s), GRAD ? CG : 1);
+            mbar_init(empty_bar(s), 1);
+            if (GRAD) mbar_init(fix_bar(s), 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(tfull_bar(b), 1);
+            mbar_init(tempty_bar(b), Cfg::EPI_WARPS * CG);
+        }
+        *abort_flag = 0u;
+        fence_barrier_init();
+    }
+    if (warp == 1) {
+        tmem_alloc<CG>(tmem_slot, Cfg::TMEM_COLS);
+        tmem_relinquish<CG>();
+    }
+    wait_for_stream();
+    for (int e = threadIdx.x; e < a.groups; e += Cfg::THREADS) ends[e] = min(max(__ldg(a.ends + e), 0), a.M);
+    tc_fence_before_sync();
+    __syncthreads();
+    if (!GRAD && warp == 0) {
+        // tiles up to each expert's last
+        const int tiles_p = (a.P + Cfg::BP - 1) / Cfg::BP;
+        int before = 0;
+        for (int e0 = 0; e0 < a.groups; e0 += 32) {
+            const int e = e0 + static_cast<int>(lane);
+            int n = 0;
+            if (e < a.groups) n = (max(ends[e] - (e ? ends[e - 1] : 0), 0) + Cfg::BQ - 1) / Cfg::BQ * tiles_p;
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const int up = __shfl_up_sync(0xFFFFFFFFu, n, d);
+                if (static_cast<int>(lane) >= d) n += up;
+            }
+            if (e < a.groups) tiles[e] = before + n;
+            before += __shfl_sync(0xFFFFFFFFu, n, 31);
+        }
+    }
+    __syncthreads();
+    if constexpr (CG == 2) cluster_sync_all();
+    tc_fence_after_sync();
+    const uint32_t tmem_base = *tmem_slot_ptr;
+    const int num_tiles = GRAD ? a.groups * (((a.P + Cfg::BP - 1) / Cfg::BP) * ((a.Q + Cfg::BQ - 1) / Cfg::BQ))
+                               : tiles[a.groups - 1];
+    const int first = static_cast<int>(blockIdx.x) / CG, step = static_cast<int>(gridDim.x) / CG;
+
+    if (warp == 0) {
+        // ------------------------------------------------ TMA producer --
+        if (lane == 0) {
+            uint32_t stage = 0, phase = 0;
+            bool ok = true;
+            for (int tile = first; ok && tile < num_tiles; tile += step) {
+                const GroupedTile t = grouped_tile<Cfg>(tile, a, ends, tiles);
+                const int p = t.p0 + static_cast<int>(rank) * Cfg::BP_CTA;
+                const int q_cta = t.n / CG, q = t.q0 + static_cast<int>(rank) * q_cta;
+                const int boxes = (q_cta + Cfg::QBOX - 1) / Cfg::QBOX;
+                const uint32_t bytes = Cfg::P_BYTES + boxes * Cfg::QBOX * Cfg::BK * 2;
+                const int blocks = (t.k_len + Cfg::BK - 1) / Cfg::BK;
+                for (int kb = 0; kb < blocks; ++kb) {
+                    if (!mbar_wait(empty_bar(stage), phase ^ 1u, abort_flag, 2 * a.timeout_ns)) {
+                        record_timeout(a.status, abort_flag, abort_slot, CG, kRoleProducer * 16 + kBarEmpty);
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t p_dst = base + stage * Cfg::STAGE_BYTES, q_dst = p_dst + Cfg::P_BYTES;
+                    const int k = t.k0 + kb * Cfg::BK;
+                    if (GRAD && (t.k_len - kb * Cfg::BK) < Cfg::BK && t.k_len % 16 != 0) {
+                        const uint32_t bar = fix_bar(stage);
+                        mbar_arrive_expect_tx(bar, bytes);
+                        tma_load_2d(p_dst, &tmP, bar, p, k);
+                        tma_load_2d(p_dst + 8192u, &tmP, bar, p + 64, k);
+                        for (int b = 0; b < boxes; ++b) tma_load_2d(q_dst + 8192u * b, &tmQ, bar, q + 64 * b, k);
+                    } else {
+                        if (rank == 0) mbar_arrive_expect_tx(full_bar(stage), CG * bytes);
+                        else if (GRAD) mbar_arrive_cluster(map_to_cta(full_bar(stage), 0));
+                        const uint32_t bar = CG == 2 ? map_to_cta(full_bar(stage), 0) : full_bar(stage);
+                        auto load2 = [&](uint32_t dst, const CUtensorMap *m, int x, int y) {
+                            if constexpr (CG == 1) tma_load_2d(dst, m, bar, x, y);
+                            else tma_load_2d_pair(dst, m, bar, x, y);
+                        };
+                        auto load3 = [&](uint32_t dst, const CUtensorMap *m, int x, int y, int z) {
+                            if constexpr (CG == 1) tma_load_3d(dst, m, bar, x, y, z);
+                            else tma_load_3d_pair(dst, m, bar, x, y, z);
+                        };
+                        if constexpr (GRAD) {
+                            load2(p_dst, &tmP, p, k);
+                            load2(p_dst + 8192u, &tmP, p + 64, k);
+                            for (int b = 0; b < boxes; ++b) load2(q_dst + 8192u * b, &tmQ, q + 64 * b, k);
+                        } else {
+                            if constexpr (Cfg::PMN) {
+                                load3(p_dst, &tmP, p, k, t.group);
+                                load3(p_dst + 8192u, &tmP, p + 64, k, t.group);
+                            } else {
+                                load3(p_dst, &tmP, k, p, t.group);
+                            }
+                            for (int b = 0; b < boxes; ++b)
+                                load2(q_dst + Cfg::QBOX * 128u * b, &tmQ, k, q + Cfg::QBOX * b);
+                        }
+                    }
+                    if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+                }
+            }
+            // the MMAs' last releases must land before this CTA exits
+            for (int i = 0; ok && i < STAGES; ++i) {
+                if (!mbar_wait(empty_bar(stage), phase ^ 1u, abort_flag, 2 * a.timeout_ns)) {
+                    record_timeout(a.status, abort_flag, abort_slot, CG, kRoleProducer * 16 + kBarTail);
+                    ok = false;
+                }
+                if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+            }
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        // ------------------------------------------ MMA issuer (pair leader) --
+        if (rank == 0 && lane == 0) {
+            uint32_t stage = 0, phase = 0, done = 0;
+            bool ok = true;
+            for (int tile = first; ok && tile < num_tiles; tile += step) {
+                const GroupedTile t = grouped_tile<Cfg>(tile, a, ends, tiles);
+                if (t.k_len == 0) continue;
+                const uint32_t buf = done & 1u;
+                if (!mbar_wait(tempty_bar(buf), ((done >> 1) & 1u) ^ 1u, abort_flag, 3 * a.timeout_ns)) {
+                    record_timeout(a.status, abort_flag, abort_slot, CG, kRoleMma * 16 + kBarTmemEmpty);
+                    break;
+                }
+                tc_fence_after_sync();
+                const uint32_t acc = tmem_base + buf * Cfg::BQ;
+                const uint32_t idesc = idesc_bf16_f32(Cfg::BP, t.n, Cfg::PMN, Cfg::QMN);
+                const int blocks = (t.k_len + Cfg::BK - 1) / Cfg::BK;
+                for (int kb = 0; kb < blocks; ++kb) {
+                    if (!mbar_wait(full_bar(stage), phase, abort_flag, a.timeout_ns)) {
+                        record_timeout(a.status, abort_flag, abort_slot, CG, kRoleMma * 16 + kBarFull);
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after_sync();
+                    const uint32_t p_src = base + stage * Cfg::STAGE_BYTES, q_src = p_src + Cfg::P_BYTES;
+                    const int steps = min(Cfg::BK / 16, (t.k_len - kb * Cfg::BK + 15) / 16);
+#pragma unroll
+                    for (int j = 0; j < Cfg::BK / 16; ++j)
+                        if (j < steps)
+                            mma_bf16_ss<CG>(acc, operand_desc(p_src, j, Cfg::PMN), operand_desc(q_src, j, Cfg::QMN),
+                                            idesc, (kb | j) != 0 ? 1u : 0u);
+                    mma_commit<CG>(empty_bar(stage), 0x3);
+                    if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+                }
+                if (!ok) break;
+                mma_commit<CG>(tfull_bar(buf), 0x3);
+                ++done;
+            }
+        }
+        __syncwarp();
+    } else if (GRAD && warp == 2) {
+        // ------------------------- rows of the next expert in a last block --
+        uint32_t blocks = 0, parity = 0;       // blocks so far; bit s: parity of fix[s]
+        for (int tile = first; tile < num_tiles; tile += step) {
+            const GroupedTile t = grouped_tile<Cfg>(tile, a, ends, tiles);
+            blocks += (t.k_len + Cfg::BK - 1) / Cfg::BK;
+            if (t.k_len % 16 == 0) continue;
+            const uint32_t stage = (blocks - 1) % STAGES;
+            uint32_t ready = 1;
+            if (lane == 0 && !mbar_wait(fix_bar(stage), (parity >> stage) & 1u, abort_flag, 3 * a.timeout_ns)) {
+                record_timeout(a.status, abort_flag, abort_slot, CG, kRoleFix * 16 + kBarFix);
+                ready = 0;
+            }
+            ready = __shfl_sync(0xFFFFFFFFu, ready, 0);
+            if (!ready) break;
+            parity ^= 1u << stage;
+            // a row of a box is 128 bytes, swizzled within itself
+            const int used = t.k_len % Cfg::BK, clear = (16 - used % 16) * 128;
+            const int boxes = 2 + (t.n / CG + 63) / 64;         // P's, then Q's, 8 KB apart
+            uint8_t *at = smem + stage * Cfg::STAGE_BYTES + used * 128;
+            for (int b = 0; b < boxes; ++b)
+                for (int i = 16 * static_cast<int>(lane); i < clear; i += 512)
+                    *reinterpret_cast<uint4 *>(at + 8192 * b + i) = make_uint4(0, 0, 0, 0);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                if (CG == 2) mbar_arrive_cluster(map_to_cta(full_bar(stage), 0));
+                else mbar_arrive_local(full_bar(stage));
+            }
+        }
+        __syncwarp();
+    } else {
+        // ----------------------------------------------------- epilogue --
+        const uint32_t sub = warp & 3u;                         // TMEM lane quarter
+        const int part = static_cast<int>(warp - Cfg::EPI0) / 4;
+        constexpr int PARTS = Cfg::EPI_WARPS / 4;               // warps that share a quarter's columns
+        uint32_t done = 0;
+        for (int tile = first; tile < num_tiles; tile += step) {
+            const GroupedTile t = grouped_tile<Cfg>(tile, a, ends, tiles);
+            const uint32_t buf = done & 1u;
+            if (t.k_len > 0) {
+                uint32_t ready = 1;
+                if (lane == 0 && !mbar_wait(tfull_bar(buf), (done >> 1) & 1u, abort_flag, 3 * a.timeout_ns)) {
+                    record_timeout(a.status, abort_flag, abort_slot, CG, kRoleEpilogue * 16 + kBarTmemFull);
+                    ready = 0;
+                }
+                ready = __shfl_sync(0xFFFFFFFFu, ready, 0);
+                if (!ready) break;
+                tc_fence_after_sync();
+            }
+            const uint32_t acc = tmem_base + ((sub * 32u) << 16) + buf * Cfg::BQ;
+            const int col = t.p0 + static_cast<int>(rank) * Cfg::BP_CTA + static_cast<int>(sub * 32u + lane);
+            const int64_t esize = a.f32 ? 4 : 2;
+            uint8_t *out = static_cast<uint8_t *>(a.out) + (GRAD ? t.group * a.out_stride * esize : 0) +
+                           t.q0 * a.ld * esize;
+            for (int j = 32 * part; j < t.count; j += 32 * PARTS) {
+                uint32_t r[32];
+                float v[32];
+                if (t.k_len > 0) {
+                    tmem_ld_32x32b_x32(acc + j, r);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) v[i] = 0.0f;
+                }
+                store_columns<32>(out + j * a.ld * esize, a.ld, t.count - j, col, a.P, a.f32, GRAD ? a.beta : 0.0f, v);
+            }
+            if (t.k_len > 0) {
+                tc_fence_before_sync();
+                __syncwarp();
+                if (lane == 0) {
+                    if (CG == 1) mbar_arrive_local(tempty_bar(buf));
+                    else mbar_arrive_cluster(map_to_cta(tempty_bar(buf), 0));
+                }
+                ++done;
+            }
+        }
+    }
+
+    tc_fence_before_sync();
+    __syncthreads();
+    if constexpr (CG == 2) cluster_sync_all();
+    if (*abort_flag) {      // copies in flight land first
+        const uint64_t t0 = global_timer_ns();
+        while (global_timer_ns() - t0 < 200000ull) __nanosleep(1000);
+    }
+    __syncthreads();
+    if constexpr (CG == 2) cluster_sync_all();
+    if (warp == 1) {
+        tc_fence_after_sync();
+        tmem_dealloc<CG>(tmem_base, Cfg::TMEM_COLS);
+    }
+}
+
+}  // namespace b200

@@ -2,6 +2,7 @@
 // the record behind gemm_last_cuda_error, overlap and alignment tests.
 // Defined in b200gemm.cu.
 #pragma once
+#include <cuda.h>
 #include <cuda_runtime_api.h>
 
 #include <atomic>
@@ -10,6 +11,9 @@
 #include "b200gemm.h"
 
 namespace b200 {
+
+struct DeviceStatus;
+
 namespace host {
 
 constexpr int kMaxDevices = 64;
@@ -22,6 +26,18 @@ gemm_status_t cuda_fail(cudaError_t e);
 // of SMs.  Allocates nothing; the first call on a device may not be captured
 // (GEMM_ERR_CAPTURE).
 gemm_status_t device(int &dev, int &sm_count, cudaStream_t stream);
+
+// The same, with the device's watchdog status block (allocated on the first
+// call on the device that needs it).
+gemm_status_t device_with_status(int &dev, int &sm_count, DeviceStatus *&status, cudaStream_t stream);
+
+// How long a wait inside a kernel with a reduction of length K may take.
+uint64_t watchdog_ns(int64_t K);
+
+// A tensor map of `rank` (2 or 3) dimensions, innermost first, without
+// interleaving, zeros outside.  strides: bytes, of the outer dimensions.
+gemm_status_t encode_map(CUtensorMap *map, CUtensorMapDataType dtype, const void *ptr, int rank, const int64_t *dims,
+                         const int64_t *strides, const uint32_t *box, CUtensorMapSwizzle swizzle);
 
 // True while `stream` is being captured into a CUDA graph.
 bool capturing(cudaStream_t stream);

@@ -1,0 +1,251 @@
+// Host side of the products that leave the dense bf16 path (include/b200gemm.h):
+// grouped by expert.  Argument checks first, then one launch.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <atomic>
+#include <cstdint>
+
+#include "b200gemm.h"
+#include "gemm_grouped_sm100.cuh"
+#include "host.h"
+
+namespace {
+
+using b200::DeviceStatus;
+using b200::host::aligned16;
+using b200::host::extent_ok;
+using b200::host::kMaxDim;
+using b200::host::overlaps;
+using b200::host::pitch16;
+
+bool valid_type(gemm_out_t t) { return t == GEMM_OUT_F32 || t == GEMM_OUT_BF16; }
+bool valid_layout(gemm_layout_t l) { return l == GEMM_LAYOUT_KMAJOR || l == GEMM_LAYOUT_MNMAJOR; }
+int64_t size_of(gemm_out_t t) { return t == GEMM_OUT_F32 ? 4 : 2; }
+
+// `count` matrices of a call, `stride` elements apart: rows x cols elements of
+// `esize` bytes, pitch ld.
+struct Mat {
+    const void *p;
+    int64_t rows, cols, ld, esize, count = 1, stride = 0;
+    // elements from the first of a matrix to its last
+    int64_t span() const { return (rows - 1) * ld + cols; }
+};
+
+// Pointer, pitch, alignment and extent; several matrices may not overlap.
+gemm_status_t check_mat(const Mat &m) {
+    if (!m.p || m.ld < m.cols) return GEMM_ERR_INVALID_VALUE;
+    if (!aligned16(m.p) || !pitch16(m.ld, m.esize)) return GEMM_ERR_MISALIGNED;
+    if (!extent_ok(m.rows, m.ld, m.esize)) return GEMM_ERR_TOO_LARGE;
+    if (m.count > 1) {
+        if (m.stride < m.span()) return GEMM_ERR_INVALID_VALUE;
+        if (!pitch16(m.stride, m.esize)) return GEMM_ERR_MISALIGNED;
+        if (!extent_ok(m.count, m.stride, m.esize)) return GEMM_ERR_TOO_LARGE;
+    }
+    return GEMM_OK;
+}
+
+bool overlap(const Mat &a, const Mat &b) {
+    return overlaps(a.p, a.count, a.span(), a.stride, a.esize, b.p, b.count, b.span(), b.stride, b.esize);
+}
+
+// Clusters of `size` blocks of a kernel that a device holds at once.  Asked
+// once per kernel, device and size, before any capture.
+template <auto Kernel>
+gemm_status_t resident_clusters(int dev, int sm_count, int threads, int smem, int size, int &n, cudaStream_t stream) {
+    static std::atomic<int> known[b200::host::kMaxDevices][4];
+    const int slot = size >= 8 ? 3 : size >= 4 ? 2 : size >= 2 ? 1 : 0;
+    n = known[dev][slot].load(std::memory_order_relaxed);
+    if (n > 0) return GEMM_OK;
+    if (b200::host::capturing(stream)) return GEMM_ERR_CAPTURE;
+    cudaLaunchConfig_t lc = {};
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = static_cast<unsigned>(size);
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    lc.gridDim = dim3(static_cast<unsigned>(sm_count / size * size));
+    lc.blockDim = dim3(static_cast<unsigned>(threads));
+    lc.dynamicSmemBytes = static_cast<size_t>(smem);
+    lc.attrs = &attr;
+    lc.numAttrs = 1;
+    const cudaError_t e = cudaOccupancyMaxActiveClusters(&n, Kernel, &lc);
+    if (e != cudaSuccess) return b200::host::cuda_fail(e);
+    n = std::max(1, n);
+    known[dev][slot].store(n, std::memory_order_relaxed);
+    return GEMM_OK;
+}
+
+// One launch in clusters of `size` blocks, with programmatic dependence on the
+// kernel before it in the stream (wait_for_stream in the kernels).
+template <class... Params, class... Args>
+gemm_status_t launch(void (*kernel)(Params...), int clusters, int size, int threads, int smem, cudaStream_t stream,
+                     const Args &...args) {
+    cudaLaunchConfig_t lc = {};
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = static_cast<unsigned>(size);
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    lc.gridDim = dim3(static_cast<unsigned>(clusters * size));
+    lc.blockDim = dim3(static_cast<unsigned>(threads));
+    lc.dynamicSmemBytes = static_cast<size_t>(smem);
+    lc.stream = stream;
+    lc.attrs = attr;
+    lc.numAttrs = 2;
+    const cudaError_t e = cudaLaunchKernelEx(&lc, kernel, args...);
+    return e == cudaSuccess ? GEMM_OK : b200::host::cuda_fail(e);
+}
+
+// ------------------------------------------------------ grouped by expert --
+
+// K-major operand of bf16: rows of K, boxes of 64 x `box` rows.
+gemm_status_t map_rows(CUtensorMap *map, const Mat &m, uint32_t box) {
+    const int64_t dims[2] = {m.cols, m.rows}, strides[1] = {m.ld * 2};
+    const uint32_t b[2] = {64, box};
+    return b200::host::encode_map(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, m.p, 2, dims, strides, b,
+                                  CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+// The experts' matrices: boxes of 64 x `box` rows of one of them.
+gemm_status_t map_experts(CUtensorMap *map, const Mat &m, uint32_t box) {
+    const int64_t stride = m.count > 1 ? m.stride : (m.rows * m.ld + 7) / 8 * 8;
+    const int64_t dims[3] = {m.cols, m.rows, m.count}, strides[2] = {m.ld * 2, stride * 2};
+    const uint32_t b[3] = {64, box, 1};
+    return b200::host::encode_map(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, m.p, 3, dims, strides, b,
+                                  CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+constexpr int64_t kMaxTiles = int64_t(1) << 30;     // tile numbers are 32-bit, one grid's step on top
+
+template <class Cfg>
+gemm_status_t launch_grouped(int dev, int sm_count, const CUtensorMap &tmP, const CUtensorMap &tmQ,
+                             const b200::GroupedArgs &a, int64_t tiles, cudaStream_t stream) {
+    constexpr auto kernel = b200::gemm_grouped_kernel<Cfg>;
+    constexpr int kMost = Cfg::smem_bytes(b200::kMaxGroups);
+    if (tiles > kMaxTiles) return GEMM_ERR_TOO_LARGE;
+    gemm_status_t s;
+    int room;
+    if ((s = b200::host::prepare<kernel>(dev, kMost, stream)) != GEMM_OK) return s;
+    if ((s = resident_clusters<kernel>(dev, sm_count, Cfg::THREADS, kMost, Cfg::CG, room, stream)) != GEMM_OK) return s;
+    return launch(kernel, static_cast<int>(std::min<int64_t>(room, tiles)), Cfg::CG, Cfg::THREADS,
+                  Cfg::smem_bytes(a.groups), stream, tmP, tmQ, a);
+}
+
+template <class Cfg>
+gemm_status_t launch_rows(int dev, int sm_count, const Mat &A, const Mat &B, const b200::GroupedArgs &a,
+                          cudaStream_t stream) {
+    alignas(64) CUtensorMap tmP{}, tmQ{};
+    gemm_status_t s;
+    if (a.K > 0) {
+        if ((s = map_experts(&tmP, B, Cfg::PMN ? Cfg::BK : Cfg::BP_CTA)) != GEMM_OK) return s;
+        if ((s = map_rows(&tmQ, A, Cfg::QBOX)) != GEMM_OK) return s;
+    }
+    // at most: whole tiles of all rows, and one more per expert that has rows
+    const int64_t tiles = (a.M / Cfg::BQ + std::min(a.groups, a.M)) * ((int64_t(a.P) + Cfg::BP - 1) / Cfg::BP);
+    return launch_grouped<Cfg>(dev, sm_count, tmP, tmQ, a, tiles, stream);
+}
+
+template <bool PMN>
+gemm_status_t dispatch_rows(int dev, int sm_count, const Mat &A, const Mat &B, const b200::GroupedArgs &a,
+                            cudaStream_t stream) {
+    if (a.M <= int64_t(64) * a.groups)
+        return launch_rows<b200::GroupedCfg<b200::kGroupedRows, PMN, 1, 64, 8>>(dev, sm_count, A, B, a, stream);
+    return launch_rows<b200::GroupedCfg<b200::kGroupedRows, PMN, 2, 256, 6>>(dev, sm_count, A, B, a, stream);
+}
+
+using CfgGrad = b200::GroupedCfg<b200::kGroupedGrad, true, 2, 256, 6>;
+
+}  // namespace
+
+extern "C" {
+
+gemm_status_t gemm_bf16_grouped(const void *A, const void *B, const int32_t *ends, void *C, int64_t groups, int64_t M,
+                                int64_t N, int64_t K, int64_t lda, int64_t ldb, int64_t strideb, int64_t ldc,
+                                gemm_out_t c_type, gemm_layout_t b_layout, cudaStream_t stream) {
+    if (groups < 0 || M < 0 || N < 0 || K < 0) return GEMM_ERR_INVALID_VALUE;
+    if (M > kMaxDim || N > kMaxDim || K > kMaxDim || groups > b200::kMaxGroups) return GEMM_ERR_TOO_LARGE;
+    if (!valid_type(c_type) || !valid_layout(b_layout)) return GEMM_ERR_INVALID_VALUE;
+    if (groups == 0 || M == 0 || N == 0) return GEMM_OK;
+    if (!ends) return GEMM_ERR_INVALID_VALUE;
+    if (reinterpret_cast<uintptr_t>(ends) & 3u) return GEMM_ERR_MISALIGNED;
+    const bool mn = b_layout == GEMM_LAYOUT_MNMAJOR;
+    const Mat mc{C, M, N, ldc, size_of(c_type)};
+    const Mat me{ends, 1, groups, groups, 4};
+    const Mat ma{A, M, K, lda, 2};
+    const Mat mb{B, mn ? K : N, mn ? N : K, ldb, 2, groups, strideb};
+    gemm_status_t s;
+    if ((s = check_mat(mc)) != GEMM_OK) return s;
+    if (overlap(mc, me)) return GEMM_ERR_ALIAS;
+    if (K > 0) {
+        if ((s = check_mat(ma)) != GEMM_OK || (s = check_mat(mb)) != GEMM_OK) return s;
+        if (overlap(mc, ma) || overlap(mc, mb)) return GEMM_ERR_ALIAS;
+    }
+    int dev, sm_count;
+    DeviceStatus *status;
+    if ((s = b200::host::device_with_status(dev, sm_count, status, stream)) != GEMM_OK) return s;
+    b200::GroupedArgs a{};
+    a.ends = ends;
+    a.out = C;
+    a.ld = ldc;
+    a.groups = static_cast<int>(groups);
+    a.M = static_cast<int>(M);
+    a.P = static_cast<int>(N);
+    a.K = static_cast<int>(K);
+    a.f32 = c_type == GEMM_OUT_F32;
+    a.status = status;
+    a.timeout_ns = b200::host::watchdog_ns(K);
+    return mn ? dispatch_rows<true>(dev, sm_count, ma, mb, a, stream)
+              : dispatch_rows<false>(dev, sm_count, ma, mb, a, stream);
+}
+
+gemm_status_t gemm_bf16_grouped_wgrad(const void *dC, const void *A, const int32_t *ends, void *dB, int64_t groups,
+                                      int64_t M, int64_t N, int64_t K, int64_t lddc, int64_t lda, int64_t lddb,
+                                      int64_t stridedb, gemm_out_t db_type, gemm_layout_t db_layout, float beta,
+                                      cudaStream_t stream) {
+    if (groups < 0 || M < 0 || N < 0 || K < 0) return GEMM_ERR_INVALID_VALUE;
+    if (M > kMaxDim || N > kMaxDim || K > kMaxDim || groups > b200::kMaxGroups) return GEMM_ERR_TOO_LARGE;
+    if (!valid_type(db_type) || !valid_layout(db_layout)) return GEMM_ERR_INVALID_VALUE;
+    if (groups == 0 || N == 0 || K == 0) return GEMM_OK;
+    if (!ends) return GEMM_ERR_INVALID_VALUE;
+    if (reinterpret_cast<uintptr_t>(ends) & 3u) return GEMM_ERR_MISALIGNED;
+    const bool mn = db_layout == GEMM_LAYOUT_MNMAJOR;
+    const Mat mg{dB, mn ? K : N, mn ? N : K, lddb, size_of(db_type), groups, stridedb};
+    const Mat me{ends, 1, groups, groups, 4};
+    const Mat mc{dC, M, N, lddc, 2};
+    const Mat ma{A, M, K, lda, 2};
+    gemm_status_t s;
+    if ((s = check_mat(mg)) != GEMM_OK) return s;
+    if (overlap(mg, me)) return GEMM_ERR_ALIAS;
+    if (M > 0) {
+        if ((s = check_mat(mc)) != GEMM_OK || (s = check_mat(ma)) != GEMM_OK) return s;
+        if (overlap(mg, mc) || overlap(mg, ma)) return GEMM_ERR_ALIAS;
+    }
+    int dev, sm_count;
+    DeviceStatus *status;
+    if ((s = b200::host::device_with_status(dev, sm_count, status, stream)) != GEMM_OK) return s;
+    const Mat &p = mn ? mc : ma, &q = mn ? ma : mc;     // P's index runs along a row of dB
+    b200::GroupedArgs a{};
+    a.ends = ends;
+    a.out = dB;
+    a.ld = lddb;
+    a.out_stride = stridedb;
+    a.groups = static_cast<int>(groups);
+    a.M = static_cast<int>(M);
+    a.P = static_cast<int>(p.cols);
+    a.Q = static_cast<int>(q.cols);
+    a.beta = beta;
+    a.f32 = db_type == GEMM_OUT_F32;
+    a.status = status;
+    a.timeout_ns = b200::host::watchdog_ns(M);
+    alignas(64) CUtensorMap tmP{}, tmQ{};
+    if (M > 0) {
+        if ((s = map_rows(&tmP, p, CfgGrad::BK)) != GEMM_OK || (s = map_rows(&tmQ, q, CfgGrad::BK)) != GEMM_OK) return s;
+    }
+    const int64_t tiles = ((p.cols + CfgGrad::BP - 1) / CfgGrad::BP) * ((q.cols + CfgGrad::BQ - 1) / CfgGrad::BQ);
+    if (tiles > kMaxTiles) return GEMM_ERR_TOO_LARGE;
+    return launch_grouped<CfgGrad>(dev, sm_count, tmP, tmQ, a, tiles * groups, stream);
+}
+
+}  // extern "C"

@@ -142,6 +142,25 @@ __device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const CUtensorMap
         : "memory");
 }
 
+// 3-D tiled loads: as tma_load_2d and tma_load_2d_pair, with a matrix index z.
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *map, uint32_t bar, int32_t x, int32_t y,
+                                            int32_t z) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5}], [%2];"
+        ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z)
+        : "memory");
+}
+
+__device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const CUtensorMap *map, uint32_t bar_cluster, int32_t x,
+                                                 int32_t y, int32_t z) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5}], [%2];"
+        ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(bar_cluster), "r"(x), "r"(y), "r"(z)
+        : "memory");
+}
+
 // L2 eviction-priority policies for TMA loads (createpolicy): an operand that
 // later tiles read again is kept (evict_last); one that only the tiles
 // running now read goes first (evict_first).
@@ -347,6 +366,25 @@ __device__ __forceinline__ void mma_mxf8_ss(uint32_t d_tmem, uint64_t a_desc, ui
                  : "memory");
 }
 
+// Block-scaled MMA of 4-bit operands (E2M1 x E2M1, K = 64, f32 accumulator).
+// NV: one E4M3 scale per 16 K elements, four to a 32-bit TMEM word; else one
+// E8M0 scale per 32, two of a word's four (chosen in the descriptor).
+template <int CG, bool NV>
+__device__ __forceinline__ void mma_fp4_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                           uint32_t sfa_tmem, uint32_t sfb_tmem, uint32_t accumulate) {
+#define B200_MMA_FP4(GROUP, KIND)                                                                               \
+    asm volatile("{\n\t.reg .pred p;\n\t"                                                                       \
+                 "setp.ne.b32 p, %4, 0;\n\t"                                                                    \
+                 "tcgen05.mma.cta_group::" GROUP ".kind::" KIND " [%0], %1, %2, %3, [%5], [%6], p;\n\t}"        \
+                 ::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(sfa_tmem), "r"(sfb_tmem) \
+                 : "memory")
+    if constexpr (CG == 1 && NV) B200_MMA_FP4("1", "mxf4nvf4.block_scale.scale_vec::4X");
+    else if constexpr (CG == 1) B200_MMA_FP4("1", "mxf4.block_scale.scale_vec::2X");
+    else if constexpr (NV) B200_MMA_FP4("2", "mxf4nvf4.block_scale.scale_vec::4X");
+    else B200_MMA_FP4("2", "mxf4.block_scale.scale_vec::2X");
+#undef B200_MMA_FP4
+}
+
 // ------------------------------------------------ cluster launch control --
 
 // Ask the hardware scheduler to cancel one cluster of this grid that has not
@@ -446,6 +484,15 @@ __device__ __forceinline__ uint64_t rows16_desc(uint32_t smem) {
 __host__ __device__ constexpr uint32_t idesc_mxf8_e8m0(int m, int n, uint32_t a_sf_id, uint32_t b_sf_id) {
     return (b_sf_id << 4) | (static_cast<uint32_t>(n >> 3) << 17) | (1u << 23) |
            (static_cast<uint32_t>(m >> 4) << 24) | (a_sf_id << 29);
+}
+
+// Instruction descriptor, kind::mxf4 and kind::mxf4nvf4: A and B E2M1 (format
+// 1, bits 7-9 / 10-11), N >> 3 (17-22), scale format (bit 23: E8M0, else
+// E4M3), M >> 4 (24-28), the first of the scales in each 32-bit word: B (bits
+// 4-5), A (29-30): 0, or with E8M0 also 2.  Dense, K = 64 per MMA, K-major.
+__host__ __device__ constexpr uint32_t idesc_fp4(bool nv, uint32_t m, uint32_t n, uint32_t sf_id) {
+    return (sf_id << 4) | (1u << 7) | (1u << 10) | ((n >> 3) << 17) | (nv ? 0u : 1u << 23) | ((m >> 4) << 24) |
+           (sf_id << 29);
 }
 
 // ----------------------------------------------------------- conversions --

@@ -82,6 +82,10 @@ lib.gemm_mxfp8_quantize.argtypes = [_vp, _vp, _vp, _i64, _i64, _i64, _i64, _int,
 lib.gemm_mxfp8_quantize.restype = _int
 lib.gemm_bf16_w4.argtypes = [_vp] * 5 + [_i64] * 8 + [_int, _vp]
 lib.gemm_bf16_w4.restype = _int
+lib.gemm_bf16_grouped.argtypes = [_vp] * 4 + [_i64] * 8 + [_int, _int, _vp]
+lib.gemm_bf16_grouped.restype = _int
+lib.gemm_bf16_grouped_wgrad.argtypes = [_vp] * 4 + [_i64] * 8 + [_int, _int, ctypes.c_float, _vp]
+lib.gemm_bf16_grouped_wgrad.restype = _int
 lib.gemm_check_device_status.argtypes = [_vp]
 lib.gemm_check_device_status.restype = _int
 lib.gemm_last_timeout_detail.argtypes = [ctypes.POINTER(ctypes.c_int32), ctypes.POINTER(ctypes.c_int32)]
@@ -215,6 +219,7 @@ def _here(stream):
         queue = getattr(torch._C, "_cuda_getCurrentRawStream",
                         lambda dev: torch.cuda.current_stream(dev).cuda_stream)
         _DTYPES.update({OUT_F32: (torch.float32,), OUT_BF16: (torch.bfloat16,), "bytes": (torch.uint8,),
+                        "ints": (torch.int32,),
                         "codes": (torch.float8_e4m3fn, torch.uint8), "scales": (torch.float8_e8m0fnu, torch.uint8),
                         "device": device, "stream": queue})
     if stream is not None:
@@ -342,6 +347,44 @@ def gemm_bf16_w4(A, B, scales, zeros, C, M: int, N: int, K: int, lda: int, ldb: 
     except GemmError as e:
         return _refused(e, check)
     return _check(st, "gemm_bf16_w4", check)
+
+
+def gemm_bf16_grouped(A, B, ends, C, groups: int, M: int, N: int, K: int, lda: int, ldb: int, strideb: int, ldc: int,
+                      c_type: int = OUT_F32, b_layout: int = KMAJOR, stream=None, check: bool = True) -> int:
+    """C[r] = A[r].B_e for the rows r of every expert e: bf16 A (M x K, rows
+    sorted by expert), `groups` bf16 matrices B (N x K each, or K x N with
+    MNMAJOR) strideb elements apart, int32 ends[e] where expert e's rows end
+    (on the device), C M x N; rows of no expert are left as they are (see
+    include/b200gemm.h, gemm_bf16_grouped)."""
+    try:
+        dev, queue = _here(stream)
+        st = lib.gemm_bf16_grouped(_operand(A, OUT_BF16, dev, "gemm_bf16_grouped: A"),
+                                   _operand(B, OUT_BF16, dev, "gemm_bf16_grouped: B"),
+                                   _operand(ends, "ints", dev, "gemm_bf16_grouped: ends", True),
+                                   _operand(C, c_type, dev, "gemm_bf16_grouped: C"), groups, M, N, K, lda, ldb, strideb,
+                                   ldc, int(c_type), int(b_layout), queue)
+    except GemmError as e:
+        return _refused(e, check)
+    return _check(st, "gemm_bf16_grouped", check)
+
+
+def gemm_bf16_grouped_wgrad(dC, A, ends, dB, groups: int, M: int, N: int, K: int, lddc: int, lda: int, lddb: int,
+                            stridedb: int, db_type: int = OUT_F32, db_layout: int = KMAJOR, beta: float = 0.0,
+                            stream=None, check: bool = True) -> int:
+    """dB_e = beta dB_e + dC_e^T.A_e, the gradient of gemm_bf16_grouped's B_e:
+    bf16 dC (M x N) and A (M x K), `groups` matrices dB (N x K each, or K x N
+    with MNMAJOR) stridedb elements apart (see include/b200gemm.h,
+    gemm_bf16_grouped_wgrad)."""
+    try:
+        dev, queue = _here(stream)
+        st = lib.gemm_bf16_grouped_wgrad(_operand(dC, OUT_BF16, dev, "gemm_bf16_grouped_wgrad: dC"),
+                                         _operand(A, OUT_BF16, dev, "gemm_bf16_grouped_wgrad: A"),
+                                         _operand(ends, "ints", dev, "gemm_bf16_grouped_wgrad: ends", True),
+                                         _operand(dB, db_type, dev, "gemm_bf16_grouped_wgrad: dB"), groups, M, N, K,
+                                         lddc, lda, lddb, stridedb, int(db_type), int(db_layout), beta, queue)
+    except GemmError as e:
+        return _refused(e, check)
+    return _check(st, "gemm_bf16_grouped_wgrad", check)
 
 
 def gemm_check_device_status(stream=None, check: bool = True) -> int:

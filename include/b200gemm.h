@@ -447,6 +447,63 @@ B200GEMM_API gemm_status_t gemm_bf16_w4(const void *A, const uint8_t *B, const v
                                         int64_t M, int64_t N, int64_t K, int64_t lda, int64_t ldb, int64_t lds, int64_t ldc,
                                         int64_t group, gemm_out_t c_type, cudaStream_t stream);
 
+/*
+ * Products grouped by expert.  A's rows are sorted by expert; ends[e], on the
+ * DEVICE, says where expert e's rows end: it has the rows [ends[e-1], ends[e])
+ * (ends[-1] = 0), possibly none.  The host never learns the sizes, so a call
+ * can be queued, or captured into a graph, before they are known.  ends must not
+ * decrease and stay within [0, M]; where it does not, which rows are computed
+ * is unspecified (nothing outside the operands is touched).
+ * Like the products these use the device's status block (its first call on a
+ * device may not be captured) and their waits are bounded by the watchdog; they
+ * need no workspace, so calls on different streams are independent.
+ */
+
+/*
+ * gemm_bf16_grouped: C[r] = A[r] . B_e for the rows r of every expert e.
+ *
+ *   A      M x K bf16, rows sorted by expert
+ *   B      `groups` matrices of bf16, strideb elements apart, each N rows of K
+ *          (b_layout K-major: the forward pass) or K rows of N (MN-major: with
+ *          the same weights, their output as A and K and N exchanged, the
+ *          gradient of the inputs)
+ *   ends   groups int32, see above
+ *   C      M x N of c_type.  Rows that belong to no expert (from
+ *          ends[groups-1] on) are left as they are
+ *   groups 0 .. 1024 (more: GEMM_ERR_TOO_LARGE)
+ * ldb is at least a stored row's length, strideb at least a matrix from its
+ * first element to its last; strideb is not looked at with one group.
+ * 16-byte aligned bases, pitches and stride.  bf16 products, fp32 sums in a fixed
+ * order, rounded once.  K == 0: the experts' rows of C = 0.  C overlaps no
+ * input.  groups, M or N == 0: nothing to do.  One kernel.
+ */
+B200GEMM_API gemm_status_t gemm_bf16_grouped(const void *A, const void *B, const int32_t *ends, void *C, int64_t groups,
+                                             int64_t M, int64_t N, int64_t K, int64_t lda, int64_t ldb, int64_t strideb,
+                                             int64_t ldc, gemm_out_t c_type, gemm_layout_t b_layout,
+                                             cudaStream_t stream);
+
+/*
+ * gemm_bf16_grouped_wgrad: the gradient of the experts' matrices,
+ *
+ *   dB_e[n][k] = beta dB_e[n][k] + sum over expert e's rows r of dC[r][n] A[r][k]
+ *
+ *   dC     M x N bf16, the gradient of gemm_bf16_grouped's C
+ *   A      M x K bf16, its A
+ *   dB     `groups` matrices of db_type, stridedb elements apart, each stored
+ *          as B is: N rows of K (db_layout K-major) or K rows of N (MN-major).
+ *          An expert without rows gets beta dB_e
+ *   beta   0: dB's old contents, NaN included, are not read; 1: added to, as
+ *          gradients over several batches are
+ * Rows that belong to no expert count nowhere, whatever they hold.  Sums are
+ * fp32 in a fixed order, beta dB_e added in fp32, rounded once.  M == 0: dB =
+ * beta dB.  dB overlaps no input.  groups, N or K == 0: nothing to do.  Other
+ * rules as gemm_bf16_grouped.  One kernel.
+ */
+B200GEMM_API gemm_status_t gemm_bf16_grouped_wgrad(const void *dC, const void *A, const int32_t *ends, void *dB,
+                                                   int64_t groups, int64_t M, int64_t N, int64_t K, int64_t lddc,
+                                                   int64_t lda, int64_t lddb, int64_t stridedb, gemm_out_t db_type,
+                                                   gemm_layout_t db_layout, float beta, cudaStream_t stream);
+
 /* Synchronises `stream`, then reports and clears the device watchdog status
  * of the current device (the status blocks of every entry point, the static
  * one of gemm_bf16_noalloc included): GEMM_OK, or GEMM_ERR_TIMEOUT if a
