@@ -92,9 +92,11 @@ constexpr uint32_t kStatusTimeout = 6;   // == GEMM_ERR_TIMEOUT
 // warp's bounded wait expires and the abort path runs.  Nothing faults.
 constexpr uint32_t kInjectDropFirstStage = 1u;
 
-enum : int { kRoleProducer = 1, kRoleMma = 2, kRoleEpilogue = 3, kRoleScheduler = 4 };
+// Watchdog codes of every kernel's warps and barriers (the scale copier and
+// its slots: block-scaled kernels; the fixer: grouped gradients).
+enum : int { kRoleProducer = 1, kRoleMma = 2, kRoleEpilogue = 3, kRoleScheduler = 4, kRoleSfCopy = 5, kRoleFix = 6 };
 enum : int { kBarFull = 1, kBarEmpty = 2, kBarTmemFull = 3, kBarTmemEmpty = 4, kBarTail = 5, kBarSched = 6,
-             kBarClc = 7, kBarPeerFree = 10, kBarRxFull = 11 };
+             kBarClc = 7, kBarSfFull = 8, kBarSfEmpty = 9, kBarPeerFree = 10, kBarRxFull = 11, kBarFix = 12 };
 
 __host__ __device__ constexpr int pow2_at_least(int v, int lo) {
     int p = lo;

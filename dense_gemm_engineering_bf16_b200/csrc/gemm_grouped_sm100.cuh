@@ -39,8 +39,6 @@
 namespace b200 {
 
 constexpr int kMaxGroups = 1024;      // two words of shared memory each
-constexpr int kRoleFix = 6;           // watchdog codes of the gradient's second warp
-constexpr int kBarFix = 12;
 
 // What a kernel computes: rows of C, or an expert's gradient.
 enum : int { kGroupedRows = 0, kGroupedGrad = 1 };

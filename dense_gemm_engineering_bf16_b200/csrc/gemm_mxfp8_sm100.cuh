@@ -48,10 +48,6 @@
 
 namespace b200 {
 
-// Watchdog codes of the scale copier (role) and the scale-slot barriers.
-constexpr int kRoleSfCopy = 5;
-constexpr int kBarSfFull = 8, kBarSfEmpty = 9;
-
 template <int CG_, int STAGES_>
 struct GemmMxf8Cfg {
     static constexpr int CG = CG_;                 // CTAs per tile (cta_group)

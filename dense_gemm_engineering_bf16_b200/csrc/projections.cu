@@ -1,5 +1,6 @@
 // Host side of the products that leave the dense bf16 path (include/b200gemm.h):
-// grouped by expert.  Argument checks first, then one launch.
+// grouped by expert, and of 4-bit floating-point operands with their
+// quantiser.  Argument checks first, then one launch.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -8,6 +9,8 @@
 #include <cstdint>
 
 #include "b200gemm.h"
+#include "fp4_quantize_sm100.cuh"
+#include "gemm_fp4_sm100.cuh"
 #include "gemm_grouped_sm100.cuh"
 #include "host.h"
 
@@ -21,6 +24,7 @@ using b200::host::overlaps;
 using b200::host::pitch16;
 
 bool valid_type(gemm_out_t t) { return t == GEMM_OUT_F32 || t == GEMM_OUT_BF16; }
+bool valid_format(gemm_fp4_t f) { return f == GEMM_FP4_MX || f == GEMM_FP4_NV; }
 bool valid_layout(gemm_layout_t l) { return l == GEMM_LAYOUT_KMAJOR || l == GEMM_LAYOUT_MNMAJOR; }
 int64_t size_of(gemm_out_t t) { return t == GEMM_OUT_F32 ? 4 : 2; }
 
@@ -98,6 +102,21 @@ gemm_status_t launch(void (*kernel)(Params...), int clusters, int size, int thre
     return e == cudaSuccess ? GEMM_OK : b200::host::cuda_fail(e);
 }
 
+template <class... Params, class... Args>
+gemm_status_t launch(void (*kernel)(Params...), dim3 grid, dim3 block, cudaStream_t stream, const Args &...args) {
+    cudaLaunchConfig_t lc = {};
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    lc.gridDim = grid;
+    lc.blockDim = block;
+    lc.stream = stream;
+    lc.attrs = &attr;
+    lc.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&lc, kernel, args...);
+    return e == cudaSuccess ? GEMM_OK : b200::host::cuda_fail(e);
+}
+
 // ------------------------------------------------------ grouped by expert --
 
 // K-major operand of bf16: rows of K, boxes of 64 x `box` rows.
@@ -153,6 +172,96 @@ gemm_status_t dispatch_rows(int dev, int sm_count, const Mat &A, const Mat &B, c
     if (a.M <= int64_t(64) * a.groups)
         return launch_rows<b200::GroupedCfg<b200::kGroupedRows, PMN, 1, 64, 8>>(dev, sm_count, A, B, a, stream);
     return launch_rows<b200::GroupedCfg<b200::kGroupedRows, PMN, 2, 256, 6>>(dev, sm_count, A, B, a, stream);
+}
+
+// ----------------------------------------------------------------- 4 bits --
+
+int64_t block_of(gemm_fp4_t f) { return f == GEMM_FP4_NV ? b200::kFp4Block<true> : b200::kFp4Block<false>; }
+
+// Scale tiles along K, and of a matrix.
+int64_t scale_tiles_k(int64_t K, gemm_fp4_t f) { return (K + 4 * block_of(f) - 1) / (4 * block_of(f)); }
+int64_t scale_tiles(int64_t rows, int64_t K, gemm_fp4_t f) { return (rows + 127) / 128 * scale_tiles_k(K, f); }
+
+// Of a matrix's scales: 32-bit words in tiles, `chunks` neighbouring ones a box.
+gemm_status_t map_scales(CUtensorMap *map, const uint8_t *sf, int64_t tiles, int chunks) {
+    const int64_t dims[2] = {b200::kScaleTile / 4, tiles}, strides[1] = {b200::kScaleTile};
+    const uint32_t b[2] = {b200::kScaleTile / 4, static_cast<uint32_t>(chunks)};
+    return b200::host::encode_map(map, CU_TENSOR_MAP_DATA_TYPE_UINT32, sf, 2, dims, strides, b,
+                                  CU_TENSOR_MAP_SWIZZLE_NONE);
+}
+
+// Codes: rows of bytes, boxes of 128 x `box` rows.
+gemm_status_t map_codes(CUtensorMap *map, const Mat &m, uint32_t box) {
+    const int64_t dims[2] = {m.cols, m.rows}, strides[1] = {m.ld};
+    const uint32_t b[2] = {128, box};
+    return b200::host::encode_map(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, m.p, 2, dims, strides, b,
+                                  CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+struct Fp4Call {
+    Mat a, b;
+    const uint8_t *sfa, *sfb;
+    gemm_fp4_t format;
+    b200::GemmFp4Args args;
+};
+
+template <class Cfg>
+gemm_status_t launch_fp4(int dev, int sm_count, const Fp4Call &c, cudaStream_t stream) {
+    constexpr auto kernel = b200::gemm_fp4_kernel<Cfg>;
+    const int64_t tiles = ((int64_t(c.args.N) + Cfg::BP - 1) / Cfg::BP) * ((int64_t(c.args.M) + Cfg::BQ - 1) / Cfg::BQ);
+    if (tiles > kMaxTiles) return GEMM_ERR_TOO_LARGE;
+    gemm_status_t s;
+    if ((s = b200::host::prepare<kernel>(dev, Cfg::SMEM_BYTES, stream)) != GEMM_OK) return s;
+    int size = Cfg::CG, room;
+    if constexpr (Cfg::SPLIT) {
+        // K in as many shares as keep every cluster resident at once, two stages each at least
+        const int64_t blocks = (int64_t(c.args.K) + Cfg::BK - 1) / Cfg::BK;
+        for (size = 8; size > 1; size /= 2) {
+            if ((s = resident_clusters<kernel>(dev, sm_count, Cfg::THREADS, Cfg::SMEM_BYTES, size, room, stream)) != GEMM_OK)
+                return s;
+            if (tiles <= room && blocks >= 2 * size) break;
+        }
+    }
+    if ((s = resident_clusters<kernel>(dev, sm_count, Cfg::THREADS, Cfg::SMEM_BYTES, size, room, stream)) != GEMM_OK)
+        return s;
+    alignas(64) CUtensorMap tmP, tmQ, tmSP, tmSQ;
+    if ((s = map_codes(&tmP, c.b, Cfg::BP_CTA)) != GEMM_OK || (s = map_codes(&tmQ, c.a, Cfg::QBOX)) != GEMM_OK ||
+        (s = map_scales(&tmSP, c.sfb, scale_tiles(c.args.N, c.args.K, c.format), Cfg::CHUNKS)) != GEMM_OK ||
+        (s = map_scales(&tmSQ, c.sfa, scale_tiles(c.args.M, c.args.K, c.format), Cfg::CHUNKS)) != GEMM_OK)
+        return s;
+    return launch(kernel, static_cast<int>(std::min<int64_t>(room, tiles)), size, Cfg::THREADS, Cfg::SMEM_BYTES, stream,
+                  tmP, tmQ, tmSP, tmSQ, c.args);
+}
+
+template <bool NV>
+gemm_status_t dispatch_fp4(int dev, int sm_count, const Fp4Call &c, cudaStream_t stream) {
+    if (c.args.M <= 64) return launch_fp4<b200::GemmFp4Cfg<NV, 1, 64, 6, true>>(dev, sm_count, c, stream);
+    const int64_t pairs = (int64_t(c.args.M) + 255) / 256 * ((int64_t(c.args.N) + 255) / 256);
+    if (2 * pairs >= sm_count) return launch_fp4<b200::GemmFp4Cfg<NV, 2, 256, 5>>(dev, sm_count, c, stream);
+    return launch_fp4<b200::GemmFp4Cfg<NV, 1, 128, 6>>(dev, sm_count, c, stream);
+}
+
+template <int XT, bool NV>
+gemm_status_t launch_fp4_quantize(int dev, const b200::Fp4QuantizeArgs &a, gemm_layout_t layout, cudaStream_t stream) {
+    gemm_status_t s;
+    if (layout == GEMM_LAYOUT_MNMAJOR) {
+        const int64_t i_tiles = (a.M + 63) / 64, blocks = i_tiles * ((a.K + 127) / 128);
+        if (blocks > kMaxDim) return GEMM_ERR_TOO_LARGE;
+        if ((s = b200::host::prepare<b200::fp4_quantize_mn_kernel<XT, NV>>(dev, 0, stream)) != GEMM_OK) return s;
+        return launch(b200::fp4_quantize_mn_kernel<XT, NV>, dim3(static_cast<unsigned>(blocks)), dim3(128), stream, a,
+                      static_cast<unsigned>(i_tiles));
+    }
+    constexpr int VPT = 4;
+    const int64_t vecs = a.K / 8;
+    dim3 block(32, 8);
+    if (vecs > 32 * VPT)
+        block = dim3(static_cast<unsigned>(std::min<int64_t>(256, ((vecs + VPT - 1) / VPT + 31) / 32 * 32)));
+    const int64_t parts = (vecs + VPT * block.x - 1) / (VPT * block.x);
+    const int64_t blocks = (a.M + block.y - 1) / block.y * parts;
+    if (blocks > kMaxDim) return GEMM_ERR_TOO_LARGE;
+    if ((s = b200::host::prepare<b200::fp4_quantize_kernel<XT, NV, VPT>>(dev, 0, stream)) != GEMM_OK) return s;
+    return launch(b200::fp4_quantize_kernel<XT, NV, VPT>, dim3(static_cast<unsigned>(blocks)), block, stream, a,
+                  static_cast<unsigned>(parts));
 }
 
 using CfgGrad = b200::GroupedCfg<b200::kGroupedGrad, true, 2, 256, 6>;
@@ -246,6 +355,90 @@ gemm_status_t gemm_bf16_grouped_wgrad(const void *dC, const void *A, const int32
     const int64_t tiles = ((p.cols + CfgGrad::BP - 1) / CfgGrad::BP) * ((q.cols + CfgGrad::BQ - 1) / CfgGrad::BQ);
     if (tiles > kMaxTiles) return GEMM_ERR_TOO_LARGE;
     return launch_grouped<CfgGrad>(dev, sm_count, tmP, tmQ, a, tiles * groups, stream);
+}
+
+int64_t gemm_fp4_scale_bytes(int64_t rows, int64_t K, gemm_fp4_t format) {
+    if (rows <= 0 || K <= 0 || rows > kMaxDim || K > kMaxDim || !valid_format(format)) return 0;
+    return scale_tiles(rows, K, format) * b200::kScaleTile;
+}
+
+gemm_status_t gemm_fp4_quantize(const void *X, const float *scale, uint8_t *Q, uint8_t *sf, int64_t M, int64_t K,
+                                int64_t ldx, int64_t ldq, gemm_fp4_t format, gemm_out_t x_type, gemm_layout_t layout,
+                                cudaStream_t stream) {
+    if (M < 0 || K < 0) return GEMM_ERR_INVALID_VALUE;
+    if (M > kMaxDim || K > kMaxDim) return GEMM_ERR_TOO_LARGE;
+    if (!valid_type(x_type) || !valid_layout(layout) || !valid_format(format) || K % 32) return GEMM_ERR_INVALID_VALUE;
+    if (format == GEMM_FP4_MX && scale) return GEMM_ERR_INVALID_VALUE;
+    if (M == 0 || K == 0) return GEMM_OK;
+    if (!X || !Q || !sf) return GEMM_ERR_INVALID_VALUE;
+    const bool mn = layout == GEMM_LAYOUT_MNMAJOR;
+    const int64_t sf_bytes = gemm_fp4_scale_bytes(M, K, format);
+    const Mat mx{X, mn ? K : M, mn ? M : K, ldx, size_of(x_type)};
+    const Mat mq{Q, M, K / 2, ldq, 1};
+    const Mat ms{sf, 1, sf_bytes, sf_bytes, 1};
+    const Mat mg{scale, 1, 1, 1, 4};
+    gemm_status_t s;
+    if ((s = check_mat(mx)) != GEMM_OK || (s = check_mat(mq)) != GEMM_OK) return s;
+    if (!aligned16(sf) || (reinterpret_cast<uintptr_t>(scale) & 3u)) return GEMM_ERR_MISALIGNED;
+    if (overlap(mq, mx) || overlap(mq, ms) || overlap(ms, mx) || overlap(mq, mg) || overlap(ms, mg)) return GEMM_ERR_ALIAS;
+    int dev, sm_count;
+    if ((s = b200::host::device(dev, sm_count, stream)) != GEMM_OK) return s;
+    const b200::Fp4QuantizeArgs a{X, scale, Q, sf, M, K, ldx, ldq, scale_tiles_k(K, format)};
+    if (format == GEMM_FP4_NV)
+        return x_type == GEMM_OUT_F32 ? launch_fp4_quantize<b200::kF32, true>(dev, a, layout, stream)
+                                      : launch_fp4_quantize<b200::kBF16, true>(dev, a, layout, stream);
+    return x_type == GEMM_OUT_F32 ? launch_fp4_quantize<b200::kF32, false>(dev, a, layout, stream)
+                                  : launch_fp4_quantize<b200::kBF16, false>(dev, a, layout, stream);
+}
+
+gemm_status_t gemm_fp4(const uint8_t *A, const uint8_t *sfa, const float *scale_a, const uint8_t *B, const uint8_t *sfb,
+                       const float *scale_b, void *C, int64_t M, int64_t N, int64_t K, int64_t lda, int64_t ldb,
+                       int64_t ldc, gemm_fp4_t format, gemm_out_t c_type, cudaStream_t stream) {
+    if (M < 0 || N < 0 || K < 0) return GEMM_ERR_INVALID_VALUE;
+    if (M > kMaxDim || N > kMaxDim || K > kMaxDim) return GEMM_ERR_TOO_LARGE;
+    if (!valid_type(c_type) || !valid_format(format) || K % 32) return GEMM_ERR_INVALID_VALUE;
+    if (format == GEMM_FP4_MX && (scale_a || scale_b)) return GEMM_ERR_INVALID_VALUE;
+    if (M == 0 || N == 0) return GEMM_OK;
+    const int64_t ec = size_of(c_type);
+    const Mat mc{C, M, N, ldc, ec};
+    gemm_status_t s;
+    if ((s = check_mat(mc)) != GEMM_OK) return s;
+    int dev, sm_count;
+    if (K == 0) {   // the empty sum
+        if ((s = b200::host::device(dev, sm_count, stream)) != GEMM_OK) return s;
+        const cudaError_t e = M == 1 ? cudaMemsetAsync(C, 0, static_cast<size_t>(N * ec), stream)
+                                     : cudaMemset2DAsync(C, static_cast<size_t>(ldc * ec), 0, static_cast<size_t>(N * ec),
+                                                         static_cast<size_t>(M), stream);
+        return e == cudaSuccess ? GEMM_OK : b200::host::cuda_fail(e);
+    }
+    const Mat ma{A, M, K / 2, lda, 1}, mb{B, N, K / 2, ldb, 1};
+    const int64_t na = gemm_fp4_scale_bytes(M, K, format), nb = gemm_fp4_scale_bytes(N, K, format);
+    const Mat sa{sfa, 1, na, na, 1}, sb{sfb, 1, nb, nb, 1}, ga{scale_a, 1, 1, 1, 4}, gb{scale_b, 1, 1, 1, 4};
+    for (const Mat *m : {&ma, &mb})
+        if ((s = check_mat(*m)) != GEMM_OK) return s;
+    if (!sfa || !sfb) return GEMM_ERR_INVALID_VALUE;
+    if (!aligned16(sfa) || !aligned16(sfb) || ((reinterpret_cast<uintptr_t>(scale_a) | reinterpret_cast<uintptr_t>(scale_b)) & 3u))
+        return GEMM_ERR_MISALIGNED;
+    // scale tiles are addressed by a 32-bit coordinate
+    if (na / b200::kScaleTile > kMaxDim || nb / b200::kScaleTile > kMaxDim) return GEMM_ERR_TOO_LARGE;
+    for (const Mat *m : {&ma, &mb, &sa, &sb, &ga, &gb})
+        if (overlap(mc, *m)) return GEMM_ERR_ALIAS;
+    DeviceStatus *status;
+    if ((s = b200::host::device_with_status(dev, sm_count, status, stream)) != GEMM_OK) return s;
+    Fp4Call c{ma, mb, sfa, sfb, format, {}};
+    c.args.ga = scale_a;
+    c.args.gb = scale_b;
+    c.args.c = C;
+    c.args.ldc = ldc;
+    c.args.M = static_cast<int>(M);
+    c.args.N = static_cast<int>(N);
+    c.args.K = static_cast<int>(K);
+    c.args.tiles_k = static_cast<int>(scale_tiles_k(K, format));
+    c.args.f32 = c_type == GEMM_OUT_F32;
+    c.args.status = status;
+    c.args.timeout_ns = b200::host::watchdog_ns(K);
+    return format == GEMM_FP4_NV ? dispatch_fp4<true>(dev, sm_count, c, stream)
+                                 : dispatch_fp4<false>(dev, sm_count, c, stream);
 }
 
 }  // extern "C"

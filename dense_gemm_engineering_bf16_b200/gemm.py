@@ -24,6 +24,8 @@ OUT_F32 = 0
 OUT_BF16 = 1
 KMAJOR = 0      # A as M x K, B as N x K
 MNMAJOR = 1     # A as K x M, B as K x N (row-major K x N)
+FP4_MX = 0      # blocks of 32, E8M0 scales
+FP4_NV = 1      # blocks of 16, E4M3 scales, one fp32 scale of the matrix
 ACT_NONE = 0
 ACT_RELU = 1
 ACT_GELU = 2
@@ -86,6 +88,12 @@ lib.gemm_bf16_grouped.argtypes = [_vp] * 4 + [_i64] * 8 + [_int, _int, _vp]
 lib.gemm_bf16_grouped.restype = _int
 lib.gemm_bf16_grouped_wgrad.argtypes = [_vp] * 4 + [_i64] * 8 + [_int, _int, ctypes.c_float, _vp]
 lib.gemm_bf16_grouped_wgrad.restype = _int
+lib.gemm_fp4_scale_bytes.argtypes = [_i64, _i64, _int]
+lib.gemm_fp4_scale_bytes.restype = _i64
+lib.gemm_fp4_quantize.argtypes = [_vp] * 4 + [_i64] * 4 + [_int, _int, _int, _vp]
+lib.gemm_fp4_quantize.restype = _int
+lib.gemm_fp4.argtypes = [_vp] * 7 + [_i64] * 6 + [_int, _int, _vp]
+lib.gemm_fp4.restype = _int
 lib.gemm_check_device_status.argtypes = [_vp]
 lib.gemm_check_device_status.restype = _int
 lib.gemm_last_timeout_detail.argtypes = [ctypes.POINTER(ctypes.c_int32), ctypes.POINTER(ctypes.c_int32)]
@@ -220,6 +228,9 @@ def _here(stream):
                         lambda dev: torch.cuda.current_stream(dev).cuda_stream)
         _DTYPES.update({OUT_F32: (torch.float32,), OUT_BF16: (torch.bfloat16,), "bytes": (torch.uint8,),
                         "ints": (torch.int32,),
+                        "fp4": (torch.uint8,) + ((torch.float4_e2m1fn_x2,) if hasattr(torch, "float4_e2m1fn_x2") else ()),
+                        FP4_MX + 2: (torch.float8_e8m0fnu, torch.uint8),
+                        FP4_NV + 2: (torch.float8_e4m3fn, torch.uint8),
                         "codes": (torch.float8_e4m3fn, torch.uint8), "scales": (torch.float8_e8m0fnu, torch.uint8),
                         "device": device, "stream": queue})
     if stream is not None:
@@ -385,6 +396,47 @@ def gemm_bf16_grouped_wgrad(dC, A, ends, dB, groups: int, M: int, N: int, K: int
     except GemmError as e:
         return _refused(e, check)
     return _check(st, "gemm_bf16_grouped_wgrad", check)
+
+
+def gemm_fp4_scale_bytes(rows: int, K: int, format: int) -> int:
+    """Bytes of the tiled scales of a rows x K matrix in 4 bits."""
+    return int(lib.gemm_fp4_scale_bytes(rows, K, int(format)))
+
+
+def gemm_fp4_quantize(X, scale, Q, sf, M: int, K: int, ldx: int, ldq: int, format: int = FP4_NV, x_type: int = OUT_BF16,
+                      layout: int = KMAJOR, stream=None, check: bool = True) -> int:
+    """E2M1 codes Q (M x ldq bytes, two each, even k in the low half) and tiled
+    scales sf (gemm_fp4_scale_bytes) of X, stored M x K (KMAJOR) or K x M
+    (MNMAJOR): an operand of gemm_fp4.  scale: FP4_NV's scale of the matrix, one
+    float on the device, or None (see include/b200gemm.h, gemm_fp4_quantize)."""
+    try:
+        dev, queue = _here(stream)
+        st = lib.gemm_fp4_quantize(_operand(X, x_type, dev, "gemm_fp4_quantize: X"),
+                                   _operand(scale, OUT_F32, dev, "gemm_fp4_quantize: scale", True),
+                                   _operand(Q, "fp4", dev, "gemm_fp4_quantize: Q"),
+                                   _operand(sf, format + 2, dev, "gemm_fp4_quantize: sf", True), M, K, ldx, ldq,
+                                   int(format), int(x_type), int(layout), queue)
+    except GemmError as e:
+        return _refused(e, check)
+    return _check(st, "gemm_fp4_quantize", check)
+
+
+def gemm_fp4(A, sfa, scale_a, B, sfb, scale_b, C, M: int, N: int, K: int, lda: int, ldb: int, ldc: int,
+             format: int = FP4_NV, c_type: int = OUT_F32, stream=None, check: bool = True) -> int:
+    """C = ga gb (sa.A).(sb.B)^T: E2M1 codes A (M x lda bytes) and B (N x ldb),
+    tiled scales sfa and sfb, FP4_NV's scales of the matrices scale_a and
+    scale_b (one float each on the device, or None), C M x N (see
+    include/b200gemm.h, gemm_fp4)."""
+    try:
+        dev, queue = _here(stream)
+        st = lib.gemm_fp4(_operand(A, "fp4", dev, "gemm_fp4: A"), _operand(sfa, format + 2, dev, "gemm_fp4: sfa", True),
+                          _operand(scale_a, OUT_F32, dev, "gemm_fp4: scale_a", True), _operand(B, "fp4", dev, "gemm_fp4: B"),
+                          _operand(sfb, format + 2, dev, "gemm_fp4: sfb", True),
+                          _operand(scale_b, OUT_F32, dev, "gemm_fp4: scale_b", True), _operand(C, c_type, dev, "gemm_fp4: C"),
+                          M, N, K, lda, ldb, ldc, int(format), int(c_type), queue)
+    except GemmError as e:
+        return _refused(e, check)
+    return _check(st, "gemm_fp4", check)
 
 
 def gemm_check_device_status(stream=None, check: bool = True) -> int:

@@ -504,6 +504,77 @@ B200GEMM_API gemm_status_t gemm_bf16_grouped_wgrad(const void *dC, const void *A
                                                    int64_t lda, int64_t lddb, int64_t stridedb, gemm_out_t db_type,
                                                    gemm_layout_t db_layout, float beta, cudaStream_t stream);
 
+/*
+ * 4-bit floating point: E2M1 codes (0, 0.5, 1, 1.5, 2, 3, 4, 6 and their
+ * negatives), two a byte, with one scale per block of consecutive K elements
+ * of a row.
+ */
+typedef enum {
+    GEMM_FP4_MX = 0,                /* blocks of 32, scales 2^e as E8M0 bytes (e + 127) */
+    GEMM_FP4_NV = 1                 /* blocks of 16, scales as E4M3 bytes, under one fp32 scale of
+                                       the whole matrix */
+} gemm_fp4_t;
+
+/*
+ * Scales are kept as the tensor cores take them, so that a product need not lay
+ * them out: tiles of 128 rows x 4 blocks, 512 bytes each.  The scale of row i
+ * and block b is byte
+ *
+ *   512 ((i/128) T + b/4) + 16 (i%32) + 4 (i%128/32) + b%4,   T = ceil(blocks of a row / 4)
+ *
+ * and gemm_fp4_scale_bytes(rows, K, format) = 512 ceil(rows/128) T the length of
+ * all (0 for an empty matrix or a bad argument).  Where a row's blocks end inside
+ * a tile, its other bytes there must not be NaN; the quantiser writes 0.  Bytes
+ * of rows past the last are neither written nor do they count.
+ */
+B200GEMM_API int64_t gemm_fp4_scale_bytes(int64_t rows, int64_t K, gemm_fp4_t format);
+
+/*
+ * gemm_fp4_quantize: an operand of gemm_fp4 from a bf16 or fp32 matrix.
+ *
+ *   MX  scale 2^e, the smallest with |x| <= 6 * 2^e in the block, -127 <= e <= 127
+ *       (nothing saturates); code E2M1(x / 2^e)
+ *   NV  scale s = E4M3(max |x| / (6 g)), at least 2^-9, at most 448, with g =
+ *       *scale; code E2M1(x / (s g)).  E4M3 rounds to nearest, so a block's largest
+ *       values may saturate by up to a sixteenth
+ *
+ * all to nearest even, each step rounded to fp32 (6 g, the quotients, s g);
+ * beyond 6 a code is 6, and a zero's sign means nothing.  A block with a NaN or an infinity gets the scale's NaN
+ * byte (0xFF; 0x7F), its codes mean nothing.
+ *   X       layout K-major: M x K, element (i, k) at X[i ldx + k].  MN-major:
+ *           K x M, element (i, k) at X[k ldx + i]: the transposed operand
+ *   scale   NV: one float on the device, positive, 2^-100 to 2^100, usually
+ *           max |X| / 2688 (= 6 * 448) as calibrated; NULL: 1.  MX: NULL
+ *   Q       M x ldq bytes: element k is byte k/2's low half for even k, its high
+ *           half for odd k
+ *   sf      gemm_fp4_scale_bytes(M, K, format) bytes, 16-byte aligned
+ * K must be a multiple of 32.  Q and sf overlap no other operand.  M == 0 or K ==
+ * 0: nothing to do.  One kernel.
+ */
+B200GEMM_API gemm_status_t gemm_fp4_quantize(const void *X, const float *scale, uint8_t *Q, uint8_t *sf, int64_t M,
+                                             int64_t K, int64_t ldx, int64_t ldq, gemm_fp4_t format, gemm_out_t x_type,
+                                             gemm_layout_t layout, cudaStream_t stream);
+
+/*
+ * gemm_fp4: the product of two such matrices,
+ *
+ *   C[i][j] = ga gb sum_k (a_ik sa_i,k/block) (b_jk sb_j,k/block)
+ *
+ *   A, sfa, scale_a   M x lda bytes of codes, their scales, NV: the matrix's
+ *                     scale (on the device; NULL: 1.  MX: NULL)
+ *   B, sfb, scale_b   the same, N x ldb (stored K-major)
+ *   C                 M x N of c_type
+ * Both operands have the same format.  K must be a multiple of 32, lda and ldb
+ * of 16, all pointers to codes, scales and C 16-byte aligned.  Products are exact,
+ * sums fp32 in a fixed order, times ga gb in fp32, rounded once.  C overlaps no
+ * input.  M == 0 or N == 0: nothing to do; K == 0: C = 0.  One kernel, no
+ * workspace; the status block and the watchdog as for the products.
+ */
+B200GEMM_API gemm_status_t gemm_fp4(const uint8_t *A, const uint8_t *sfa, const float *scale_a, const uint8_t *B,
+                                    const uint8_t *sfb, const float *scale_b, void *C, int64_t M, int64_t N, int64_t K,
+                                    int64_t lda, int64_t ldb, int64_t ldc, gemm_fp4_t format, gemm_out_t c_type,
+                                    cudaStream_t stream);
+
 /* Synchronises `stream`, then reports and clears the device watchdog status
  * of the current device (the status blocks of every entry point, the static
  * one of gemm_bf16_noalloc included): GEMM_OK, or GEMM_ERR_TIMEOUT if a
