@@ -1,6 +1,16 @@
 // Write-back of products whose accumulator lies the other way round than C: a
-// TMEM lane is a column of C, a TMEM column one of its rows.  A warp holds 32
-// columns of C; each of its stores covers consecutive columns of a row.
+// TMEM lane is a column of C, a TMEM column one of its rows.  Four warps, one per
+// lane quarter, hold 128 columns of C.
+//
+// bf16: tcgen05.ld 16x256b gives a thread two neighbouring rows of one column;
+// packed, they are a fragment that stmatrix.trans writes to shared memory as
+// rows, from where they go out as 16 bytes a lane, whole lines of 128 bytes: about
+// 50 instructions for 32 x 32 values.  (Straight from the registers, a column a
+// lane, they took 400: with two such warps per scheduler that, not memory, was
+// the time, 5.6 us for a 256 x 256 tile.  One bulk copy per row of 256 bytes is
+// bound by the copies, about 20 cycles each.)
+//
+// fp32: a lane's column straight from its registers, a line per row and warp.
 #pragma once
 #include <cuda_bf16.h>
 
@@ -11,50 +21,122 @@
 
 namespace b200 {
 
-// W rows of C (from `c` on, the row of v[0], `ld` elements apart, the first
-// `rows` of them written) x the warp's 32 columns, of which this lane holds
-// column `col`: C = v + beta * C, rounded once.  Rows are 4-byte aligned (16 in
-// fact) and the warp's first column is even.  bf16: neighbouring lanes trade
-// halves, so that each holds two columns of one row and a store writes two rows
-// of 64 bytes; half as many stores as with 16 bits a lane.
-template <int W>
-__device__ __forceinline__ void store_columns(void *c, int64_t ld, int rows, int col, int cols, bool f32, float beta,
-                                              float (&v)[W]) {
-    const bool mine = col < cols;
-    if (f32) {
-        float *p = static_cast<float *>(c) + col;
+// 16 lanes x 32 columns: thread t gets of lane t / 4 (and t / 4 + 8) the columns
+// 8 i + 2 (t % 4) and the next in r[4 i], r[4 i + 1] (r[4 i + 2], r[4 i + 3]).
+__device__ __forceinline__ void tmem_ld_16x256b_x4(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+}
+
+__device__ __forceinline__ void stmatrix_x4_trans(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};"
+                 ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d)
+                 : "memory");
+}
+
+// 32 rows x 32 columns of this warp as packed bf16: `from` its quarter's first
+// row in TMEM; w[8 h + 2 i + p] has lanes 16 h + 8 p + t / 4, rows 8 i + 2 (t % 4).
+__device__ __forceinline__ void load_rows_bf16(uint32_t from, float alpha, uint32_t (&w)[16]) {
+    uint32_t lo[16], hi[16];
+    tmem_ld_16x256b_x4(from, lo);
+    tmem_ld_16x256b_x4(from + (16u << 16), hi);
+    tmem_ld_wait();
 #pragma unroll
-        for (int j = 0; j < W; ++j) {
-            if (j < rows && mine) {
-                if (beta != 0.0f) v[j] = fmaf(beta, *p, v[j]);
-                *p = v[j];
+    for (int i = 0; i < 8; ++i) {
+        w[i] = pack_bf16x2(alpha * __uint_as_float(lo[2 * i]), alpha * __uint_as_float(lo[2 * i + 1]));
+        w[8 + i] = pack_bf16x2(alpha * __uint_as_float(hi[2 * i]), alpha * __uint_as_float(hi[2 * i + 1]));
+    }
+}
+
+constexpr int kOutHalf = 32 * 128;              // 32 rows x 64 columns of bf16
+constexpr int kOutBytes = 2 * 2 * kOutHalf;     // two buffers of 128 columns for each four warps
+
+// Where a warp's bf16 rows go.  The warps of two neighbouring quarters share 64
+// columns, a line of 128 bytes per row; they call every member together.
+struct ColumnsOut {
+    uint32_t buffer;        // the two warps' shared memory: two of kOutHalf bytes
+    uint32_t barrier;       // their named barrier
+    uint32_t quarter, lane;
+    int64_t ld_bytes;
+    int cols;               // of C from the four warps' first one on; may be none
+    uint32_t turn;
+
+    __device__ __forceinline__ ColumnsOut(uint32_t base, uint32_t part, uint32_t sub, uint32_t lane_, int64_t ld)
+        : buffer(base + part * kOutBytes + sub / 2 * 2 * kOutHalf), barrier(1 + 2 * part + sub / 2), quarter(sub),
+          lane(lane_), ld_bytes(ld), cols(0), turn(0) {}
+
+    // Whether neither warp failed.
+    __device__ __forceinline__ bool agree(bool ok) {
+        uint32_t both;
+        asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+                     "barrier.red.and.pred q, %2, 64, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+                     : "=r"(both) : "r"(ok ? 1u : 0u), "r"(barrier) : "memory");
+        return both != 0;
+    }
+
+    // 32 rows from load_rows_bf16, the first `count` of them to C's from `c` on
+    // (the four warps' first column).  Rows are 128 bytes in shared memory, their
+    // 16-byte pieces swapped by row, so that neither direction has bank
+    // conflicts.  The barrier also says that both warps have read the other
+    // buffer, which the next rows go to.
+    __device__ __forceinline__ void rows(const uint32_t (&w)[16], uint8_t *c, int count) {
+        const uint32_t at = buffer + turn * kOutHalf;
+        // matrix m of a store: rows of C 8 (m / 2) .., columns 8 (m % 2) .. of 16
+        const uint32_t m = lane >> 3, r0 = 8 * (m >> 1) + (lane & 7), piece = 4 * (quarter & 1) + (m & 1);
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int i = 0; i < 4; i += 2)
+                stmatrix_x4_trans(at + (r0 + 8 * i) * 128 + (((piece + 2 * h) ^ (r0 & 7)) << 4), w[8 * h + 2 * i],
+                                  w[8 * h + 2 * i + 1], w[8 * h + 2 * i + 2], w[8 * h + 2 * i + 3]);
+        asm volatile("bar.sync %0, 64;" ::"r"(barrier) : "memory");
+        const int col = 64 * (quarter >> 1) + 8 * (lane & 7), left = cols - col;
+        int r = 16 * (quarter & 1) + (lane >> 3);
+        uint8_t *p = c + r * ld_bytes + 2 * col;
+#pragma unroll
+        for (int i = 0; i < 4; ++i, r += 4, p += 4 * ld_bytes) {
+            uint32_t v[4];
+            ld_shared_v4(at + r * 128 + (((lane & 7) ^ (r & 7)) << 4), v[0], v[1], v[2], v[3]);
+            if (r < count && left > 0) {
+                if (left >= 8) {
+                    *reinterpret_cast<uint4 *>(p) = make_uint4(v[0], v[1], v[2], v[3]);
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 7; ++k)
+                        if (k < left) reinterpret_cast<uint16_t *>(p)[k] = static_cast<uint16_t>(v[k / 2] >> 16 * (k & 1));
+                }
             }
-            p += ld;
         }
+        turn ^= 1u;
+    }
+};
+
+// W rows of C straight from the registers, a column a lane (`mine`: it is C's):
+// the first `rows` of them, C = v + beta * C, rounded once.
+template <int W>
+__device__ __forceinline__ void store_columns(uint8_t *c, int64_t ld_bytes, int rows, bool mine, bool f32, float beta,
+                                              const float *v) {
+    if (!mine) return;
+    if (f32 && beta == 0.0f) {
+#pragma unroll
+        for (int j = 0; j < W; ++j, c += ld_bytes)
+            if (j < rows) *reinterpret_cast<float *>(c) = v[j];
         return;
     }
-    if (beta != 0.0f) {
-        const __nv_bfloat16 *p = static_cast<const __nv_bfloat16 *>(c) + col;
 #pragma unroll
-        for (int j = 0; j < W; ++j) {
-            if (j < rows && mine) v[j] = fmaf(beta, __bfloat162float(*p), v[j]);
-            p += ld;
+    for (int j = 0; j < W; ++j, c += ld_bytes) {
+        if (j >= rows) break;
+        if (f32) {
+            float *p = reinterpret_cast<float *>(c);
+            *p = fmaf(beta, *p, v[j]);
+        } else {
+            __nv_bfloat16 *p = reinterpret_cast<__nv_bfloat16 *>(c);
+            *p = __float2bfloat16_rn(beta != 0.0f ? fmaf(beta, __bfloat162float(*p), v[j]) : v[j]);
         }
-        __syncwarp();   // a neighbour may overwrite what this lane read
-    }
-    const bool odd = col & 1;
-    uint16_t *p = static_cast<uint16_t *>(c) + (odd ? ld : 0) + (col & ~1);
-    const bool pair = (col | 1) < cols, single = (col & ~1) < cols;
-#pragma unroll
-    for (int j = 0; j < W; j += 2) {
-        const uint32_t own = pack_bf16x2(v[j], v[j + 1]);
-        const uint32_t other = __shfl_xor_sync(0xFFFFFFFFu, own, 1);
-        const uint32_t w = odd ? __byte_perm(other, own, 0x7632) : __byte_perm(own, other, 0x5410);
-        if (j + (odd ? 1 : 0) < rows) {
-            if (pair) *reinterpret_cast<uint32_t *>(p) = w;
-            else if (single) *p = static_cast<uint16_t>(w);
-        }
-        p += 2 * ld;
     }
 }
 

@@ -60,7 +60,8 @@ struct GemmFp4Cfg {
     // full[S], empty[S], tmem_full[2], tmem_empty[2], sf_full[slots], sf_empty[slots], received
     static constexpr int NUM_BARS = 2 * STAGES + 4 + 2 * SF_SLOTS + 1;
     static constexpr int BAR_OFF = STAGES * STAGE_BYTES;
-    static constexpr int PART_OFF = BAR_OFF + (NUM_BARS * 8 + 8 + 127) / 128 * 128;   // other members' partials
+    static constexpr int OUT_OFF = BAR_OFF + (NUM_BARS * 8 + 8 + 127) / 128 * 128;    // + TMEM address, abort flag
+    static constexpr int PART_OFF = OUT_OFF + EPI_WARPS / 4 * kOutBytes;              // other members' partials
     static constexpr int SMEM_BYTES = 1024 + PART_OFF + (SPLIT ? BQ * 128 * 4 : 0);
     static_assert(TMEM_COLS <= 512 && STAGE_BYTES % 1024 == 0 && SMEM_BYTES <= 232448, "it fits");
     static_assert(!SPLIT || (CG == 1 && EPI_WARPS == 4), "split: one-CTA tiles");
@@ -291,8 +292,12 @@ gemm_fp4_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__
         // ----------------------------------------------------- epilogue --
         const uint32_t sub = warp & 3u;                         // TMEM lane quarter
         const int part = static_cast<int>(warp - Cfg::EPI0) / 4;
+        constexpr int PARTS = Cfg::EPI_WARPS / 4;               // fours of warps that share a tile's rows of C
+        constexpr int CHUNKS = Cfg::BQ / 32 / PARTS;            // of 32 rows, for each of them
         const float alpha = (a.ga ? __ldg(a.ga) : 1.0f) * (a.gb ? __ldg(a.gb) : 1.0f);
         const int64_t esize = a.f32 ? 4 : 2;
+        ColumnsOut to(base + Cfg::OUT_OFF, part, sub, lane, a.ldc * esize);
+        const int mine = static_cast<int>(sub * 32u + lane);   // this lane's column
         uint32_t done = 0;
         for (int tile = first; tile < num_tiles; tile += step, ++done) {
             int tq, tp;
@@ -304,12 +309,13 @@ gemm_fp4_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__
                 ready = 0;
             }
             ready = __shfl_sync(0xFFFFFFFFu, ready, 0);
-            if (!ready) break;
+            if (!to.agree(ready != 0)) break;
             tc_fence_after_sync();
             const uint32_t acc = tmem_base + ((sub * 32u) << 16) + buf * Cfg::BQ;
-            const int col = tp * Cfg::BP + static_cast<int>(rank) * Cfg::BP_CTA + static_cast<int>(sub * 32u + lane);
+            const int col0 = tp * Cfg::BP + static_cast<int>(rank) * Cfg::BP_CTA;
             const int count = min(Cfg::BQ, a.M - tq * Cfg::BQ);
-            uint8_t *out = static_cast<uint8_t *>(a.c) + tq * Cfg::BQ * a.ldc * esize;
+            uint8_t *out = static_cast<uint8_t *>(a.c) + (static_cast<int64_t>(tq) * Cfg::BQ * a.ldc + col0) * esize;
+            to.cols = a.N - col0;
             auto release = [&]() {
                 tc_fence_before_sync();
                 __syncwarp();
@@ -321,7 +327,6 @@ gemm_fp4_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__
             if (Cfg::SPLIT && members > 1) {
                 // Rows of C in fours; member o sums fours [o share, (o + 1) share).
                 const int fours = mma_n(tq) / 4, share = (fours + static_cast<int>(members) - 1) / static_cast<int>(members);
-                const uint32_t mine = sub * 32u + lane;
                 for (int f = 0; f < fours; f += 8) {
                     uint32_t r[32];
                     tmem_ld_32x32b_x32(acc + 4 * f, r);
@@ -330,7 +335,7 @@ gemm_fp4_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__
                     for (int i = 0; i < 8; ++i) {
                         const uint32_t owner = static_cast<uint32_t>((f + i) / share);
                         if (f + i < fours && owner != me) {
-                            const uint32_t at = (me * share + (f + i) - owner * share) * 128u + mine;
+                            const uint32_t at = (me * share + (f + i) - owner * share) * 128u + sub * 32u + lane;
                             store_cluster_v4(map_to_cta(base + Cfg::PART_OFF + 16u * at, owner), r[4 * i], r[4 * i + 1],
                                              r[4 * i + 2], r[4 * i + 3]);
                         }
@@ -354,42 +359,59 @@ gemm_fp4_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__
                     for (uint32_t m = 0; m < members; ++m) {
                         uint32_t x[4] = {own[0], own[1], own[2], own[3]};
                         if (m != me)
-                            ld_shared_v4(base + Cfg::PART_OFF + 16u * ((m * share + f - me * share) * 128u + mine), x[0],
+                            ld_shared_v4(base + Cfg::PART_OFF + 16u * ((m * share + f - me * share) * 128u + sub * 32u + lane), x[0],
                                          x[1], x[2], x[3]);
 #pragma unroll
                         for (int i = 0; i < 4; ++i) v[i] += __uint_as_float(x[i]);
                     }
 #pragma unroll
                     for (int i = 0; i < 4; ++i) v[i] *= alpha;
-                    store_columns<4>(out + 4 * f * a.ldc * esize, a.ldc, count - 4 * f, col, a.N, a.f32, 0.0f, v);
+                    store_columns<4>(out + 4 * f * to.ld_bytes + mine * esize, to.ld_bytes, count - 4 * f,
+                                     mine < to.cols, a.f32, 0.0f, v);
                 }
                 release();
-            } else if constexpr (Cfg::ACC_BUFS == 2) {
-                for (int j = 32 * part; j < count; j += 8 * Cfg::EPI_WARPS) {
+                continue;
+            }
+            // A single accumulator goes into registers whole, so that the next
+            // tile's MMAs wait for that alone.
+            constexpr int HELD = Cfg::ACC_BUFS == 1 ? CHUNKS : 1;
+            if (a.f32) {
+                float v[HELD][32];
+#pragma unroll
+                for (int chunk = 0; chunk < CHUNKS; ++chunk) {
                     uint32_t r[32];
-                    float v[32];
-                    tmem_ld_32x32b_x32(acc + j, r);
+                    tmem_ld_32x32b_x32(acc + 32 * (chunk * PARTS + part), r);
                     tmem_ld_wait();
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) v[i] = alpha * __uint_as_float(r[i]);
-                    store_columns<32>(out + j * a.ldc * esize, a.ldc, count - j, col, a.N, a.f32, 0.0f, v);
+                    for (int i = 0; i < 32; ++i) v[chunk % HELD][i] = alpha * __uint_as_float(r[i]);
+                    if (HELD > 1) continue;
+                    const int j = 32 * (chunk * PARTS + part);
+                    store_columns<32>(out + j * to.ld_bytes + mine * esize, to.ld_bytes, count - j, mine < to.cols, true,
+                                      0.0f, v[0]);
                 }
                 release();
+                if (HELD > 1)
+#pragma unroll
+                    for (int chunk = 0; chunk < CHUNKS; ++chunk) {
+                        const int j = 32 * (chunk * PARTS + part);
+                        store_columns<32>(out + j * to.ld_bytes + mine * esize, to.ld_bytes, count - j, mine < to.cols,
+                                          true, 0.0f, v[chunk % HELD]);
+                    }
             } else {
-                // one accumulator: everything into registers, TMEM handed back, then stored
-                float v[128];
-                const int j0 = 128 * part;
+                uint32_t w[HELD][16];
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    uint32_t r[32];
-                    tmem_ld_32x32b_x32(acc + j0 + 32 * c, r);
-                    tmem_ld_wait();
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) v[32 * c + i] = alpha * __uint_as_float(r[i]);
+                for (int chunk = 0; chunk < CHUNKS; ++chunk) {
+                    const int j = 32 * (chunk * PARTS + part);
+                    load_rows_bf16(acc + j, alpha, w[chunk % HELD]);
+                    if (HELD == 1 && j < count) to.rows(w[0], out + j * to.ld_bytes, count - j);
                 }
                 release();
-                if (j0 < count)
-                    store_columns<128>(out + j0 * a.ldc * esize, a.ldc, count - j0, col, a.N, a.f32, 0.0f, v);
+                if (HELD > 1)
+#pragma unroll
+                    for (int chunk = 0; chunk < CHUNKS; ++chunk) {
+                        const int j = 32 * (chunk * PARTS + part);
+                        if (j < count) to.rows(w[chunk % HELD], out + j * to.ld_bytes, count - j);
+                    }
             }
         }
     }

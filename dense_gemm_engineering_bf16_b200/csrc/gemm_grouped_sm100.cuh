@@ -23,7 +23,7 @@
 //              zeroes the foreign rows up to the MMA's next step of 16 in both
 //              operands and hands the block on.
 //   the rest   epilogue: TMEM to registers to global memory (columns_out.cuh),
-//              double-buffered against the next tile's MMAs
+//              which overlaps the next tile's MMAs
 //
 // Every CTA works out the tiles from `ends` itself: the numbers of tiles up to
 // each expert in shared memory, a binary search per tile.  Rows outside every
@@ -66,7 +66,8 @@ struct GroupedCfg {
     // full[S], empty[S], fix[S] (gradient), tmem_full[2], tmem_empty[2]
     static constexpr int NUM_BARS = (MODE == kGroupedGrad ? 3 : 2) * STAGES + 4;
     static constexpr int BAR_OFF = STAGES * STAGE_BYTES;
-    static constexpr int TABLE_OFF = BAR_OFF + NUM_BARS * 8 + 16;    // + TMEM address, abort flag
+    static constexpr int OUT_OFF = BAR_OFF + (NUM_BARS * 8 + 8 + 127) / 128 * 128;    // + TMEM address, abort flag
+    static constexpr int TABLE_OFF = OUT_OFF + EPI_WARPS / 4 * kOutBytes;
     static constexpr int TMEM_COLS = pow2_at_least(2 * BQ, 32);
     static constexpr int smem_bytes(int groups) { return 1024 + TABLE_OFF + 8 * groups; }
 
@@ -83,6 +84,7 @@ struct GroupedArgs {
     int P, Q, K;                // P's extent (columns of the output); gradient: Q's (its rows); rows: K
     float beta;                 // gradient
     bool f32;                   // type of the output
+    int segment;                // blocks of the reduction that the tensor core sums by itself
     DeviceStatus *status;
     uint64_t timeout_ns;
 };
@@ -91,6 +93,12 @@ struct GroupedArgs {
 // gradient: rows of the output), `n` the MMA's N, reduction from k0 over k_len.
 struct GroupedTile {
     int group, p0, q0, count, n, k0, k_len;
+
+    // for the warps that issue copies and MMAs
+    __device__ __forceinline__ GroupedTile uniform() const {
+        return {b200::uniform(group), b200::uniform(p0), b200::uniform(q0), b200::uniform(count), b200::uniform(n),
+                b200::uniform(k0), b200::uniform(k_len)};
+    }
 };
 
 template <class Cfg>
@@ -141,7 +149,7 @@ gemm_grouped_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_consta
     const uint32_t raw = smem_addr(smem_raw);
     uint8_t *smem = smem_raw + ((1024u - (raw & 1023u)) & 1023u);
     const uint32_t base = smem_addr(smem);
-    const uint32_t warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const uint32_t warp = uniform(threadIdx.x / 32), lane = threadIdx.x % 32;
     const uint32_t rank = CG == 2 ? cluster_cta_rank() : 0u;
 
     const uint32_t bar0 = base + Cfg::BAR_OFF;
@@ -204,110 +212,129 @@ gemm_grouped_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_consta
 
     if (warp == 0) {
         // ------------------------------------------------ TMA producer --
-        if (lane == 0) {
-            uint32_t stage = 0, phase = 0;
-            bool ok = true;
-            for (int tile = first; ok && tile < num_tiles; tile += step) {
-                const GroupedTile t = grouped_tile<Cfg>(tile, a, ends, tiles);
-                const int p = t.p0 + static_cast<int>(rank) * Cfg::BP_CTA;
-                const int q_cta = t.n / CG, q = t.q0 + static_cast<int>(rank) * q_cta;
-                const int boxes = (q_cta + Cfg::QBOX - 1) / Cfg::QBOX;
-                const uint32_t bytes = Cfg::P_BYTES + boxes * Cfg::QBOX * Cfg::BK * 2;
-                const int blocks = (t.k_len + Cfg::BK - 1) / Cfg::BK;
-                for (int kb = 0; kb < blocks; ++kb) {
-                    if (!mbar_wait(empty_bar(stage), phase ^ 1u, abort_flag, 2 * a.timeout_ns)) {
-                        record_timeout(a.status, abort_flag, abort_slot, CG, kRoleProducer * 16 + kBarEmpty);
-                        ok = false;
-                        break;
-                    }
-                    const uint32_t p_dst = base + stage * Cfg::STAGE_BYTES, q_dst = p_dst + Cfg::P_BYTES;
-                    const int k = t.k0 + kb * Cfg::BK;
-                    if (GRAD && (t.k_len - kb * Cfg::BK) < Cfg::BK && t.k_len % 16 != 0) {
+        const bool issue = elect_one();
+        uint32_t stage = 0, phase = 0;
+        bool ok = true;
+        for (int tile = first; ok && tile < num_tiles; tile += step) {
+            const GroupedTile t = grouped_tile<Cfg>(tile, a, ends, tiles).uniform();
+            const int p = t.p0 + static_cast<int>(rank) * Cfg::BP_CTA;
+            const int q_cta = t.n / CG, q = t.q0 + static_cast<int>(rank) * q_cta;
+            const int boxes = (q_cta + Cfg::QBOX - 1) / Cfg::QBOX;
+            const uint32_t bytes = Cfg::P_BYTES + boxes * Cfg::QBOX * Cfg::BK * 2;
+            int k = t.k0;
+            for (int left = t.k_len; left > 0; left -= Cfg::BK, k += Cfg::BK) {
+                if (!mbar_wait_warp(empty_bar(stage), phase ^ 1u, abort_flag, 2 * a.timeout_ns)) {
+                    if (issue) record_timeout(a.status, abort_flag, abort_slot, CG, kRoleProducer * 16 + kBarEmpty);
+                    ok = false;
+                    break;
+                }
+                const uint32_t p_dst = base + stage * Cfg::STAGE_BYTES, q_dst = p_dst + Cfg::P_BYTES;
+                if (GRAD && left < Cfg::BK && left % 16 != 0) {     // through warp 2
+                    if (issue) {
                         const uint32_t bar = fix_bar(stage);
                         mbar_arrive_expect_tx(bar, bytes);
                         tma_load_2d(p_dst, &tmP, bar, p, k);
                         tma_load_2d(p_dst + 8192u, &tmP, bar, p + 64, k);
                         for (int b = 0; b < boxes; ++b) tma_load_2d(q_dst + 8192u * b, &tmQ, bar, q + 64 * b, k);
-                    } else {
-                        if (rank == 0) mbar_arrive_expect_tx(full_bar(stage), CG * bytes);
-                        else if (GRAD) mbar_arrive_cluster(map_to_cta(full_bar(stage), 0));
-                        const uint32_t bar = CG == 2 ? map_to_cta(full_bar(stage), 0) : full_bar(stage);
-                        auto load2 = [&](uint32_t dst, const CUtensorMap *m, int x, int y) {
-                            if constexpr (CG == 1) tma_load_2d(dst, m, bar, x, y);
-                            else tma_load_2d_pair(dst, m, bar, x, y);
-                        };
-                        auto load3 = [&](uint32_t dst, const CUtensorMap *m, int x, int y, int z) {
-                            if constexpr (CG == 1) tma_load_3d(dst, m, bar, x, y, z);
-                            else tma_load_3d_pair(dst, m, bar, x, y, z);
-                        };
-                        if constexpr (GRAD) {
-                            load2(p_dst, &tmP, p, k);
-                            load2(p_dst + 8192u, &tmP, p + 64, k);
-                            for (int b = 0; b < boxes; ++b) load2(q_dst + 8192u * b, &tmQ, q + 64 * b, k);
-                        } else {
-                            if constexpr (Cfg::PMN) {
-                                load3(p_dst, &tmP, p, k, t.group);
-                                load3(p_dst + 8192u, &tmP, p + 64, k, t.group);
-                            } else {
-                                load3(p_dst, &tmP, k, p, t.group);
-                            }
-                            for (int b = 0; b < boxes; ++b)
-                                load2(q_dst + Cfg::QBOX * 128u * b, &tmQ, k, q + Cfg::QBOX * b);
-                        }
                     }
-                    if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+                } else if (issue) {
+                    // bytes are counted by the pair's leader
+                    if (rank == 0) mbar_arrive_expect_tx(full_bar(stage), CG * bytes);
+                    else if (GRAD) mbar_arrive_cluster_relaxed(map_to_cta(full_bar(stage), 0));
+                    const uint32_t bar = CG == 2 ? map_to_cta(full_bar(stage), 0) : full_bar(stage);
+                    auto load2 = [&](uint32_t dst, const CUtensorMap *m, int x, int y) {
+                        if constexpr (CG == 1) tma_load_2d(dst, m, bar, x, y);
+                        else tma_load_2d_pair(dst, m, bar, x, y);
+                    };
+                    auto load3 = [&](uint32_t dst, const CUtensorMap *m, int x, int y, int z) {
+                        if constexpr (CG == 1) tma_load_3d(dst, m, bar, x, y, z);
+                        else tma_load_3d_pair(dst, m, bar, x, y, z);
+                    };
+                    if constexpr (GRAD) {
+                        load2(p_dst, &tmP, p, k);
+                        load2(p_dst + 8192u, &tmP, p + 64, k);
+                        for (int b = 0; b < boxes; ++b) load2(q_dst + 8192u * b, &tmQ, q + 64 * b, k);
+                    } else {
+                        if constexpr (Cfg::PMN) {
+                            load3(p_dst, &tmP, p, k, t.group);
+                            load3(p_dst + 8192u, &tmP, p + 64, k, t.group);
+                        } else {
+                            load3(p_dst, &tmP, k, p, t.group);
+                        }
+                        for (int b = 0; b < boxes; ++b) load2(q_dst + Cfg::QBOX * 128u * b, &tmQ, k, q + Cfg::QBOX * b);
+                    }
                 }
-            }
-            // the MMAs' last releases must land before this CTA exits
-            for (int i = 0; ok && i < STAGES; ++i) {
-                if (!mbar_wait(empty_bar(stage), phase ^ 1u, abort_flag, 2 * a.timeout_ns)) {
-                    record_timeout(a.status, abort_flag, abort_slot, CG, kRoleProducer * 16 + kBarTail);
-                    ok = false;
-                }
+                __syncwarp();
                 if (++stage == STAGES) { stage = 0; phase ^= 1u; }
             }
         }
-        __syncwarp();
+        // the MMAs' last releases must land before this CTA exits
+        for (int i = 0; ok && i < STAGES; ++i) {
+            if (!mbar_wait_warp(empty_bar(stage), phase ^ 1u, abort_flag, 2 * a.timeout_ns)) {
+                if (issue) record_timeout(a.status, abort_flag, abort_slot, CG, kRoleProducer * 16 + kBarTail);
+                ok = false;
+            }
+            if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+        }
     } else if (warp == 1) {
         // ------------------------------------------ MMA issuer (pair leader) --
-        if (rank == 0 && lane == 0) {
+        if (rank == 0) {
+            // Descriptors of stage 0, step 0; a stage and a step of 16 add their
+            // offset to the address field, one add per operand and MMA.
+            const uint64_t p_desc0 = operand_desc(base, 0, Cfg::PMN), q_desc0 = operand_desc(base + Cfg::P_BYTES, 0, Cfg::QMN);
+            constexpr uint32_t p_step = (Cfg::PMN ? 2048u : 32u) >> 4, q_step = (Cfg::QMN ? 2048u : 32u) >> 4;
+            const bool issue = elect_one();
             uint32_t stage = 0, phase = 0, done = 0;
             bool ok = true;
             for (int tile = first; ok && tile < num_tiles; tile += step) {
-                const GroupedTile t = grouped_tile<Cfg>(tile, a, ends, tiles);
-                if (t.k_len == 0) continue;
-                const uint32_t buf = done & 1u;
-                if (!mbar_wait(tempty_bar(buf), ((done >> 1) & 1u) ^ 1u, abort_flag, 3 * a.timeout_ns)) {
-                    record_timeout(a.status, abort_flag, abort_slot, CG, kRoleMma * 16 + kBarTmemEmpty);
-                    break;
-                }
-                tc_fence_after_sync();
-                const uint32_t acc = tmem_base + buf * Cfg::BQ;
+                const GroupedTile t = grouped_tile<Cfg>(tile, a, ends, tiles).uniform();
                 const uint32_t idesc = idesc_bf16_f32(Cfg::BP, t.n, Cfg::PMN, Cfg::QMN);
-                const int blocks = (t.k_len + Cfg::BK - 1) / Cfg::BK;
-                for (int kb = 0; kb < blocks; ++kb) {
-                    if (!mbar_wait(full_bar(stage), phase, abort_flag, a.timeout_ns)) {
-                        record_timeout(a.status, abort_flag, abort_slot, CG, kRoleMma * 16 + kBarFull);
+                int until = 0;          // blocks until the segment's end
+                uint32_t acc = 0, more = 0;
+                for (int left = t.k_len; left > 0; left -= Cfg::BK) {
+                    if (until == 0) {
+                        const uint32_t buf = done & 1u;
+                        if (!mbar_wait_warp(tempty_bar(buf), ((done >> 1) & 1u) ^ 1u, abort_flag, 3 * a.timeout_ns)) {
+                            if (issue) record_timeout(a.status, abort_flag, abort_slot, CG, kRoleMma * 16 + kBarTmemEmpty);
+                            ok = false;
+                            break;
+                        }
+                        acc = tmem_base + buf * Cfg::BQ;
+                        more = 0;
+                        until = a.segment;
+                    }
+                    if (!mbar_wait_warp(full_bar(stage), phase, abort_flag, a.timeout_ns)) {
+                        if (issue) record_timeout(a.status, abort_flag, abort_slot, CG, kRoleMma * 16 + kBarFull);
                         ok = false;
                         break;
                     }
                     tc_fence_after_sync();
-                    const uint32_t p_src = base + stage * Cfg::STAGE_BYTES, q_src = p_src + Cfg::P_BYTES;
-                    const int steps = min(Cfg::BK / 16, (t.k_len - kb * Cfg::BK + 15) / 16);
+                    const bool last = --until == 0 || left <= Cfg::BK;
+                    if (issue) {
+                        const uint64_t p_desc = p_desc0 + (stage * Cfg::STAGE_BYTES >> 4);
+                        const uint64_t q_desc = q_desc0 + (stage * Cfg::STAGE_BYTES >> 4);
+                        mma_bf16_ss<CG>(acc, p_desc, q_desc, idesc, more);
+                        if (left >= Cfg::BK) {
 #pragma unroll
-                    for (int j = 0; j < Cfg::BK / 16; ++j)
-                        if (j < steps)
-                            mma_bf16_ss<CG>(acc, operand_desc(p_src, j, Cfg::PMN), operand_desc(q_src, j, Cfg::QMN),
-                                            idesc, (kb | j) != 0 ? 1u : 0u);
-                    mma_commit<CG>(empty_bar(stage), 0x3);
+                            for (int j = 1; j < Cfg::BK / 16; ++j)
+                                mma_bf16_ss<CG>(acc, p_desc + j * p_step, q_desc + j * q_step, idesc, 1u);
+                        } else {
+                            for (int j = 1; 16 * j < left; ++j)
+                                mma_bf16_ss<CG>(acc, p_desc + j * p_step, q_desc + j * q_step, idesc, 1u);
+                        }
+                        mma_commit<CG>(empty_bar(stage), 0x3);
+                        if (last) mma_commit<CG>(tfull_bar(done & 1u), 0x3);
+                    }
+                    __syncwarp();
+                    more = 1;
                     if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+                    if (last) {
+                        ++done;
+                        until = 0;
+                    }
                 }
-                if (!ok) break;
-                mma_commit<CG>(tfull_bar(buf), 0x3);
-                ++done;
             }
         }
-        __syncwarp();
     } else if (GRAD && warp == 2) {
         // ------------------------- rows of the next expert in a last block --
         uint32_t blocks = 0, parity = 0;       // blocks so far; bit s: parity of fix[s]
@@ -343,48 +370,82 @@ gemm_grouped_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_consta
         // ----------------------------------------------------- epilogue --
         const uint32_t sub = warp & 3u;                         // TMEM lane quarter
         const int part = static_cast<int>(warp - Cfg::EPI0) / 4;
-        constexpr int PARTS = Cfg::EPI_WARPS / 4;               // warps that share a quarter's columns
+        constexpr int PARTS = Cfg::EPI_WARPS / 4;               // fours of warps that share a tile's rows of the output
+        constexpr int CHUNKS = Cfg::BQ / 32 / PARTS;            // of 32 rows, for each of them
+        const int64_t esize = a.f32 ? 4 : 2;
+        const bool whole = a.f32 || (GRAD && a.beta != 0.0f);   // sums go through registers in fp32
+        ColumnsOut to(base + Cfg::OUT_OFF, part, sub, lane, a.ld * esize);
         uint32_t done = 0;
+        // the accumulator of a tile's next segment is complete
+        auto wait_full = [&]() {
+            uint32_t ready = 1;
+            if (lane == 0 && !mbar_wait(tfull_bar(done & 1u), (done >> 1) & 1u, abort_flag, 3 * a.timeout_ns)) {
+                record_timeout(a.status, abort_flag, abort_slot, CG, kRoleEpilogue * 16 + kBarTmemFull);
+                ready = 0;
+            }
+            ready = __shfl_sync(0xFFFFFFFFu, ready, 0);
+            tc_fence_after_sync();
+            return ready != 0;
+        };
+        auto release = [&]() {
+            tc_fence_before_sync();
+            __syncwarp();
+            if (lane == 0) {
+                if (CG == 1) mbar_arrive_local(tempty_bar(done & 1u));
+                else mbar_arrive_cluster(map_to_cta(tempty_bar(done & 1u), 0));
+            }
+            ++done;
+        };
         for (int tile = first; tile < num_tiles; tile += step) {
             const GroupedTile t = grouped_tile<Cfg>(tile, a, ends, tiles);
-            const uint32_t buf = done & 1u;
-            if (t.k_len > 0) {
-                uint32_t ready = 1;
-                if (lane == 0 && !mbar_wait(tfull_bar(buf), (done >> 1) & 1u, abort_flag, 3 * a.timeout_ns)) {
-                    record_timeout(a.status, abort_flag, abort_slot, CG, kRoleEpilogue * 16 + kBarTmemFull);
-                    ready = 0;
+            const int col0 = t.p0 + static_cast<int>(rank) * Cfg::BP_CTA;
+            uint8_t *out = static_cast<uint8_t *>(a.out) + col0 * esize +
+                           ((GRAD ? t.group * a.out_stride : 0) + static_cast<int64_t>(t.q0) * a.ld) * esize;
+            to.cols = a.P - col0;
+            auto from = [&](int chunk) {
+                return tmem_base + ((sub * 32u) << 16) + (done & 1u) * Cfg::BQ + 32u * (chunk * PARTS + part);
+            };
+            if (!whole) {
+                if (!to.agree(t.k_len == 0 || wait_full())) break;
+#pragma unroll 1
+                for (int chunk = 0; chunk < CHUNKS; ++chunk) {
+                    const int j = 32 * (chunk * PARTS + part);
+                    if (j >= t.count) break;
+                    uint32_t w[16] = {};
+                    if (t.k_len > 0) load_rows_bf16(from(chunk), 1.0f, w);
+                    to.rows(w, out + j * to.ld_bytes, t.count - j);
                 }
-                ready = __shfl_sync(0xFFFFFFFFu, ready, 0);
-                if (!ready) break;
-                tc_fence_after_sync();
+                if (t.k_len > 0) release();
+                continue;
             }
-            const uint32_t acc = tmem_base + ((sub * 32u) << 16) + buf * Cfg::BQ;
-            const int col = t.p0 + static_cast<int>(rank) * Cfg::BP_CTA + static_cast<int>(sub * 32u + lane);
-            const int64_t esize = a.f32 ? 4 : 2;
-            uint8_t *out = static_cast<uint8_t *>(a.out) + (GRAD ? t.group * a.out_stride * esize : 0) +
-                           t.q0 * a.ld * esize;
-            for (int j = 32 * part; j < t.count; j += 32 * PARTS) {
-                uint32_t r[32];
-                float v[32];
-                if (t.k_len > 0) {
-                    tmem_ld_32x32b_x32(acc + j, r);
-                    tmem_ld_wait();
+            // fp32: the tensor core cuts what its sums do not hold, always towards
+            // zero, so the error grows with the length (4.5e-6 of the result at
+            // 4096); segments are added here, to nearest (5e-7)
+            float v[CHUNKS][32] = {};
+            bool ok = true;
+            for (int left = t.k_len; left > 0 && ok; left -= a.segment * Cfg::BK) {
+                ok = wait_full();
+                if (!ok) break;
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
-                } else {
+                for (int chunk = 0; chunk < CHUNKS; ++chunk) {
+                    if (32 * (chunk * PARTS + part) < t.count) {
+                        uint32_t r[32];
+                        tmem_ld_32x32b_x32(from(chunk), r);
+                        tmem_ld_wait();
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) v[i] = 0.0f;
+                        for (int i = 0; i < 32; ++i) v[chunk][i] += __uint_as_float(r[i]);
+                    }
                 }
-                store_columns<32>(out + j * a.ld * esize, a.ld, t.count - j, col, a.P, a.f32, GRAD ? a.beta : 0.0f, v);
+                release();
             }
-            if (t.k_len > 0) {
-                tc_fence_before_sync();
-                __syncwarp();
-                if (lane == 0) {
-                    if (CG == 1) mbar_arrive_local(tempty_bar(buf));
-                    else mbar_arrive_cluster(map_to_cta(tempty_bar(buf), 0));
-                }
-                ++done;
+            if (!ok) break;
+            const int c = static_cast<int>(sub * 32u + lane);
+#pragma unroll
+            for (int chunk = 0; chunk < CHUNKS; ++chunk) {
+                const int j = 32 * (chunk * PARTS + part);
+                if (j < t.count)
+                    store_columns<32>(out + j * to.ld_bytes + c * esize, to.ld_bytes, t.count - j, c < to.cols, a.f32,
+                                      GRAD ? a.beta : 0.0f, v[chunk]);
             }
         }
     }

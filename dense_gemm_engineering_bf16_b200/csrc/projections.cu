@@ -136,6 +136,10 @@ gemm_status_t map_experts(CUtensorMap *map, const Mat &m, uint32_t box) {
                                   CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
+// Blocks of 64 that a tensor core sums by itself: all for a bf16 result, 512
+// elements for an fp32 one (gemm_grouped_kernel's epilogue).
+int segment_blocks(bool f32) { return f32 ? 8 : 1 << 24; }
+
 constexpr int64_t kMaxTiles = int64_t(1) << 30;     // tile numbers are 32-bit, one grid's step on top
 
 template <class Cfg>
@@ -171,7 +175,7 @@ gemm_status_t dispatch_rows(int dev, int sm_count, const Mat &A, const Mat &B, c
                             cudaStream_t stream) {
     if (a.M <= int64_t(64) * a.groups)
         return launch_rows<b200::GroupedCfg<b200::kGroupedRows, PMN, 1, 64, 8>>(dev, sm_count, A, B, a, stream);
-    return launch_rows<b200::GroupedCfg<b200::kGroupedRows, PMN, 2, 256, 6>>(dev, sm_count, A, B, a, stream);
+    return launch_rows<b200::GroupedCfg<b200::kGroupedRows, PMN, 2, 256, 5>>(dev, sm_count, A, B, a, stream);
 }
 
 // ----------------------------------------------------------------- 4 bits --
@@ -238,7 +242,7 @@ gemm_status_t dispatch_fp4(int dev, int sm_count, const Fp4Call &c, cudaStream_t
     if (c.args.M <= 64) return launch_fp4<b200::GemmFp4Cfg<NV, 1, 64, 6, true>>(dev, sm_count, c, stream);
     const int64_t pairs = (int64_t(c.args.M) + 255) / 256 * ((int64_t(c.args.N) + 255) / 256);
     if (2 * pairs >= sm_count) return launch_fp4<b200::GemmFp4Cfg<NV, 2, 256, 5>>(dev, sm_count, c, stream);
-    return launch_fp4<b200::GemmFp4Cfg<NV, 1, 128, 6>>(dev, sm_count, c, stream);
+    return launch_fp4<b200::GemmFp4Cfg<NV, 1, 128, 5>>(dev, sm_count, c, stream);
 }
 
 template <int XT, bool NV>
@@ -264,7 +268,7 @@ gemm_status_t launch_fp4_quantize(int dev, const b200::Fp4QuantizeArgs &a, gemm_
                   static_cast<unsigned>(parts));
 }
 
-using CfgGrad = b200::GroupedCfg<b200::kGroupedGrad, true, 2, 256, 6>;
+using CfgGrad = b200::GroupedCfg<b200::kGroupedGrad, true, 2, 256, 5>;
 
 }  // namespace
 
@@ -303,6 +307,7 @@ gemm_status_t gemm_bf16_grouped(const void *A, const void *B, const int32_t *end
     a.P = static_cast<int>(N);
     a.K = static_cast<int>(K);
     a.f32 = c_type == GEMM_OUT_F32;
+    a.segment = segment_blocks(a.f32);
     a.status = status;
     a.timeout_ns = b200::host::watchdog_ns(K);
     return mn ? dispatch_rows<true>(dev, sm_count, ma, mb, a, stream)
@@ -346,6 +351,7 @@ gemm_status_t gemm_bf16_grouped_wgrad(const void *dC, const void *A, const int32
     a.Q = static_cast<int>(q.cols);
     a.beta = beta;
     a.f32 = db_type == GEMM_OUT_F32;
+    a.segment = segment_blocks(a.f32);
     a.status = status;
     a.timeout_ns = b200::host::watchdog_ns(M);
     alignas(64) CUtensorMap tmP{}, tmQ{};

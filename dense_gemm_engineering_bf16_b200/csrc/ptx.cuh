@@ -86,6 +86,13 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_bar) {
                  ::"r"(cluster_bar) : "memory");
 }
 
+// The same where nothing that this thread did has to be visible with it (a
+// release at cluster scope waits for the thread's earlier accesses).
+__device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t cluster_bar) {
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];"
+                 ::"r"(cluster_bar) : "memory");
+}
+
 // One bounded probe: true once the phase with parity `parity` has completed.
 __device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity) {
     uint32_t ok;
@@ -113,6 +120,25 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity,
     }
     return true;
 }
+
+// The same by all lanes of a warp, which get one answer.  A loop that issues
+// TMA copies or MMAs keeps its operands in uniform registers only where the
+// whole warp runs it, with elect_one around the instructions themselves: inside a
+// branch of one lane they are moved there one by one, about 200 cycles an MMA.
+__device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity, const volatile uint32_t *abort_flag,
+                                               uint64_t timeout_ns) {
+    return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, abort_flag, timeout_ns));
+}
+
+// True in one lane of the (converged) warp.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
+}
+
+// A value that is the same in all lanes, known as such to the compiler.
+__device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xFFFFFFFFu, v, 0); }
 
 // ------------------------------------------------------------------- TMA --
 
