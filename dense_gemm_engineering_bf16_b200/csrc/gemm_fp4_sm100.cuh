@@ -88,7 +88,7 @@ gemm_fp4_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__
     const uint32_t raw = smem_addr(smem_raw);
     uint8_t *smem = smem_raw + ((1024u - (raw & 1023u)) & 1023u);
     const uint32_t base = smem_addr(smem);
-    const uint32_t warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const uint32_t warp = uniform(threadIdx.x / 32), lane = threadIdx.x % 32;
     const uint32_t rank = CG == 2 ? cluster_cta_rank() : 0u;
     const uint32_t members = Cfg::SPLIT ? cluster_num_ctas() : 1u, me = Cfg::SPLIT ? cluster_cta_rank() : 0u;
     const int cluster = CG * static_cast<int>(members);
@@ -146,25 +146,27 @@ gemm_fp4_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__
 
     if (warp == 0) {
         // ------------------------------------------------ TMA producer --
-        if (lane == 0) {
-            uint32_t stage = 0, phase = 0;
-            bool ok = true;
-            for (int tile = first; ok && tile < num_tiles; tile += step) {
-                int tq, tp;
-                raster_tile(tile, tiles_q, tiles_p, 8, tq, tp);
-                const int p = tp * Cfg::BP + static_cast<int>(rank) * Cfg::BP_CTA;
-                const int q_cta = mma_n(tq) / CG, q = tq * Cfg::BQ + static_cast<int>(rank) * q_cta;
-                const int boxes = (q_cta + Cfg::QBOX - 1) / Cfg::QBOX;
-                const uint32_t bytes = Cfg::P_BYTES + boxes * Cfg::QBOX * Cfg::ROW_BYTES + (1 + Cfg::Q_BLOCKS) * Cfg::SF_BYTES;
-                const int sp = p / 128 * a.tiles_k, sq = tq * Cfg::BQ / 128 * a.tiles_k;
-                for (int kb = kb0; kb < kb1; ++kb) {
-                    if (!mbar_wait(empty_bar(stage), phase ^ 1u, abort_flag, 2 * a.timeout_ns)) {
-                        record_timeout(a.status, abort_flag, abort_slot, cluster, kRoleProducer * 16 + kBarEmpty);
-                        ok = false;
-                        break;
-                    }
-                    const uint32_t p_dst = base + stage * Cfg::STAGE_BYTES, q_dst = p_dst + Cfg::P_BYTES;
-                    const uint32_t s_dst = q_dst + Cfg::Q_BYTES;
+        const bool issue = elect_one();
+        uint32_t stage = 0, phase = 0;
+        bool ok = true;
+        for (int tile = first; ok && tile < num_tiles; tile += step) {
+            int tq, tp;
+            raster_tile(tile, tiles_q, tiles_p, 8, tq, tp);
+            const int p = tp * Cfg::BP + static_cast<int>(rank) * Cfg::BP_CTA;
+            const int q_cta = mma_n(tq) / CG, q = tq * Cfg::BQ + static_cast<int>(rank) * q_cta;
+            const int boxes = (q_cta + Cfg::QBOX - 1) / Cfg::QBOX;
+            const uint32_t bytes = Cfg::P_BYTES + boxes * Cfg::QBOX * Cfg::ROW_BYTES + (1 + Cfg::Q_BLOCKS) * Cfg::SF_BYTES;
+            const int sp = p / 128 * a.tiles_k, sq = tq * Cfg::BQ / 128 * a.tiles_k;
+            for (int kb = kb0; kb < kb1; ++kb) {
+                if (!mbar_wait_warp(empty_bar(stage), phase ^ 1u, abort_flag, 2 * a.timeout_ns)) {
+                    if (issue) record_timeout(a.status, abort_flag, abort_slot, cluster, kRoleProducer * 16 + kBarEmpty);
+                    ok = false;
+                    break;
+                }
+                const uint32_t p_dst = base + stage * Cfg::STAGE_BYTES, q_dst = p_dst + Cfg::P_BYTES;
+                const uint32_t s_dst = q_dst + Cfg::Q_BYTES;
+                if (issue) {
+                    // bytes are counted by the pair's leader
                     if (rank == 0) mbar_arrive_expect_tx(full_bar(stage), CG * bytes);
                     const uint32_t bar = CG == 2 ? map_to_cta(full_bar(stage), 0) : full_bar(stage);
                     auto load = [&](uint32_t dst, const CUtensorMap *m, int x, int y) {
@@ -178,22 +180,24 @@ gemm_fp4_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__
 #pragma unroll
                     for (int b = 0; b < Cfg::Q_BLOCKS; ++b)
                         load(s_dst + Cfg::SF_BYTES * (1 + b), &tmSQ, 0, sq + b * a.tiles_k + kb * Cfg::CHUNKS);
-                    if (++stage == STAGES) { stage = 0; phase ^= 1u; }
                 }
-            }
-            // the MMAs' last releases must land before this CTA exits
-            for (int i = 0; ok && i < STAGES; ++i) {
-                if (!mbar_wait(empty_bar(stage), phase ^ 1u, abort_flag, 2 * a.timeout_ns)) {
-                    record_timeout(a.status, abort_flag, abort_slot, cluster, kRoleProducer * 16 + kBarTail);
-                    ok = false;
-                }
+                __syncwarp();
                 if (++stage == STAGES) { stage = 0; phase ^= 1u; }
             }
         }
-        __syncwarp();
+        // the MMAs' last releases must land before this CTA exits
+        for (int i = 0; ok && i < STAGES; ++i) {
+            if (!mbar_wait_warp(empty_bar(stage), phase ^ 1u, abort_flag, 2 * a.timeout_ns)) {
+                if (issue) record_timeout(a.status, abort_flag, abort_slot, cluster, kRoleProducer * 16 + kBarTail);
+                ok = false;
+            }
+            if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+        }
     } else if (warp == 1) {
         // ------------------------------------------ MMA issuer (pair leader) --
-        if (rank == 0 && lane == 0) {
+        if (rank == 0) {
+            const uint64_t p_desc0 = sw128_kmajor_desc(base), q_desc0 = sw128_kmajor_desc(base + Cfg::P_BYTES);
+            const bool issue = elect_one();
             uint32_t stage = 0, phase = 0, n = 0, done = 0;
             bool ok = true;
             for (int tile = first; ok && tile < num_tiles; tile += step, ++done) {
@@ -201,93 +205,91 @@ gemm_fp4_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__
                 raster_tile(tile, tiles_q, tiles_p, 8, tq, tp);
                 const uint32_t width = static_cast<uint32_t>(mma_n(tq));
                 const uint32_t buf = done % Cfg::ACC_BUFS;
-                if (!mbar_wait(tempty_bar(buf), ((done / Cfg::ACC_BUFS) & 1u) ^ 1u, abort_flag, 3 * a.timeout_ns)) {
-                    record_timeout(a.status, abort_flag, abort_slot, cluster, kRoleMma * 16 + kBarTmemEmpty);
+                if (!mbar_wait_warp(tempty_bar(buf), ((done / Cfg::ACC_BUFS) & 1u) ^ 1u, abort_flag, 3 * a.timeout_ns)) {
+                    if (issue) record_timeout(a.status, abort_flag, abort_slot, cluster, kRoleMma * 16 + kBarTmemEmpty);
                     break;
                 }
-                tc_fence_after_sync();
                 const uint32_t acc = tmem_base + buf * Cfg::BQ;
                 // a tile of 64 rows of A may be the second half of its scales' 128
                 const uint32_t q_col = Cfg::BQ == 64 ? 2u * (tq & 1) : 0u;
                 for (int kb = kb0; kb < kb1; ++kb) {
                     const uint32_t slot = n % Cfg::SF_SLOTS;
-                    if (!mbar_wait(full_bar(stage), phase, abort_flag, a.timeout_ns)) {
-                        record_timeout(a.status, abort_flag, abort_slot, cluster, kRoleMma * 16 + kBarFull);
-                        ok = false;
-                        break;
-                    }
-                    if (!mbar_wait(sf_full(slot), (n / Cfg::SF_SLOTS) & 1u, abort_flag, a.timeout_ns)) {
-                        record_timeout(a.status, abort_flag, abort_slot, cluster, kRoleMma * 16 + kBarSfFull);
+                    // the copier waited for the stage's bytes before it copied them
+                    if (!mbar_wait_warp(full_bar(stage), phase, abort_flag, a.timeout_ns) ||
+                        !mbar_wait_warp(sf_full(slot), (n / Cfg::SF_SLOTS) & 1u, abort_flag, a.timeout_ns)) {
+                        if (issue) record_timeout(a.status, abort_flag, abort_slot, cluster, kRoleMma * 16 + kBarSfFull);
                         ok = false;
                         break;
                     }
                     tc_fence_after_sync();
-                    const uint32_t p_src = base + stage * Cfg::STAGE_BYTES, q_src = p_src + Cfg::P_BYTES;
-                    const uint32_t sp = tmem_base + Cfg::SF_COL0 + slot * Cfg::SLOT_COLS;
-                    const uint32_t sq = sp + 4 * Cfg::CHUNKS + q_col;
-                    const int left = a.K - kb * Cfg::BK;
+                    if (issue) {
+                        const uint64_t p_desc = p_desc0 + (stage * Cfg::STAGE_BYTES >> 4);
+                        const uint64_t q_desc = q_desc0 + (stage * Cfg::STAGE_BYTES >> 4);
+                        const uint32_t sp = tmem_base + Cfg::SF_COL0 + slot * Cfg::SLOT_COLS;
+                        const uint32_t sq = sp + 4 * Cfg::CHUNKS + q_col;
+                        const int left = a.K - kb * Cfg::BK;
 #pragma unroll
-                    for (int j = 0; j < Cfg::MMAS; ++j) {
-                        if (64 * j >= left) break;      // the scales there are not this row's
-                        const uint32_t chunk = Cfg::NV ? j : j / 2, sf_id = Cfg::NV ? 0 : 2 * (j & 1);
-                        mma_fp4_ss<CG, Cfg::NV>(acc, sw128_kmajor_desc(p_src + 32 * j), sw128_kmajor_desc(q_src + 32 * j),
-                                                idesc_fp4(Cfg::NV, Cfg::BP, width, sf_id), sp + 4 * chunk,
-                                                sq + 4 * Cfg::Q_BLOCKS * chunk, (kb - kb0) | j ? 1u : 0u);
+                        for (int j = 0; j < Cfg::MMAS; ++j) {
+                            if (64 * j >= left) break;      // the scales there are not this row's
+                            const uint32_t chunk = Cfg::NV ? j : j / 2, sf_id = Cfg::NV ? 0 : 2 * (j & 1);
+                            mma_fp4_ss<CG, Cfg::NV>(acc, p_desc + 2 * j, q_desc + 2 * j,
+                                                    idesc_fp4(Cfg::NV, Cfg::BP, width, sf_id), sp + 4 * chunk,
+                                                    sq + 4 * Cfg::Q_BLOCKS * chunk, (kb - kb0) | j ? 1u : 0u);
+                        }
+                        mma_commit<CG>(empty_bar(stage), 0x3);
+                        mma_commit<CG>(sf_empty(slot), 0x1);
+                        if (kb + 1 == kb1) mma_commit<CG>(tfull_bar(buf), 0x3);
                     }
-                    mma_commit<CG>(empty_bar(stage), 0x3);
-                    mma_commit<CG>(sf_empty(slot), 0x1);
+                    __syncwarp();
                     ++n;
                     if (++stage == STAGES) { stage = 0; phase ^= 1u; }
                 }
-                if (!ok) break;
-                mma_commit<CG>(tfull_bar(buf), 0x3);
             }
         }
-        __syncwarp();
     } else if (warp == 2) {
         // ---------------------------------- scale copier (pair leader) --
-        if (rank == 0 && lane == 0) {
+        if (rank == 0) {
+            const bool issue = elect_one();
             uint32_t stage = 0, phase = 0, n = 0;
             bool ok = true;
             for (int tile = first; ok && tile < num_tiles; tile += step) {
                 for (int kb = kb0; kb < kb1; ++kb, ++n) {
                     const uint32_t slot = n % Cfg::SF_SLOTS;
-                    if (!mbar_wait(sf_empty(slot), ((n / Cfg::SF_SLOTS) & 1u) ^ 1u, abort_flag, 2 * a.timeout_ns)) {
-                        record_timeout(a.status, abort_flag, abort_slot, cluster, kRoleSfCopy * 16 + kBarSfEmpty);
-                        ok = false;
-                        break;
-                    }
-                    if (!mbar_wait(full_bar(stage), phase, abort_flag, 2 * a.timeout_ns)) {
-                        record_timeout(a.status, abort_flag, abort_slot, cluster, kRoleSfCopy * 16 + kBarFull);
+                    if (!mbar_wait_warp(sf_empty(slot), ((n / Cfg::SF_SLOTS) & 1u) ^ 1u, abort_flag, 2 * a.timeout_ns) ||
+                        !mbar_wait_warp(full_bar(stage), phase, abort_flag, 2 * a.timeout_ns)) {
+                        if (issue) record_timeout(a.status, abort_flag, abort_slot, cluster, kRoleSfCopy * 16 + kBarSfEmpty);
                         ok = false;
                         break;
                     }
                     tc_fence_after_sync();
-                    const uint32_t src = base + stage * Cfg::STAGE_BYTES + Cfg::P_BYTES + Cfg::Q_BYTES;
-                    const uint32_t dst = tmem_base + Cfg::SF_COL0 + slot * Cfg::SLOT_COLS;
-                    auto copy = [&](uint32_t col, uint32_t from) {
-                        if constexpr (CG == 1) tmem_cp_32x128b_warpx4(dst + col, rows16_desc(src + from));
-                        else tmem_cp_32x128b_warpx4_pair(dst + col, rows16_desc(src + from));
-                    };
+                    if (issue) {
+                        const uint64_t src = rows16_desc(base + Cfg::P_BYTES + Cfg::Q_BYTES) + (stage * Cfg::STAGE_BYTES >> 4);
+                        const uint32_t dst = tmem_base + Cfg::SF_COL0 + slot * Cfg::SLOT_COLS;
+                        auto copy = [&](uint32_t col, uint32_t from) {
+                            if constexpr (CG == 1) tmem_cp_32x128b_warpx4(dst + col, src + (from >> 4));
+                            else tmem_cp_32x128b_warpx4_pair(dst + col, src + (from >> 4));
+                        };
 #pragma unroll
-                    for (int c = 0; c < Cfg::CHUNKS; ++c) {
-                        copy(4 * c, kScaleTile * c);
+                        for (int c = 0; c < Cfg::CHUNKS; ++c) {
+                            copy(4 * c, kScaleTile * c);
 #pragma unroll
-                        for (int b = 0; b < Cfg::Q_BLOCKS; ++b)
-                            copy(4 * (Cfg::CHUNKS + Cfg::Q_BLOCKS * c + b), Cfg::SF_BYTES * (1 + b) + kScaleTile * c);
+                            for (int b = 0; b < Cfg::Q_BLOCKS; ++b)
+                                copy(4 * (Cfg::CHUNKS + Cfg::Q_BLOCKS * c + b), Cfg::SF_BYTES * (1 + b) + kScaleTile * c);
+                        }
+                        mma_commit<CG>(sf_full(slot), 0x1);
                     }
-                    mma_commit<CG>(sf_full(slot), 0x1);
+                    __syncwarp();
                     if (++stage == STAGES) { stage = 0; phase ^= 1u; }
                 }
             }
             for (int i = 0; ok && i < Cfg::SF_SLOTS; ++i, ++n) {
-                if (!mbar_wait(sf_empty(n % Cfg::SF_SLOTS), ((n / Cfg::SF_SLOTS) & 1u) ^ 1u, abort_flag, 2 * a.timeout_ns)) {
-                    record_timeout(a.status, abort_flag, abort_slot, cluster, kRoleSfCopy * 16 + kBarTail);
+                if (!mbar_wait_warp(sf_empty(n % Cfg::SF_SLOTS), ((n / Cfg::SF_SLOTS) & 1u) ^ 1u, abort_flag,
+                                    2 * a.timeout_ns)) {
+                    if (issue) record_timeout(a.status, abort_flag, abort_slot, cluster, kRoleSfCopy * 16 + kBarTail);
                     ok = false;
                 }
             }
         }
-        __syncwarp();
     } else {
         // ----------------------------------------------------- epilogue --
         const uint32_t sub = warp & 3u;                         // TMEM lane quarter
