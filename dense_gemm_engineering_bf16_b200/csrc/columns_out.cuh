@@ -38,17 +38,35 @@ __device__ __forceinline__ void stmatrix_x4_trans(uint32_t addr, uint32_t a, uin
                  : "memory");
 }
 
-// 32 rows x 32 columns of this warp as packed bf16: `from` its quarter's first
-// row in TMEM; w[8 h + 2 i + p] has lanes 16 h + 8 p + t / 4, rows 8 i + 2 (t % 4).
-__device__ __forceinline__ void load_rows_bf16(uint32_t from, float alpha, uint32_t (&w)[16]) {
-    uint32_t lo[16], hi[16];
+// 32 rows x 32 columns of this warp: `from` its quarter's first row in TMEM.
+__device__ __forceinline__ void load_rows(uint32_t from, uint32_t (&lo)[16], uint32_t (&hi)[16]) {
     tmem_ld_16x256b_x4(from, lo);
     tmem_ld_16x256b_x4(from + (16u << 16), hi);
-    tmem_ld_wait();
+}
+
+// Packed as bf16 once they have arrived: w[8 h + 2 i + p] has lanes 16 h + 8 p + t / 4,
+// rows 8 i + 2 (t % 4).
+__device__ __forceinline__ void pack_rows(float alpha, const uint32_t (&lo)[16], const uint32_t (&hi)[16],
+                                          uint32_t (&w)[16]) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         w[i] = pack_bf16x2(alpha * __uint_as_float(lo[2 * i]), alpha * __uint_as_float(lo[2 * i + 1]));
         w[8 + i] = pack_bf16x2(alpha * __uint_as_float(hi[2 * i]), alpha * __uint_as_float(hi[2 * i + 1]));
+    }
+}
+
+// N chunks of 32 rows, `stride` TMEM columns apart, two of them on their way at
+// a time (registers).
+template <int N>
+__device__ __forceinline__ void load_chunks_bf16(uint32_t from, uint32_t stride, float alpha, uint32_t (&w)[N][16]) {
+    uint32_t lo[2][16], hi[2][16];
+#pragma unroll
+    for (int c = 0; c < N; c += 2) {
+#pragma unroll
+        for (int i = 0; i < 2 && c + i < N; ++i) load_rows(from + (c + i) * stride, lo[i], hi[i]);
+        tmem_ld_wait();
+#pragma unroll
+        for (int i = 0; i < 2 && c + i < N; ++i) pack_rows(alpha, lo[i], hi[i], w[c + i]);
     }
 }
 
@@ -78,7 +96,7 @@ struct ColumnsOut {
         return both != 0;
     }
 
-    // 32 rows from load_rows_bf16, the first `count` of them to C's from `c` on
+    // 32 rows from pack_rows, the first `count` of them to C's from `c` on
     // (the four warps' first column).  Rows are 128 bytes in shared memory, their
     // 16-byte pieces swapped by row, so that neither direction has bank
     // conflicts.  The barrier also says that both warps have read the other

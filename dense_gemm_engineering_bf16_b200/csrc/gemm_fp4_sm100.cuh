@@ -400,20 +400,14 @@ gemm_fp4_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__
                                           true, 0.0f, v[chunk % HELD]);
                     }
             } else {
-                uint32_t w[HELD][16];
+                uint32_t w[CHUNKS][16];
+                load_chunks_bf16<CHUNKS>(acc + 32 * part, 32 * PARTS, alpha, w);
+                release();
 #pragma unroll
                 for (int chunk = 0; chunk < CHUNKS; ++chunk) {
                     const int j = 32 * (chunk * PARTS + part);
-                    load_rows_bf16(acc + j, alpha, w[chunk % HELD]);
-                    if (HELD == 1 && j < count) to.rows(w[0], out + j * to.ld_bytes, count - j);
+                    if (j < count) to.rows(w[chunk], out + j * to.ld_bytes, count - j);
                 }
-                release();
-                if (HELD > 1)
-#pragma unroll
-                    for (int chunk = 0; chunk < CHUNKS; ++chunk) {
-                        const int j = 32 * (chunk * PARTS + part);
-                        if (j < count) to.rows(w[chunk % HELD], out + j * to.ld_bytes, count - j);
-                    }
             }
         }
     }

@@ -38,7 +38,7 @@
 
 namespace b200 {
 
-constexpr int kMaxGroups = 1024;      // two words of shared memory each
+constexpr int kMaxGroups = 1024;      // three words of shared memory each
 
 // What a kernel computes: rows of C, or an expert's gradient.
 enum : int { kGroupedRows = 0, kGroupedGrad = 1 };
@@ -69,7 +69,7 @@ struct GroupedCfg {
     static constexpr int OUT_OFF = BAR_OFF + (NUM_BARS * 8 + 8 + 127) / 128 * 128;    // + TMEM address, abort flag
     static constexpr int TABLE_OFF = OUT_OFF + EPI_WARPS / 4 * kOutBytes;
     static constexpr int TMEM_COLS = pow2_at_least(2 * BQ, 32);
-    static constexpr int smem_bytes(int groups) { return 1024 + TABLE_OFF + 8 * groups; }
+    static constexpr int smem_bytes(int groups) { return 1024 + TABLE_OFF + 12 * groups; }
 
     static_assert(Q_CTA % QBOX == 0 && Q_BYTES % 1024 == 0, "whole boxes and swizzle atoms");
     static_assert(BQ >= 32 && BQ <= 256, "the epilogue reads 32 columns at a time");
@@ -101,44 +101,68 @@ struct GroupedTile {
     }
 };
 
+// Where the tiles are, the same in every warp: one look-up per tile and role,
+// so it has no division but these (a dozen of them were 1000 cycles a tile).
 template <class Cfg>
-__device__ __forceinline__ GroupedTile grouped_tile(int tile, const GroupedArgs &a, const int *ends, const int *tiles) {
-    GroupedTile t;
-    int local, extent;
-    if constexpr (Cfg::MODE == kGroupedRows) {
-        int lo = 0, hi = a.groups - 1;      // the first group whose tiles reach past `tile`
-        while (lo < hi) {
-            const int mid = (lo + hi) / 2;
-            if (tiles[mid] > tile) hi = mid;
-            else lo = mid + 1;
-        }
-        t.group = lo;
-        local = tile - (lo ? tiles[lo - 1] : 0);
-        t.q0 = lo ? ends[lo - 1] : 0;
-        extent = ends[lo] - t.q0;
-        t.k0 = 0;
-        t.k_len = a.K;
-    } else {
-        const int per = ((a.P + Cfg::BP - 1) / Cfg::BP) * ((a.Q + Cfg::BQ - 1) / Cfg::BQ);
-        t.group = tile / per;
-        local = tile - t.group * per;
-        t.q0 = 0;
-        extent = a.Q;
-        t.k0 = t.group ? ends[t.group - 1] : 0;
-        t.k_len = max(ends[t.group] - t.k0, 0);
+struct GroupedTiles {
+    const int *ends, *tiles, *widths;   // shared memory; gradient: ends alone
+    int groups, P, Q, K;
+    int tiles_p, tiles_q, width;        // gradient: tiles along Q, and their width
+    Divisor band, per;                  // tiles of eight Q tiles' band; of a group (gradient)
+
+    __device__ __forceinline__ static int width_of(int extent) {
+        const int n = max((extent + Cfg::BQ - 1) / Cfg::BQ, 1);
+        return ((extent + n - 1) / n + Cfg::N_STEP - 1) / Cfg::N_STEP * Cfg::N_STEP;
     }
-    // Q in tiles of one size (the last may be smaller), in bands of eight so
-    // that clusters running at the same time share both operands in L2
-    const int tiles_p = (a.P + Cfg::BP - 1) / Cfg::BP, tiles_q = (extent + Cfg::BQ - 1) / Cfg::BQ;
-    const int width = ((extent + tiles_q - 1) / tiles_q + Cfg::N_STEP - 1) / Cfg::N_STEP * Cfg::N_STEP;
-    int tq, tp;
-    raster_tile(local, tiles_q, tiles_p, 8, tq, tp);
-    t.p0 = tp * Cfg::BP;
-    t.q0 += tq * width;
-    t.count = min(width, extent - tq * width);
-    t.n = (t.count + Cfg::N_STEP - 1) / Cfg::N_STEP * Cfg::N_STEP;
-    return t;
-}
+
+    __device__ __forceinline__ GroupedTiles(const GroupedArgs &a, const int *ends_, const int *tiles_, const int *widths_)
+        : ends(ends_), tiles(tiles_), widths(widths_), groups(a.groups), P(a.P), Q(a.Q), K(a.K),
+          tiles_p((a.P + Cfg::BP - 1) / Cfg::BP), tiles_q((a.Q + Cfg::BQ - 1) / Cfg::BQ), width(width_of(a.Q)),
+          band(8 * static_cast<uint32_t>(tiles_p)), per(static_cast<uint32_t>(max(tiles_p * tiles_q, 1))) {}
+
+    __device__ __forceinline__ int count() const {
+        return Cfg::MODE == kGroupedGrad ? groups * tiles_p * tiles_q : tiles[groups - 1];
+    }
+
+    __device__ __forceinline__ GroupedTile operator()(int tile) const {
+        GroupedTile t;
+        int local, extent, n, wide;     // Q tiles, of `wide` (the last may be smaller)
+        if constexpr (Cfg::MODE == kGroupedRows) {
+            int lo = 0, hi = groups - 1;      // the first group whose tiles reach past `tile`
+            while (lo < hi) {
+                const int mid = (lo + hi) / 2;
+                if (tiles[mid] > tile) hi = mid;
+                else lo = mid + 1;
+            }
+            t.group = lo;
+            local = tile - (lo ? tiles[lo - 1] : 0);
+            t.q0 = lo ? ends[lo - 1] : 0;
+            extent = ends[lo] - t.q0;
+            n = (extent + Cfg::BQ - 1) / Cfg::BQ;
+            wide = widths[lo];
+            t.k0 = 0;
+            t.k_len = K;
+        } else {
+            t.group = static_cast<int>(per.divide(tile));
+            local = tile - t.group * tiles_p * tiles_q;
+            t.q0 = 0;
+            extent = Q;
+            n = tiles_q;
+            wide = width;
+            t.k0 = t.group ? ends[t.group - 1] : 0;
+            t.k_len = max(ends[t.group] - t.k0, 0);
+        }
+        // bands of eight Q tiles, so that clusters running at the same time
+        // share both operands in L2
+        const int b = static_cast<int>(band.divide(local)), in_band = local - b * 8 * tiles_p, rows = min(n - 8 * b, 8);
+        const int tp = static_cast<int>(divide_small(in_band, rows)), tq = 8 * b + in_band - tp * rows;
+        t.p0 = tp * Cfg::BP;
+        t.q0 += tq * wide;
+        t.count = min(wide, extent - tq * wide);
+        t.n = (t.count + Cfg::N_STEP - 1) / Cfg::N_STEP * Cfg::N_STEP;
+        return t;
+    }
+};
 
 template <class Cfg>
 __global__ void __launch_bounds__(Cfg::THREADS, 1)
@@ -161,7 +185,7 @@ gemm_grouped_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_consta
     const uint32_t tmem_slot = bar0 + 8u * Cfg::NUM_BARS, abort_slot = tmem_slot + 4u;
     volatile uint32_t *tmem_slot_ptr = reinterpret_cast<volatile uint32_t *>(smem + Cfg::BAR_OFF + 8 * Cfg::NUM_BARS);
     volatile uint32_t *abort_flag = tmem_slot_ptr + 1;
-    int *ends = reinterpret_cast<int *>(smem + Cfg::TABLE_OFF), *tiles = ends + a.groups;
+    int *ends = reinterpret_cast<int *>(smem + Cfg::TABLE_OFF), *tiles = ends + a.groups, *widths = tiles + a.groups;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < STAGES; ++s) {
@@ -192,7 +216,11 @@ gemm_grouped_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_consta
         for (int e0 = 0; e0 < a.groups; e0 += 32) {
             const int e = e0 + static_cast<int>(lane);
             int n = 0;
-            if (e < a.groups) n = (max(ends[e] - (e ? ends[e - 1] : 0), 0) + Cfg::BQ - 1) / Cfg::BQ * tiles_p;
+            if (e < a.groups) {
+                const int rows = max(ends[e] - (e ? ends[e - 1] : 0), 0);
+                widths[e] = GroupedTiles<Cfg>::width_of(rows);
+                n = (rows + Cfg::BQ - 1) / Cfg::BQ * tiles_p;
+            }
 #pragma unroll
             for (int d = 1; d < 32; d <<= 1) {
                 const int up = __shfl_up_sync(0xFFFFFFFFu, n, d);
@@ -206,8 +234,8 @@ gemm_grouped_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_consta
     if constexpr (CG == 2) cluster_sync_all();
     tc_fence_after_sync();
     const uint32_t tmem_base = *tmem_slot_ptr;
-    const int num_tiles = GRAD ? a.groups * (((a.P + Cfg::BP - 1) / Cfg::BP) * ((a.Q + Cfg::BQ - 1) / Cfg::BQ))
-                               : tiles[a.groups - 1];
+    const GroupedTiles<Cfg> tile_at(a, ends, tiles, widths);
+    const int num_tiles = tile_at.count();
     const int first = static_cast<int>(blockIdx.x) / CG, step = static_cast<int>(gridDim.x) / CG;
 
     if (warp == 0) {
@@ -216,7 +244,7 @@ gemm_grouped_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_consta
         uint32_t stage = 0, phase = 0;
         bool ok = true;
         for (int tile = first; ok && tile < num_tiles; tile += step) {
-            const GroupedTile t = grouped_tile<Cfg>(tile, a, ends, tiles).uniform();
+            const GroupedTile t = tile_at(tile).uniform();
             const int p = t.p0 + static_cast<int>(rank) * Cfg::BP_CTA;
             const int q_cta = t.n / CG, q = t.q0 + static_cast<int>(rank) * q_cta;
             const int boxes = (q_cta + Cfg::QBOX - 1) / Cfg::QBOX;
@@ -287,7 +315,7 @@ gemm_grouped_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_consta
             uint32_t stage = 0, phase = 0, done = 0;
             bool ok = true;
             for (int tile = first; ok && tile < num_tiles; tile += step) {
-                const GroupedTile t = grouped_tile<Cfg>(tile, a, ends, tiles).uniform();
+                const GroupedTile t = tile_at(tile).uniform();
                 const uint32_t idesc = idesc_bf16_f32(Cfg::BP, t.n, Cfg::PMN, Cfg::QMN);
                 int until = 0;          // blocks until the segment's end
                 uint32_t acc = 0, more = 0;
@@ -339,7 +367,7 @@ gemm_grouped_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_consta
         // ------------------------- rows of the next expert in a last block --
         uint32_t blocks = 0, parity = 0;       // blocks so far; bit s: parity of fix[s]
         for (int tile = first; tile < num_tiles; tile += step) {
-            const GroupedTile t = grouped_tile<Cfg>(tile, a, ends, tiles);
+            const GroupedTile t = tile_at(tile);
             blocks += (t.k_len + Cfg::BK - 1) / Cfg::BK;
             if (t.k_len % 16 == 0) continue;
             const uint32_t stage = (blocks - 1) % STAGES;
@@ -397,7 +425,7 @@ gemm_grouped_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_consta
             ++done;
         };
         for (int tile = first; tile < num_tiles; tile += step) {
-            const GroupedTile t = grouped_tile<Cfg>(tile, a, ends, tiles);
+            const GroupedTile t = tile_at(tile);
             const int col0 = t.p0 + static_cast<int>(rank) * Cfg::BP_CTA;
             uint8_t *out = static_cast<uint8_t *>(a.out) + col0 * esize +
                            ((GRAD ? t.group * a.out_stride : 0) + static_cast<int64_t>(t.q0) * a.ld) * esize;
@@ -407,15 +435,16 @@ gemm_grouped_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_consta
             };
             if (!whole) {
                 if (!to.agree(t.k_len == 0 || wait_full())) break;
-#pragma unroll 1
+                uint32_t w[CHUNKS][16] = {};
+                if (t.k_len > 0) {
+                    load_chunks_bf16<CHUNKS>(from(0), 32 * PARTS, 1.0f, w);
+                    release();
+                }
+#pragma unroll
                 for (int chunk = 0; chunk < CHUNKS; ++chunk) {
                     const int j = 32 * (chunk * PARTS + part);
-                    if (j >= t.count) break;
-                    uint32_t w[16] = {};
-                    if (t.k_len > 0) load_rows_bf16(from(chunk), 1.0f, w);
-                    to.rows(w, out + j * to.ld_bytes, t.count - j);
+                    if (j < t.count) to.rows(w[chunk], out + j * to.ld_bytes, t.count - j);
                 }
-                if (t.k_len > 0) release();
                 continue;
             }
             // fp32: the tensor core cuts what its sums do not hold, always towards

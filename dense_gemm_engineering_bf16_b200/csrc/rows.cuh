@@ -166,6 +166,31 @@ __device__ __forceinline__ void wait_for_stream() {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
+// Division of 32-bit numbers by one that stays the same: the upper half of a
+// product with 2^64 / d, rounded up, which is exact for every x (D. Lemire, O. Kaser
+// and N. Kurz, "Faster remainder by direct computation", 2019).
+struct Divisor {
+    uint64_t m;
+    __device__ __forceinline__ explicit Divisor(uint32_t d) : m(~uint64_t(0) / d + 1) {}
+    __device__ __forceinline__ uint32_t divide(uint32_t x) const {
+        return m ? static_cast<uint32_t>(__umul64hi(m, x)) : x;     // d = 1: m wraps to zero
+    }
+};
+
+// x / d for 1 <= d <= 8.
+__device__ __forceinline__ uint32_t divide_small(uint32_t x, uint32_t d) {
+    switch (d) {
+        case 1: return x;
+        case 2: return x / 2;
+        case 3: return x / 3;
+        case 4: return x / 4;
+        case 5: return x / 5;
+        case 6: return x / 6;
+        case 7: return x / 7;
+        default: return x / 8;
+    }
+}
+
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
     for (int m = 16; m > 0; m >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, m);
