@@ -44,6 +44,7 @@ __device__ __forceinline__ uint32_t max_magnitude(const float *v) {
 struct Fp4Scale {
     uint32_t byte;
     float by, inv;
+    bool saturated;     // NV: quotients past 6.375
 };
 
 template <bool NV>
@@ -60,12 +61,14 @@ __device__ __forceinline__ Fp4Scale fp4_scale(uint32_t top, float g) {
         asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.f32.f16 %0, lo;\n\t}" : "=f"(f) : "r"(h));
         s.by = f * g;
         s.inv = __frcp_rn(s.by);
+        s.saturated = s.byte == 0x7Eu;
         if (!finite) s.byte = 0x7Fu;
     } else {
         // 6 = 1.5 * 2^2, so e = E - 127 - 2 for a magnitude 1.f * 2^(E - 127), one more where 1.f > 1.5
         const int b = static_cast<int>(top >> 23) - 2 + ((top & 0x7FFFFFu) > 0x400000u ? 1 : 0);
         s.byte = static_cast<uint32_t>(max(b, 0));
         s.by = 0.0f;
+        s.saturated = false;
         s.inv = __uint_as_float((254u - s.byte) << 23);
         if (!finite) {
             s.byte = 0xFFu;
@@ -75,29 +78,28 @@ __device__ __forceinline__ Fp4Scale fp4_scale(uint32_t top, float g) {
     return s;
 }
 
-// v divided by the scale.  MX: exact (a power of two).  NV: the rounded product
-// with the reciprocal may miss a quotient that lies halfway between two codes,
-// where the last bit decides; one step of iterative refinement (the residual is
-// exact in an fma) gives the rounded quotient (P. Markstein, "Computation of
-// elementary functions on the IBM RISC System/6000 processor", 1990).  Bounded
-// first, so that the residual stays finite: every quotient past 6 is a 6.
-template <bool NV>
-__device__ __forceinline__ float fp4_quotient(float v, const Fp4Scale &s) {
-    float q = v * s.inv;
-    if constexpr (NV) {
-        q = fminf(fmaxf(q, -8.0f), 8.0f);
-        q = fmaf(fmaf(-q, s.by, v), s.inv, q);
-    }
-    return q;
+// Two fp32 numbers in one register pair, and their packed arithmetic.
+__device__ __forceinline__ uint64_t f32x2(float lo, float hi) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+
+__device__ __forceinline__ uint64_t mul_f32x2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
+__device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
 }
 
 // Eight codes, the first in the lowest bits; past 6 they are 6.
-template <bool NV>
-__device__ __forceinline__ uint32_t fp4_codes8(const float *v, const Fp4Scale &s) {
+__device__ __forceinline__ uint32_t e2m1_codes8(const float (&q)[8]) {
     uint32_t w;
-    float q[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) q[i] = fp4_quotient<NV>(v[i], s);
     asm("{\n\t.reg .b8 a, b, c, d;\n\t"
         "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\t"
         "cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
@@ -109,41 +111,76 @@ __device__ __forceinline__ uint32_t fp4_codes8(const float *v, const Fp4Scale &s
     return w;
 }
 
+// Eight values divided by their block's scale, as codes.  MX: exact (a power of
+// two).  NV: the rounded product with the reciprocal may miss a quotient that
+// lies halfway between two codes, where the last bit decides; one step of
+// iterative refinement (the residual is exact in an fma) gives the rounded
+// quotient (P. Markstein, "Computation of elementary functions on the IBM RISC
+// System/6000 processor", 1990).  Where the scale has saturated, quotients are
+// bounded first, so that the residual stays finite: all past 6 are a 6.
 template <bool NV>
-__device__ __forceinline__ uint16_t fp4_codes4(const float *v, const Fp4Scale &s) {
-    uint16_t w;
-    float q[4];
+__device__ __forceinline__ uint32_t fp4_codes8(const float *v, const Fp4Scale &s) {
+    float q[8];
+    if (NV && s.saturated) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) q[i] = fp4_quotient<NV>(v[i], s);
-    asm("{\n\t.reg .b8 a, b;\n\t"
-        "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\t"
-        "cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
-        "mov.b16 %0, {a, b};\n\t}"
-        : "=h"(w)
-        : "f"(q[0]), "f"(q[1]), "f"(q[2]), "f"(q[3]));
-    return w;
+        for (int i = 0; i < 8; ++i) {
+            q[i] = fminf(fmaxf(v[i] * s.inv, -8.0f), 8.0f);
+            q[i] = fmaf(fmaf(-q[i], s.by, v[i]), s.inv, q[i]);
+        }
+        return e2m1_codes8(q);
+    }
+    const uint64_t inv = f32x2(s.inv, s.inv), by = f32x2(-s.by, -s.by);
+#pragma unroll
+    for (int i = 0; i < 8; i += 2) {
+        const uint64_t x = f32x2(v[i], v[i + 1]);
+        uint64_t r = mul_f32x2(x, inv);
+        if (NV) r = fma_f32x2(fma_f32x2(r, by, x), inv, r);
+        asm("mov.b64 {%0, %1}, %2;" : "=f"(q[i]), "=f"(q[i + 1]) : "l"(r));
+    }
+    return e2m1_codes8(q);
 }
 
-// Encodes a group of values that the warp's lanes hold side by side, E (8 or 4)
-// each from element e on, those past K as zeros: a block is B / E neighbouring
-// lanes, four blocks' scales a word.  All 32 lanes call it.
-template <bool NV, int E>
-__device__ __forceinline__ void fp4_store(const float *v, int64_t e, int64_t K, float g, uint8_t *q, uint8_t *sf,
-                                          int64_t row, int64_t tiles) {
-    constexpr int LANES = kFp4Block<NV> / E;
-    uint32_t top = max_magnitude<E>(v);
+// Sixteen consecutive elements, as they are in memory.
+template <int T>
+struct Raw16 {
+    uint32_t w[T == kF32 ? 16 : 8];
+};
+
+// WIDE: 32-byte aligned.
+template <int T, bool WIDE>
+__device__ __forceinline__ void load_raw16(const uint8_t *p, Raw16<T> &r) {
 #pragma unroll
-    for (int m = 1; m < LANES; m <<= 1) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, m));
-    const Fp4Scale s = fp4_scale<NV>(top, g);
-    const int lane = threadIdx.x & 31;
-    uint32_t word = e < K ? s.byte << (8 * (lane / LANES & 3)) : 0u;
-    word |= __shfl_xor_sync(0xFFFFFFFFu, word, LANES);
-    word |= __shfl_xor_sync(0xFFFFFFFFu, word, 2 * LANES);
-    if (e < K) {
-        if constexpr (E == 8) *reinterpret_cast<uint32_t *>(q + e / 2) = fp4_codes8<NV>(v, s);
-        else *reinterpret_cast<uint16_t *>(q + e / 2) = fp4_codes4<NV>(v, s);
-        if (lane % (4 * LANES) == 0)
-            *reinterpret_cast<uint32_t *>(scale_word(sf, row, tiles, e / (4 * kFp4Block<NV>))) = word;
+    for (int i = 0; i < (T == kF32 ? 16 : 8); i += 8) {
+        if constexpr (WIDE) {
+            asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                         : "=r"(r.w[i]), "=r"(r.w[i + 1]), "=r"(r.w[i + 2]), "=r"(r.w[i + 3]), "=r"(r.w[i + 4]),
+                           "=r"(r.w[i + 5]), "=r"(r.w[i + 6]), "=r"(r.w[i + 7])
+                         : "l"(p + 4 * i));
+        } else {
+            const uint4 a = *reinterpret_cast<const uint4 *>(p + 4 * i), b = *reinterpret_cast<const uint4 *>(p + 4 * i + 16);
+            r.w[i] = a.x, r.w[i + 1] = a.y, r.w[i + 2] = a.z, r.w[i + 3] = a.w;
+            r.w[i + 4] = b.x, r.w[i + 5] = b.y, r.w[i + 6] = b.z, r.w[i + 7] = b.w;
+        }
+    }
+}
+
+// The largest magnitude (fp32 bits) and the values.  bf16: two at a time.
+template <int T>
+__device__ __forceinline__ uint32_t widen16(const Raw16<T> &r, float (&v)[16]) {
+    if constexpr (T == kF32) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r.w[i]);
+        return max_magnitude<16>(v);
+    } else {
+        uint32_t m = r.w[0] & 0x7FFF7FFFu;
+#pragma unroll
+        for (int i = 1; i < 8; ++i) asm("max.u16x2 %0, %0, %1;" : "+r"(m) : "r"(r.w[i] & 0x7FFF7FFFu));
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            v[2 * i] = __uint_as_float(r.w[i] << 16);
+            v[2 * i + 1] = __uint_as_float(r.w[i] & 0xFFFF0000u);
+        }
+        return max(m << 16, m & 0xFFFF0000u);
     }
 }
 
@@ -154,33 +191,41 @@ struct Fp4QuantizeArgs {
     int64_t M, K, ldx, ldq, tiles;   // tiles: scale tiles along K
 };
 
-// X stored K-major (M rows of K): VPT eights per thread.  A row takes
-// blockDim.x threads in each of `parts` blocks; short rows share a block
-// (blockDim.y).
-template <int XT, bool NV, int VPT>
+// X stored K-major (M rows of K): VPT sixteens per thread, one NV block each or
+// half an MX block; 4 neighbouring threads (MX: 8) hold the blocks of a word of
+// scales.  A row takes blockDim.x threads in each of `parts` blocks; short rows
+// share a block (blockDim.y).
+template <int XT, bool NV, int VPT, bool WIDE>
 __global__ void __launch_bounds__(256) fp4_quantize_kernel(Fp4QuantizeArgs a, unsigned parts) {
-    constexpr bool SPLIT = XT == kF32;
     wait_for_stream();
     const unsigned part = blockIdx.x % parts;
     const int64_t row = static_cast<int64_t>(blockIdx.x / parts) * blockDim.y + threadIdx.y;
     if (row >= a.M) return;   // whole warps
     const uint8_t *p = static_cast<const uint8_t *>(a.x) + row * a.ldx * elem_bytes<XT>;
-    uint8_t *q = a.q + row * a.ldq;
-    Raw8<XT> r[VPT];
+    const int64_t first = 16 * (static_cast<int64_t>(part) * VPT * blockDim.x + threadIdx.x);
+    Raw16<XT> r[VPT] = {};
 #pragma unroll
-    for (int i = 0; i < VPT; ++i)
-        r[i] = load_raw8<XT, SPLIT>(p, first8<SPLIT>(threadIdx.x, part * VPT + i, blockDim.x), a.K);
+    for (int i = 0; i < VPT; ++i) {
+        const int64_t e = first + 16 * i * static_cast<int64_t>(blockDim.x);
+        if (e < a.K) load_raw16<XT, WIDE>(p + e * elem_bytes<XT>, r[i]);
+    }
     const float g = NV && a.g ? __ldg(a.g) : 1.0f;
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-        float v[8];
-        widen8<XT>(r[i], v);
-        const int64_t e = first8<SPLIT>(threadIdx.x, part * VPT + i, blockDim.x);
-        if constexpr (SPLIT) {
-            fp4_store<NV, 4>(&v[0], e, a.K, g, q, a.sf, row, a.tiles);
-            fp4_store<NV, 4>(&v[4], e + at8<true>(4), a.K, g, q, a.sf, row, a.tiles);
-        } else {
-            fp4_store<NV, 8>(v, e, a.K, g, q, a.sf, row, a.tiles);
+        const int64_t e = first + 16 * i * static_cast<int64_t>(blockDim.x);
+        float v[16];
+        uint32_t top = widen16<XT>(r[i], v);
+        if (!NV) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+        const Fp4Scale s = fp4_scale<NV>(top, g);
+        constexpr int LANES = NV ? 1 : 2;       // of a block
+        uint32_t word = e < a.K ? s.byte << (8 * (threadIdx.x / LANES & 3)) : 0u;
+        word |= __shfl_xor_sync(0xFFFFFFFFu, word, LANES);
+        word |= __shfl_xor_sync(0xFFFFFFFFu, word, 2 * LANES);
+        if (e < a.K) {
+            *reinterpret_cast<uint2 *>(a.q + row * a.ldq + e / 2) =
+                make_uint2(fp4_codes8<NV>(&v[0], s), fp4_codes8<NV>(&v[8], s));
+            if (threadIdx.x % (4 * LANES) == 0)
+                *reinterpret_cast<uint32_t *>(scale_word(a.sf, row, a.tiles, e / (64 * LANES))) = word;
         }
     }
 }

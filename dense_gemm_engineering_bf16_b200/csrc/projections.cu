@@ -245,8 +245,23 @@ gemm_status_t dispatch_fp4(int dev, int sm_count, const Fp4Call &c, cudaStream_t
     return launch_fp4<b200::GemmFp4Cfg<NV, 1, 128, 5>>(dev, sm_count, c, stream);
 }
 
+template <int XT, bool NV, int VPT, bool WIDE>
+gemm_status_t launch_fp4_rows(int dev, const b200::Fp4QuantizeArgs &a, cudaStream_t stream) {
+    const int64_t sixteens = a.K / 16, most = VPT == 1 ? 64 : 256;
+    dim3 block(32, 8);
+    if (sixteens > 32 * VPT)
+        block = dim3(static_cast<unsigned>(std::min(most, ((sixteens + VPT - 1) / VPT + 31) / 32 * 32)));
+    const int64_t parts = (sixteens + VPT * block.x - 1) / (VPT * block.x);
+    const int64_t blocks = (a.M + block.y - 1) / block.y * parts;
+    if (blocks > kMaxDim) return GEMM_ERR_TOO_LARGE;
+    gemm_status_t s;
+    if ((s = b200::host::prepare<b200::fp4_quantize_kernel<XT, NV, VPT, WIDE>>(dev, 0, stream)) != GEMM_OK) return s;
+    return launch(b200::fp4_quantize_kernel<XT, NV, VPT, WIDE>, dim3(static_cast<unsigned>(blocks)), block, stream, a,
+                  static_cast<unsigned>(parts));
+}
+
 template <int XT, bool NV>
-gemm_status_t launch_fp4_quantize(int dev, const b200::Fp4QuantizeArgs &a, gemm_layout_t layout, cudaStream_t stream) {
+gemm_status_t launch_fp4_quantize(int dev, int sm_count, const b200::Fp4QuantizeArgs &a, gemm_layout_t layout, cudaStream_t stream) {
     gemm_status_t s;
     if (layout == GEMM_LAYOUT_MNMAJOR) {
         const int64_t i_tiles = (a.M + 63) / 64, blocks = i_tiles * ((a.K + 127) / 128);
@@ -255,17 +270,13 @@ gemm_status_t launch_fp4_quantize(int dev, const b200::Fp4QuantizeArgs &a, gemm_
         return launch(b200::fp4_quantize_mn_kernel<XT, NV>, dim3(static_cast<unsigned>(blocks)), dim3(128), stream, a,
                       static_cast<unsigned>(i_tiles));
     }
-    constexpr int VPT = 4;
-    const int64_t vecs = a.K / 8;
-    dim3 block(32, 8);
-    if (vecs > 32 * VPT)
-        block = dim3(static_cast<unsigned>(std::min<int64_t>(256, ((vecs + VPT - 1) / VPT + 31) / 32 * 32)));
-    const int64_t parts = (vecs + VPT * block.x - 1) / (VPT * block.x);
-    const int64_t blocks = (a.M + block.y - 1) / block.y * parts;
-    if (blocks > kMaxDim) return GEMM_ERR_TOO_LARGE;
-    if ((s = b200::host::prepare<b200::fp4_quantize_kernel<XT, NV, VPT>>(dev, 0, stream)) != GEMM_OK) return s;
-    return launch(b200::fp4_quantize_kernel<XT, NV, VPT>, dim3(static_cast<unsigned>(blocks)), block, stream, a,
-                  static_cast<unsigned>(parts));
+    // Few rows: one sixteen per thread, in small blocks, so that a row spreads
+    // over SMs; else four of bf16 or two of fp32, as many bytes in flight.
+    const bool few = a.M * a.K <= int64_t(16) * 256 * sm_count;
+    const bool wide = (reinterpret_cast<uintptr_t>(a.x) & 31u) == 0 && a.ldx * b200::elem_bytes<XT> % 32 == 0;
+    if (few) return wide ? launch_fp4_rows<XT, NV, 1, true>(dev, a, stream) : launch_fp4_rows<XT, NV, 1, false>(dev, a, stream);
+    constexpr int VPT = XT == b200::kF32 ? 2 : 4;
+    return wide ? launch_fp4_rows<XT, NV, VPT, true>(dev, a, stream) : launch_fp4_rows<XT, NV, VPT, false>(dev, a, stream);
 }
 
 using CfgGrad = b200::GroupedCfg<b200::kGroupedGrad, true, 2, 256, 5>;
@@ -391,10 +402,10 @@ gemm_status_t gemm_fp4_quantize(const void *X, const float *scale, uint8_t *Q, u
     if ((s = b200::host::device(dev, sm_count, stream)) != GEMM_OK) return s;
     const b200::Fp4QuantizeArgs a{X, scale, Q, sf, M, K, ldx, ldq, scale_tiles_k(K, format)};
     if (format == GEMM_FP4_NV)
-        return x_type == GEMM_OUT_F32 ? launch_fp4_quantize<b200::kF32, true>(dev, a, layout, stream)
-                                      : launch_fp4_quantize<b200::kBF16, true>(dev, a, layout, stream);
-    return x_type == GEMM_OUT_F32 ? launch_fp4_quantize<b200::kF32, false>(dev, a, layout, stream)
-                                  : launch_fp4_quantize<b200::kBF16, false>(dev, a, layout, stream);
+        return x_type == GEMM_OUT_F32 ? launch_fp4_quantize<b200::kF32, true>(dev, sm_count, a, layout, stream)
+                                      : launch_fp4_quantize<b200::kBF16, true>(dev, sm_count, a, layout, stream);
+    return x_type == GEMM_OUT_F32 ? launch_fp4_quantize<b200::kF32, false>(dev, sm_count, a, layout, stream)
+                                  : launch_fp4_quantize<b200::kBF16, false>(dev, sm_count, a, layout, stream);
 }
 
 gemm_status_t gemm_fp4(const uint8_t *A, const uint8_t *sfa, const float *scale_a, const uint8_t *B, const uint8_t *sfb,
