@@ -50,7 +50,7 @@ struct GemmFp4Cfg {
     static constexpr int Q_BYTES = Q_CTA * ROW_BYTES;
     static constexpr int SF_BYTES = CHUNKS * kScaleTile;      // of 128 rows
     static constexpr int STAGE_BYTES = P_BYTES + Q_BYTES + (1 + Q_BLOCKS) * SF_BYTES;
-    static constexpr int SF_SLOTS = 4, SLOT_COLS = 4 * CHUNKS * (1 + Q_BLOCKS);
+    static constexpr int SF_SLOTS = BQ <= 128 ? 4 : NV ? 5 : 8, SLOT_COLS = 4 * CHUNKS * (1 + Q_BLOCKS);
     static constexpr int ACC_BUFS = BQ > 128 ? 1 : 2;
     static constexpr int SF_COL0 = ACC_BUFS * BQ;
     static constexpr int TMEM_COLS = pow2_at_least(SF_COL0 + SF_SLOTS * SLOT_COLS, 32);
@@ -131,7 +131,7 @@ gemm_fp4_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__
     if (cluster > 1) cluster_sync_all();
     tc_fence_after_sync();
     wait_for_stream();
-    const uint32_t tmem_base = *tmem_slot_ptr;
+    const uint32_t tmem_base = static_cast<uint32_t>(uniform(static_cast<int>(*tmem_slot_ptr)));
 
     const int tiles_p = (a.N + Cfg::BP - 1) / Cfg::BP, tiles_q = (a.M + Cfg::BQ - 1) / Cfg::BQ;
     const int num_tiles = tiles_p * tiles_q;
@@ -415,12 +415,12 @@ gemm_fp4_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__
     tc_fence_before_sync();
     __syncthreads();
     if (cluster > 1) cluster_sync_all();
-    if (*abort_flag) {      // copies in flight land first
+    if (*abort_flag) {      // set in every CTA of the cluster before that; copies in flight land first
         const uint64_t t0 = global_timer_ns();
         while (global_timer_ns() - t0 < 200000ull) __nanosleep(1000);
+        __syncthreads();
+        if (cluster > 1) cluster_sync_all();
     }
-    __syncthreads();
-    if (cluster > 1) cluster_sync_all();
     if (warp == 1) {
         tc_fence_after_sync();
         tmem_dealloc<CG>(tmem_base, Cfg::TMEM_COLS);

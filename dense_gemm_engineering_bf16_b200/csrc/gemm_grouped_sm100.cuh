@@ -233,7 +233,7 @@ gemm_grouped_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_consta
     __syncthreads();
     if constexpr (CG == 2) cluster_sync_all();
     tc_fence_after_sync();
-    const uint32_t tmem_base = *tmem_slot_ptr;
+    const uint32_t tmem_base = static_cast<uint32_t>(uniform(static_cast<int>(*tmem_slot_ptr)));
     const GroupedTiles<Cfg> tile_at(a, ends, tiles, widths);
     const int num_tiles = tile_at.count();
     const int first = static_cast<int>(blockIdx.x) / CG, step = static_cast<int>(gridDim.x) / CG;
@@ -482,12 +482,12 @@ gemm_grouped_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_consta
     tc_fence_before_sync();
     __syncthreads();
     if constexpr (CG == 2) cluster_sync_all();
-    if (*abort_flag) {      // copies in flight land first
+    if (*abort_flag) {      // set in every CTA of the cluster before that; copies in flight land first
         const uint64_t t0 = global_timer_ns();
         while (global_timer_ns() - t0 < 200000ull) __nanosleep(1000);
+        __syncthreads();
+        if constexpr (CG == 2) cluster_sync_all();
     }
-    __syncthreads();
-    if constexpr (CG == 2) cluster_sync_all();
     if (warp == 1) {
         tc_fence_after_sync();
         tmem_dealloc<CG>(tmem_base, Cfg::TMEM_COLS);
