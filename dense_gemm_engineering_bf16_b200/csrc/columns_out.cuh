@@ -158,4 +158,50 @@ __device__ __forceinline__ void store_columns(uint8_t *c, int64_t ld_bytes, int 
     }
 }
 
+// Sum over a cluster's members, each of which has the same rows x 128 of C over
+// its share of the reduction in TMEM at `acc` (the warp's quarter): `fours` times
+// four rows, the first `count` rows are C's.  Member o sums the fours [o share,
+// (o + 1) share): the others send theirs to its shared memory (`parts`, 16 bytes
+// per four, member and column; `received` counts 128 arrivals from each), and it
+// adds all members' in their order and writes them to `c` (the first row of the
+// lane's column).  `wait` waits for `received`; false: it failed.
+template <class Wait>
+__device__ __forceinline__ bool cluster_sum(uint32_t acc, int fours, int members, int me, uint32_t column, uint32_t parts,
+                                            uint32_t received, Wait wait, uint8_t *c, int64_t ld_bytes, int count,
+                                            bool mine, bool f32, float alpha) {
+    const int share = (fours + members - 1) / members;
+    for (int f = 0; f < fours; f += 8) {
+        uint32_t r[32];
+        tmem_ld_32x32b_x32(acc + 4 * f, r);
+        tmem_ld_wait();
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int owner = (f + i) / share;
+            if (f + i < fours && owner != me)
+                store_cluster_v4(map_to_cta(parts + 16u * ((me * share + (f + i) - owner * share) * 128u + column), owner),
+                                 r[4 * i], r[4 * i + 1], r[4 * i + 2], r[4 * i + 3]);
+        }
+    }
+    for (int o = 0; o < members; ++o)      // release: the stores come first
+        if (o != me) mbar_arrive_cluster(map_to_cta(received, o));
+    if (!wait()) return false;
+    for (int f = me * share; f < min(fours, (me + 1) * share); ++f) {
+        uint32_t own[4];
+        asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(own[0]), "=r"(own[1]), "=r"(own[2]), "=r"(own[3]) : "r"(acc + 4 * f));
+        tmem_ld_wait();
+        float sum[4] = {};
+        for (int m = 0; m < members; ++m) {
+            uint32_t x[4] = {own[0], own[1], own[2], own[3]};
+            if (m != me) ld_shared_v4(parts + 16u * ((m * share + f - me * share) * 128u + column), x[0], x[1], x[2], x[3]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) sum[i] += __uint_as_float(x[i]);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) sum[i] *= alpha;
+        store_columns<4>(c + 4 * f * ld_bytes, ld_bytes, count - 4 * f, mine, f32, 0.0f, sum);
+    }
+    return true;
+}
+
 }  // namespace b200

@@ -65,7 +65,8 @@ struct GemmFp4Cfg {
     static constexpr int SMEM_BYTES = 1024 + PART_OFF + (SPLIT ? BQ * 128 * 4 : 0);
     static_assert(TMEM_COLS <= 512 && STAGE_BYTES % 1024 == 0 && SMEM_BYTES <= 232448, "it fits");
     static_assert(!SPLIT || (CG == 1 && EPI_WARPS == 4), "split: one-CTA tiles");
-    static_assert(BQ == 64 || BQ % 128 == 0, "a tile's scales start at a tile of scales, or in its middle");
+    // a tile's scales start at a tile of scales, or in its middle (64); 32: one tile
+    static_assert(BQ == 32 || BQ == 64 || BQ % 128 == 0, "rows of A per tile");
 };
 
 struct GemmFp4Args {
@@ -327,50 +328,18 @@ gemm_fp4_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__
                 }
             };
             if (Cfg::SPLIT && members > 1) {
-                // Rows of C in fours; member o sums fours [o share, (o + 1) share).
-                const int fours = mma_n(tq) / 4, share = (fours + static_cast<int>(members) - 1) / static_cast<int>(members);
-                for (int f = 0; f < fours; f += 8) {
-                    uint32_t r[32];
-                    tmem_ld_32x32b_x32(acc + 4 * f, r);
-                    tmem_ld_wait();
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const uint32_t owner = static_cast<uint32_t>((f + i) / share);
-                        if (f + i < fours && owner != me) {
-                            const uint32_t at = (me * share + (f + i) - owner * share) * 128u + sub * 32u + lane;
-                            store_cluster_v4(map_to_cta(base + Cfg::PART_OFF + 16u * at, owner), r[4 * i], r[4 * i + 1],
-                                             r[4 * i + 2], r[4 * i + 3]);
-                        }
+                auto wait = [&]() {
+                    uint32_t got = 1;
+                    if (lane == 0 && !mbar_wait(received_bar, 0, abort_flag, 3 * a.timeout_ns)) {
+                        record_timeout(a.status, abort_flag, abort_slot, cluster, kRoleEpilogue * 16 + kBarRxFull);
+                        got = 0;
                     }
-                }
-                for (uint32_t o = 0; o < members; ++o)      // release: the stores come first
-                    if (o != me) mbar_arrive_cluster(map_to_cta(received_bar, o));
-                if (lane == 0 && !mbar_wait(received_bar, 0, abort_flag, 3 * a.timeout_ns)) {
-                    record_timeout(a.status, abort_flag, abort_slot, cluster, kRoleEpilogue * 16 + kBarRxFull);
-                    ready = 0;
-                }
-                ready = __shfl_sync(0xFFFFFFFFu, ready, 0);
-                __syncwarp();   // lane 0's acquire orders every lane's accesses that follow
-                if (!ready) break;
-                for (int f = static_cast<int>(me) * share; f < min(fours, (static_cast<int>(me) + 1) * share); ++f) {
-                    uint32_t own[4];
-                    asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];"
-                                 : "=r"(own[0]), "=r"(own[1]), "=r"(own[2]), "=r"(own[3]) : "r"(acc + 4 * f));
-                    tmem_ld_wait();
-                    float v[4] = {};
-                    for (uint32_t m = 0; m < members; ++m) {
-                        uint32_t x[4] = {own[0], own[1], own[2], own[3]};
-                        if (m != me)
-                            ld_shared_v4(base + Cfg::PART_OFF + 16u * ((m * share + f - me * share) * 128u + sub * 32u + lane), x[0],
-                                         x[1], x[2], x[3]);
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) v[i] += __uint_as_float(x[i]);
-                    }
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) v[i] *= alpha;
-                    store_columns<4>(out + 4 * f * to.ld_bytes + mine * esize, to.ld_bytes, count - 4 * f,
-                                     mine < to.cols, a.f32, 0.0f, v);
-                }
+                    return __shfl_sync(0xFFFFFFFFu, got, 0) != 0;
+                };
+                if (!cluster_sum(acc, mma_n(tq) / 4, static_cast<int>(members), static_cast<int>(me), sub * 32u + lane,
+                                 base + Cfg::PART_OFF, received_bar, wait, out + mine * esize, to.ld_bytes, count,
+                                 mine < to.cols, a.f32, alpha))
+                    break;
                 release();
                 continue;
             }

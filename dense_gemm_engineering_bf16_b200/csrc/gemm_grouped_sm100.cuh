@@ -25,6 +25,10 @@
 //   the rest   epilogue: TMEM to registers to global memory (columns_out.cuh),
 //              which overlaps the next tile's MMAs
 //
+// SPLIT, for the few rows of a token: a cluster of 2, 4 or 8 CTAs owns a tile,
+// each over a share of K, and their partials meet in distributed shared memory
+// (cluster_sum).  One tile per cluster.
+//
 // Every CTA works out the tiles from `ends` itself: the numbers of tiles up to
 // each expert in shared memory, a binary search per tile.  Rows outside every
 // expert are neither computed nor written.
@@ -43,9 +47,10 @@ constexpr int kMaxGroups = 1024;      // three words of shared memory each
 // What a kernel computes: rows of C, or an expert's gradient.
 enum : int { kGroupedRows = 0, kGroupedGrad = 1 };
 
-template <int MODE_, bool PMN_, int CG_, int BQ_, int STAGES_>
+template <int MODE_, bool PMN_, int CG_, int BQ_, int STAGES_, bool SPLIT_ = false>
 struct GroupedCfg {
     static constexpr int MODE = MODE_;
+    static constexpr bool SPLIT = SPLIT_;
     static constexpr bool PMN = PMN_ || MODE_ == kGroupedGrad;   // P stored MN-major
     static constexpr bool QMN = MODE_ == kGroupedGrad;
     static constexpr int CG = CG_;
@@ -63,16 +68,18 @@ struct GroupedCfg {
     static constexpr int EPI_WARPS = BQ >= 128 ? 8 : 4;
     static constexpr int EPI0 = MODE == kGroupedGrad ? 3 : 2;    // first epilogue warp
     static constexpr int THREADS = 32 * (EPI0 + EPI_WARPS);
-    // full[S], empty[S], fix[S] (gradient), tmem_full[2], tmem_empty[2]
-    static constexpr int NUM_BARS = (MODE == kGroupedGrad ? 3 : 2) * STAGES + 4;
+    // full[S], empty[S], tmem_full[2], tmem_empty[2], fix[S] (gradient), received (split)
+    static constexpr int NUM_BARS = (MODE == kGroupedGrad ? 3 : 2) * STAGES + 4 + (SPLIT ? 1 : 0);
     static constexpr int BAR_OFF = STAGES * STAGE_BYTES;
     static constexpr int OUT_OFF = BAR_OFF + (NUM_BARS * 8 + 8 + 127) / 128 * 128;    // + TMEM address, abort flag
-    static constexpr int TABLE_OFF = OUT_OFF + EPI_WARPS / 4 * kOutBytes;
+    static constexpr int PART_OFF = OUT_OFF + EPI_WARPS / 4 * kOutBytes;      // other members' partials
+    static constexpr int TABLE_OFF = PART_OFF + (SPLIT ? BQ * 128 * 4 : 0);
     static constexpr int TMEM_COLS = pow2_at_least(2 * BQ, 32);
     static constexpr int smem_bytes(int groups) { return 1024 + TABLE_OFF + 12 * groups; }
 
     static_assert(Q_CTA % QBOX == 0 && Q_BYTES % 1024 == 0, "whole boxes and swizzle atoms");
     static_assert(BQ >= 32 && BQ <= 256, "the epilogue reads 32 columns at a time");
+    static_assert(!SPLIT || (CG == 1 && EPI_WARPS == 4 && MODE == kGroupedRows), "split: one-CTA tiles of rows");
     static_assert(smem_bytes(kMaxGroups) <= 232448, "dynamic shared memory per CTA on sm_100");
 };
 
@@ -106,7 +113,7 @@ struct GroupedTile {
 template <class Cfg>
 struct GroupedTiles {
     const int *ends, *tiles, *widths;   // shared memory; gradient: ends alone
-    int groups, P, Q, K;
+    int groups, P, Q, k0, k_len;        // rows: this CTA's share of K
     int tiles_p, tiles_q, width;        // gradient: tiles along Q, and their width
     Divisor band, per;                  // tiles of eight Q tiles' band; of a group (gradient)
 
@@ -115,10 +122,17 @@ struct GroupedTiles {
         return ((extent + n - 1) / n + Cfg::N_STEP - 1) / Cfg::N_STEP * Cfg::N_STEP;
     }
 
-    __device__ __forceinline__ GroupedTiles(const GroupedArgs &a, const int *ends_, const int *tiles_, const int *widths_)
-        : ends(ends_), tiles(tiles_), widths(widths_), groups(a.groups), P(a.P), Q(a.Q), K(a.K),
+    __device__ __forceinline__ GroupedTiles(const GroupedArgs &a, const int *ends_, const int *tiles_, const int *widths_,
+                                            int members, int me)
+        : ends(ends_), tiles(tiles_), widths(widths_), groups(a.groups), P(a.P), Q(a.Q), k0(0), k_len(a.K),
           tiles_p((a.P + Cfg::BP - 1) / Cfg::BP), tiles_q((a.Q + Cfg::BQ - 1) / Cfg::BQ), width(width_of(a.Q)),
-          band(8 * static_cast<uint32_t>(tiles_p)), per(static_cast<uint32_t>(max(tiles_p * tiles_q, 1))) {}
+          band(8 * static_cast<uint32_t>(tiles_p)), per(static_cast<uint32_t>(max(tiles_p * tiles_q, 1))) {
+        if (members > 1) {
+            const int64_t blocks = (int64_t(a.K) + Cfg::BK - 1) / Cfg::BK;
+            k0 = static_cast<int>(blocks * me / members) * Cfg::BK;
+            k_len = min(static_cast<int>(blocks * (me + 1) / members) * Cfg::BK, a.K) - k0;
+        }
+    }
 
     __device__ __forceinline__ int count() const {
         return Cfg::MODE == kGroupedGrad ? groups * tiles_p * tiles_q : tiles[groups - 1];
@@ -140,8 +154,8 @@ struct GroupedTiles {
             extent = ends[lo] - t.q0;
             n = (extent + Cfg::BQ - 1) / Cfg::BQ;
             wide = widths[lo];
-            t.k0 = 0;
-            t.k_len = K;
+            t.k0 = k0;
+            t.k_len = k_len;
         } else {
             t.group = static_cast<int>(per.divide(tile));
             local = tile - t.group * tiles_p * tiles_q;
@@ -175,6 +189,9 @@ gemm_grouped_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_consta
     const uint32_t base = smem_addr(smem);
     const uint32_t warp = uniform(threadIdx.x / 32), lane = threadIdx.x % 32;
     const uint32_t rank = CG == 2 ? cluster_cta_rank() : 0u;
+    const int members = Cfg::SPLIT ? static_cast<int>(cluster_num_ctas()) : 1;
+    const int me = Cfg::SPLIT ? static_cast<int>(cluster_cta_rank()) : 0;
+    const int cluster = CG * members;
 
     const uint32_t bar0 = base + Cfg::BAR_OFF;
     auto full_bar = [&](uint32_t s) { return bar0 + 8u * s; };
@@ -182,6 +199,7 @@ gemm_grouped_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_consta
     auto tfull_bar = [&](uint32_t b) { return bar0 + 8u * (2 * STAGES + b); };
     auto tempty_bar = [&](uint32_t b) { return bar0 + 8u * (2 * STAGES + 2 + b); };
     auto fix_bar = [&](uint32_t s) { return bar0 + 8u * (2 * STAGES + 4 + s); };
+    const uint32_t received_bar = bar0 + 8u * (Cfg::NUM_BARS - 1);
     const uint32_t tmem_slot = bar0 + 8u * Cfg::NUM_BARS, abort_slot = tmem_slot + 4u;
     volatile uint32_t *tmem_slot_ptr = reinterpret_cast<volatile uint32_t *>(smem + Cfg::BAR_OFF + 8 * Cfg::NUM_BARS);
     volatile uint32_t *abort_flag = tmem_slot_ptr + 1;
@@ -198,6 +216,7 @@ gemm_grouped_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_consta
             mbar_init(tfull_bar(b), 1);
             mbar_init(tempty_bar(b), Cfg::EPI_WARPS * CG);
         }
+        if (Cfg::SPLIT) mbar_init(received_bar, 128 * max(members - 1, 1));
         *abort_flag = 0u;
         fence_barrier_init();
     }
@@ -231,12 +250,12 @@ gemm_grouped_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_consta
         }
     }
     __syncthreads();
-    if constexpr (CG == 2) cluster_sync_all();
+    if (cluster > 1) cluster_sync_all();
     tc_fence_after_sync();
     const uint32_t tmem_base = static_cast<uint32_t>(uniform(static_cast<int>(*tmem_slot_ptr)));
-    const GroupedTiles<Cfg> tile_at(a, ends, tiles, widths);
+    const GroupedTiles<Cfg> tile_at(a, ends, tiles, widths, members, me);
     const int num_tiles = tile_at.count();
-    const int first = static_cast<int>(blockIdx.x) / CG, step = static_cast<int>(gridDim.x) / CG;
+    const int first = static_cast<int>(blockIdx.x) / cluster, step = static_cast<int>(gridDim.x) / cluster;
 
     if (warp == 0) {
         // ------------------------------------------------ TMA producer --
@@ -252,7 +271,7 @@ gemm_grouped_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_consta
             int k = t.k0;
             for (int left = t.k_len; left > 0; left -= Cfg::BK, k += Cfg::BK) {
                 if (!mbar_wait_warp(empty_bar(stage), phase ^ 1u, abort_flag, 2 * a.timeout_ns)) {
-                    if (issue) record_timeout(a.status, abort_flag, abort_slot, CG, kRoleProducer * 16 + kBarEmpty);
+                    if (issue) record_timeout(a.status, abort_flag, abort_slot, cluster, kRoleProducer * 16 + kBarEmpty);
                     ok = false;
                     break;
                 }
@@ -299,7 +318,7 @@ gemm_grouped_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_consta
         // the MMAs' last releases must land before this CTA exits
         for (int i = 0; ok && i < STAGES; ++i) {
             if (!mbar_wait_warp(empty_bar(stage), phase ^ 1u, abort_flag, 2 * a.timeout_ns)) {
-                if (issue) record_timeout(a.status, abort_flag, abort_slot, CG, kRoleProducer * 16 + kBarTail);
+                if (issue) record_timeout(a.status, abort_flag, abort_slot, cluster, kRoleProducer * 16 + kBarTail);
                 ok = false;
             }
             if (++stage == STAGES) { stage = 0; phase ^= 1u; }
@@ -323,7 +342,7 @@ gemm_grouped_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_consta
                     if (until == 0) {
                         const uint32_t buf = done & 1u;
                         if (!mbar_wait_warp(tempty_bar(buf), ((done >> 1) & 1u) ^ 1u, abort_flag, 3 * a.timeout_ns)) {
-                            if (issue) record_timeout(a.status, abort_flag, abort_slot, CG, kRoleMma * 16 + kBarTmemEmpty);
+                            if (issue) record_timeout(a.status, abort_flag, abort_slot, cluster, kRoleMma * 16 + kBarTmemEmpty);
                             ok = false;
                             break;
                         }
@@ -332,7 +351,7 @@ gemm_grouped_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_consta
                         until = a.segment;
                     }
                     if (!mbar_wait_warp(full_bar(stage), phase, abort_flag, a.timeout_ns)) {
-                        if (issue) record_timeout(a.status, abort_flag, abort_slot, CG, kRoleMma * 16 + kBarFull);
+                        if (issue) record_timeout(a.status, abort_flag, abort_slot, cluster, kRoleMma * 16 + kBarFull);
                         ok = false;
                         break;
                     }
@@ -373,7 +392,7 @@ gemm_grouped_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_consta
             const uint32_t stage = (blocks - 1) % STAGES;
             uint32_t ready = 1;
             if (lane == 0 && !mbar_wait(fix_bar(stage), (parity >> stage) & 1u, abort_flag, 3 * a.timeout_ns)) {
-                record_timeout(a.status, abort_flag, abort_slot, CG, kRoleFix * 16 + kBarFix);
+                record_timeout(a.status, abort_flag, abort_slot, cluster, kRoleFix * 16 + kBarFix);
                 ready = 0;
             }
             ready = __shfl_sync(0xFFFFFFFFu, ready, 0);
@@ -408,7 +427,7 @@ gemm_grouped_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_consta
         auto wait_full = [&]() {
             uint32_t ready = 1;
             if (lane == 0 && !mbar_wait(tfull_bar(done & 1u), (done >> 1) & 1u, abort_flag, 3 * a.timeout_ns)) {
-                record_timeout(a.status, abort_flag, abort_slot, CG, kRoleEpilogue * 16 + kBarTmemFull);
+                record_timeout(a.status, abort_flag, abort_slot, cluster, kRoleEpilogue * 16 + kBarTmemFull);
                 ready = 0;
             }
             ready = __shfl_sync(0xFFFFFFFFu, ready, 0);
@@ -433,6 +452,22 @@ gemm_grouped_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_consta
             auto from = [&](int chunk) {
                 return tmem_base + ((sub * 32u) << 16) + (done & 1u) * Cfg::BQ + 32u * (chunk * PARTS + part);
             };
+            if (Cfg::SPLIT && members > 1) {
+                auto wait = [&]() {
+                    uint32_t got = 1;
+                    if (lane == 0 && !mbar_wait(received_bar, 0, abort_flag, 3 * a.timeout_ns)) {
+                        record_timeout(a.status, abort_flag, abort_slot, cluster, kRoleEpilogue * 16 + kBarRxFull);
+                        got = 0;
+                    }
+                    return __shfl_sync(0xFFFFFFFFu, got, 0) != 0;
+                };
+                const int c = static_cast<int>(sub * 32u + lane);
+                if (!wait_full() || !cluster_sum(from(0), t.n / 4, members, me, c, base + Cfg::PART_OFF, received_bar, wait,
+                                                 out + c * esize, to.ld_bytes, t.count, c < to.cols, a.f32, 1.0f))
+                    break;
+                release();
+                continue;
+            }
             if (!whole) {
                 if (!to.agree(t.k_len == 0 || wait_full())) break;
                 uint32_t w[CHUNKS][16] = {};
@@ -481,12 +516,12 @@ gemm_grouped_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_consta
 
     tc_fence_before_sync();
     __syncthreads();
-    if constexpr (CG == 2) cluster_sync_all();
+    if (cluster > 1) cluster_sync_all();
     if (*abort_flag) {      // set in every CTA of the cluster before that; copies in flight land first
         const uint64_t t0 = global_timer_ns();
         while (global_timer_ns() - t0 < 200000ull) __nanosleep(1000);
         __syncthreads();
-        if constexpr (CG == 2) cluster_sync_all();
+        if (cluster > 1) cluster_sync_all();
     }
     if (warp == 1) {
         tc_fence_after_sync();

@@ -149,10 +149,19 @@ gemm_status_t launch_grouped(int dev, int sm_count, const CUtensorMap &tmP, cons
     constexpr int kMost = Cfg::smem_bytes(b200::kMaxGroups);
     if (tiles > kMaxTiles) return GEMM_ERR_TOO_LARGE;
     gemm_status_t s;
-    int room;
+    int size = Cfg::CG, room;
     if ((s = b200::host::prepare<kernel>(dev, kMost, stream)) != GEMM_OK) return s;
-    if ((s = resident_clusters<kernel>(dev, sm_count, Cfg::THREADS, kMost, Cfg::CG, room, stream)) != GEMM_OK) return s;
-    return launch(kernel, static_cast<int>(std::min<int64_t>(room, tiles)), Cfg::CG, Cfg::THREADS,
+    if constexpr (Cfg::SPLIT) {
+        // K in as many shares as keep every cluster resident at once, four blocks
+        // of 64 each at least; for an fp32 result no longer than a segment
+        const int64_t blocks = (int64_t(a.K) + Cfg::BK - 1) / Cfg::BK;
+        for (size = 8; size > 1; size /= 2) {
+            if ((s = resident_clusters<kernel>(dev, sm_count, Cfg::THREADS, kMost, size, room, stream)) != GEMM_OK) return s;
+            if (tiles <= room && blocks >= 4 * size && (blocks + size - 1) / size <= a.segment) break;
+        }
+    }
+    if ((s = resident_clusters<kernel>(dev, sm_count, Cfg::THREADS, kMost, size, room, stream)) != GEMM_OK) return s;
+    return launch(kernel, static_cast<int>(std::min<int64_t>(room, tiles)), size, Cfg::THREADS,
                   Cfg::smem_bytes(a.groups), stream, tmP, tmQ, a);
 }
 
@@ -174,7 +183,7 @@ template <bool PMN>
 gemm_status_t dispatch_rows(int dev, int sm_count, const Mat &A, const Mat &B, const b200::GroupedArgs &a,
                             cudaStream_t stream) {
     if (a.M <= int64_t(64) * a.groups)
-        return launch_rows<b200::GroupedCfg<b200::kGroupedRows, PMN, 1, 64, 8>>(dev, sm_count, A, B, a, stream);
+        return launch_rows<b200::GroupedCfg<b200::kGroupedRows, PMN, 1, 64, 6, true>>(dev, sm_count, A, B, a, stream);
     return launch_rows<b200::GroupedCfg<b200::kGroupedRows, PMN, 2, 256, 5>>(dev, sm_count, A, B, a, stream);
 }
 
@@ -239,9 +248,20 @@ gemm_status_t launch_fp4(int dev, int sm_count, const Fp4Call &c, cudaStream_t s
 
 template <bool NV>
 gemm_status_t dispatch_fp4(int dev, int sm_count, const Fp4Call &c, cudaStream_t stream) {
+    // Up to 64 rows K is split over clusters.
     if (c.args.M <= 64) return launch_fp4<b200::GemmFp4Cfg<NV, 1, 64, 6, true>>(dev, sm_count, c, stream);
+    // From there single CTAs of 128 x 128 or pairs of 256 x 256, whichever is
+    // predicted faster: a fixed cost (pairs take 2.5 us longer to start and end),
+    // and per wave one of its own and one per 256 of K, in us.  Measured, single
+    // and pair: 1000 x 2048 x 2048 6.3 and 8.5, 512 x 4096 x 4096 8.8 and 10.8, 400
+    // x 8192 x 8192 24.3 and 17.9, 1000 x 2500 x 2016 11.2 and 10.1.
+    const int64_t single = (int64_t(c.args.M) + 127) / 128 * ((int64_t(c.args.N) + 127) / 128);
     const int64_t pairs = (int64_t(c.args.M) + 255) / 256 * ((int64_t(c.args.N) + 255) / 256);
-    if (2 * pairs >= sm_count) return launch_fp4<b200::GemmFp4Cfg<NV, 2, 256, 5>>(dev, sm_count, c, stream);
+    const double steps = static_cast<double>((int64_t(c.args.K) + 255) / 256);
+    const auto waves = [](int64_t tiles, int slots) { return static_cast<double>((tiles + slots - 1) / slots); };
+    const double one = 2.3 + waves(single, sm_count) * (1.0 + 0.345 * steps);
+    const double two = 4.8 + waves(pairs, sm_count / 2) * (0.8 + 0.36 * steps);
+    if (two < one) return launch_fp4<b200::GemmFp4Cfg<NV, 2, 256, 5>>(dev, sm_count, c, stream);
     return launch_fp4<b200::GemmFp4Cfg<NV, 1, 128, 5>>(dev, sm_count, c, stream);
 }
 
