@@ -6,6 +6,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <cmath>
 #include <cstdint>
 
 #include "b200gemm.h"
@@ -152,12 +153,12 @@ gemm_status_t launch_grouped(int dev, int sm_count, const CUtensorMap &tmP, cons
     int size = Cfg::CG, room;
     if ((s = b200::host::prepare<kernel>(dev, kMost, stream)) != GEMM_OK) return s;
     if constexpr (Cfg::SPLIT) {
-        // K in as many shares as keep every cluster resident at once, four blocks
+        // K in as many shares as keep every cluster resident at once, eight blocks
         // of 64 each at least; for an fp32 result no longer than a segment
         const int64_t blocks = (int64_t(a.K) + Cfg::BK - 1) / Cfg::BK;
         for (size = 8; size > 1; size /= 2) {
             if ((s = resident_clusters<kernel>(dev, sm_count, Cfg::THREADS, kMost, size, room, stream)) != GEMM_OK) return s;
-            if (tiles <= room && blocks >= 4 * size && (blocks + size - 1) / size <= a.segment) break;
+            if (tiles <= room && blocks >= 8 * size && (blocks + size - 1) / size <= a.segment) break;
         }
     }
     if ((s = resident_clusters<kernel>(dev, sm_count, Cfg::THREADS, kMost, size, room, stream)) != GEMM_OK) return s;
@@ -179,12 +180,59 @@ gemm_status_t launch_rows(int dev, int sm_count, const Mat &A, const Mat &B, con
     return launch_grouped<Cfg>(dev, sm_count, tmP, tmQ, a, tiles, stream);
 }
 
+// Waves of `tiles` on `slots` of them at once.
+double waves(double tiles, int slots) { return std::ceil(tiles / slots); }
+
+// Tiles of `size` rows that experts with `rows` rows each on average take:
+// their sizes differ, so about half a tile more than the average alone would.
+double tiles_of(double experts, double rows, int size) {
+    return experts > 1 ? experts * (rows / size + 0.5) : std::ceil(rows / size);
+}
+
 template <bool PMN>
 gemm_status_t dispatch_rows(int dev, int sm_count, const Mat &A, const Mat &B, const b200::GroupedArgs &a,
                             cudaStream_t stream) {
-    if (a.M <= int64_t(64) * a.groups)
+    // Tiles of 64 rows for few rows an expert, or for tiles so few that K is
+    // split.  Then single CTAs of 128 x 128 or pairs of 256 x 256, whichever is
+    // predicted faster: a fixed cost, and per wave one of its own and one per 64
+    // of K, in us (K = 2048, N = 2048, skewed, 64-row tiles, single, pair: 8 experts,
+    // 64 rows 15.1 15.1 16.6; 512 rows 21.0 16.5 18.0; 4000 rows 60 40 37; 64 experts,
+    // 2000 rows 89 93 90; 8000 rows 166 120 111.  One expert, 512 rows, K = 4096, N =
+    // 512: 14.1 18.0 24.2).
+    const int experts = std::min(a.groups, a.M);
+    const double rows = static_cast<double>(a.M) / experts;
+    const int64_t blocks = (int64_t(a.K) + 63) / 64, narrow = (int64_t(a.P) + 127) / 128, wide = (int64_t(a.P) + 255) / 256;
+    if (rows <= 32 || (blocks >= 32 && 2 * (a.M / 64 + experts) * narrow <= sm_count))
         return launch_rows<b200::GroupedCfg<b200::kGroupedRows, PMN, 1, 64, 6, true>>(dev, sm_count, A, B, a, stream);
+    const double one = 2.5 + waves(tiles_of(experts, rows, 128) * narrow, sm_count) * (1.0 + 0.226 * blocks);
+    const double two = 5.0 + waves(tiles_of(experts, rows, 256) * wide, sm_count / 2) * (1.5 + 0.285 * blocks);
+    if (one < two) return launch_rows<b200::GroupedCfg<b200::kGroupedRows, PMN, 1, 128, 5>>(dev, sm_count, A, B, a, stream);
     return launch_rows<b200::GroupedCfg<b200::kGroupedRows, PMN, 2, 256, 5>>(dev, sm_count, A, B, a, stream);
+}
+
+template <class Cfg>
+gemm_status_t launch_grad(int dev, int sm_count, const Mat &p, const Mat &q, const b200::GroupedArgs &a,
+                          cudaStream_t stream) {
+    alignas(64) CUtensorMap tmP{}, tmQ{};
+    gemm_status_t s;
+    if (a.M > 0 && ((s = map_rows(&tmP, p, Cfg::BK)) != GEMM_OK || (s = map_rows(&tmQ, q, Cfg::BK)) != GEMM_OK)) return s;
+    const int64_t tiles = ((p.cols + Cfg::BP - 1) / Cfg::BP) * ((q.cols + Cfg::BQ - 1) / Cfg::BQ);
+    if (tiles > kMaxTiles) return GEMM_ERR_TOO_LARGE;
+    return launch_grouped<Cfg>(dev, sm_count, tmP, tmQ, a, tiles * a.groups, stream);
+}
+
+gemm_status_t dispatch_grad(int dev, int sm_count, const Mat &p, const Mat &q, const b200::GroupedArgs &a,
+                            cudaStream_t stream) {
+    // As above, single CTAs of 128 x 128 or pairs of 256 x 256 (single, pair: 8
+    // experts, 1000 rows, 1024 x 512 8.2 and 10.6 us; one, 8192 rows, 1024 x 1024 36
+    // and 46, 2048 x 2048 69 and 54).
+    const double tiles1 = static_cast<double>((p.cols + 127) / 128) * ((q.cols + 127) / 128) * a.groups;
+    const double tiles2 = static_cast<double>((p.cols + 255) / 256) * ((q.cols + 255) / 256) * a.groups;
+    const double blocks = std::ceil(static_cast<double>(a.M) / a.groups / 64);
+    const double one = 2.5 + waves(tiles1, sm_count) * (1.2 + 0.252 * blocks);
+    const double two = 4.5 + waves(tiles2, sm_count / 2) * (2.0 + 0.311 * blocks);
+    if (one < two) return launch_grad<b200::GroupedCfg<b200::kGroupedGrad, true, 1, 128, 5>>(dev, sm_count, p, q, a, stream);
+    return launch_grad<b200::GroupedCfg<b200::kGroupedGrad, true, 2, 256, 5>>(dev, sm_count, p, q, a, stream);
 }
 
 // ----------------------------------------------------------------- 4 bits --
@@ -255,10 +303,9 @@ gemm_status_t dispatch_fp4(int dev, int sm_count, const Fp4Call &c, cudaStream_t
     // and per wave one of its own and one per 256 of K, in us.  Measured, single
     // and pair: 1000 x 2048 x 2048 6.3 and 8.5, 512 x 4096 x 4096 8.8 and 10.8, 400
     // x 8192 x 8192 24.3 and 17.9, 1000 x 2500 x 2016 11.2 and 10.1.
-    const int64_t single = (int64_t(c.args.M) + 127) / 128 * ((int64_t(c.args.N) + 127) / 128);
-    const int64_t pairs = (int64_t(c.args.M) + 255) / 256 * ((int64_t(c.args.N) + 255) / 256);
+    const double single = static_cast<double>((int64_t(c.args.M) + 127) / 128 * ((int64_t(c.args.N) + 127) / 128));
+    const double pairs = static_cast<double>((int64_t(c.args.M) + 255) / 256 * ((int64_t(c.args.N) + 255) / 256));
     const double steps = static_cast<double>((int64_t(c.args.K) + 255) / 256);
-    const auto waves = [](int64_t tiles, int slots) { return static_cast<double>((tiles + slots - 1) / slots); };
     const double one = 2.3 + waves(single, sm_count) * (1.0 + 0.345 * steps);
     const double two = 4.8 + waves(pairs, sm_count / 2) * (0.8 + 0.36 * steps);
     if (two < one) return launch_fp4<b200::GemmFp4Cfg<NV, 2, 256, 5>>(dev, sm_count, c, stream);
@@ -298,8 +345,6 @@ gemm_status_t launch_fp4_quantize(int dev, int sm_count, const b200::Fp4Quantize
     constexpr int VPT = XT == b200::kF32 ? 2 : 4;
     return wide ? launch_fp4_rows<XT, NV, VPT, true>(dev, a, stream) : launch_fp4_rows<XT, NV, VPT, false>(dev, a, stream);
 }
-
-using CfgGrad = b200::GroupedCfg<b200::kGroupedGrad, true, 2, 256, 5>;
 
 }  // namespace
 
@@ -385,13 +430,7 @@ gemm_status_t gemm_bf16_grouped_wgrad(const void *dC, const void *A, const int32
     a.segment = segment_blocks(a.f32);
     a.status = status;
     a.timeout_ns = b200::host::watchdog_ns(M);
-    alignas(64) CUtensorMap tmP{}, tmQ{};
-    if (M > 0) {
-        if ((s = map_rows(&tmP, p, CfgGrad::BK)) != GEMM_OK || (s = map_rows(&tmQ, q, CfgGrad::BK)) != GEMM_OK) return s;
-    }
-    const int64_t tiles = ((p.cols + CfgGrad::BP - 1) / CfgGrad::BP) * ((q.cols + CfgGrad::BQ - 1) / CfgGrad::BQ);
-    if (tiles > kMaxTiles) return GEMM_ERR_TOO_LARGE;
-    return launch_grouped<CfgGrad>(dev, sm_count, tmP, tmQ, a, tiles * groups, stream);
+    return dispatch_grad(dev, sm_count, p, q, a, stream);
 }
 
 int64_t gemm_fp4_scale_bytes(int64_t rows, int64_t K, gemm_fp4_t format) {
