@@ -164,7 +164,7 @@ struct GroupedTiles {
             n = tiles_q;
             wide = width;
             t.k0 = t.group ? ends[t.group - 1] : 0;
-            t.k_len = max(ends[t.group] - t.k0, 0);
+            t.k_len = ends[t.group] - t.k0;
         }
         // bands of eight Q tiles, so that clusters running at the same time
         // share both operands in L2
@@ -228,25 +228,38 @@ gemm_grouped_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_consta
     for (int e = threadIdx.x; e < a.groups; e += Cfg::THREADS) ends[e] = min(max(__ldg(a.ends + e), 0), a.M);
     tc_fence_before_sync();
     __syncthreads();
-    if (!GRAD && warp == 0) {
-        // tiles up to each expert's last
+    if (warp == 0) {
+        // An end below an earlier one counts as that one, so that the experts'
+        // rows never overlap; then the tiles up to each expert's last.
         const int tiles_p = (a.P + Cfg::BP - 1) / Cfg::BP;
-        int before = 0;
+        int top = 0, before = 0;
         for (int e0 = 0; e0 < a.groups; e0 += 32) {
             const int e = e0 + static_cast<int>(lane);
-            int n = 0;
-            if (e < a.groups) {
-                const int rows = max(ends[e] - (e ? ends[e - 1] : 0), 0);
-                widths[e] = GroupedTiles<Cfg>::width_of(rows);
-                n = (rows + Cfg::BQ - 1) / Cfg::BQ * tiles_p;
-            }
+            int end = e < a.groups ? ends[e] : 0;
 #pragma unroll
             for (int d = 1; d < 32; d <<= 1) {
-                const int up = __shfl_up_sync(0xFFFFFFFFu, n, d);
-                if (static_cast<int>(lane) >= d) n += up;
+                const int up = __shfl_up_sync(0xFFFFFFFFu, end, d);
+                if (static_cast<int>(lane) >= d) end = max(end, up);
             }
-            if (e < a.groups) tiles[e] = before + n;
-            before += __shfl_sync(0xFFFFFFFFu, n, 31);
+            end = max(end, top);
+            int start = __shfl_up_sync(0xFFFFFFFFu, end, 1);
+            if (lane == 0) start = top;
+            top = __shfl_sync(0xFFFFFFFFu, end, 31);
+            int n = 0;
+            if (e < a.groups) {
+                ends[e] = end;
+                n = (end - start + Cfg::BQ - 1) / Cfg::BQ * tiles_p;
+                widths[e] = GroupedTiles<Cfg>::width_of(end - start);
+            }
+            if constexpr (!GRAD) {
+#pragma unroll
+                for (int d = 1; d < 32; d <<= 1) {
+                    const int up = __shfl_up_sync(0xFFFFFFFFu, n, d);
+                    if (static_cast<int>(lane) >= d) n += up;
+                }
+                if (e < a.groups) tiles[e] = before + n;
+                before += __shfl_sync(0xFFFFFFFFu, n, 31);
+            }
         }
     }
     __syncthreads();

@@ -130,7 +130,7 @@ gemm_status_t map_rows(CUtensorMap *map, const Mat &m, uint32_t box) {
 
 // The experts' matrices: boxes of 64 x `box` rows of one of them.
 gemm_status_t map_experts(CUtensorMap *map, const Mat &m, uint32_t box) {
-    const int64_t stride = m.count > 1 ? m.stride : (m.rows * m.ld + 7) / 8 * 8;
+    const int64_t stride = m.count > 1 ? m.stride : m.ld;     // one matrix: not looked at
     const int64_t dims[3] = {m.cols, m.rows, m.count}, strides[2] = {m.ld * 2, stride * 2};
     const uint32_t b[3] = {64, box, 1};
     return b200::host::encode_map(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, m.p, 3, dims, strides, b,

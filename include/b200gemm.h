@@ -451,9 +451,8 @@ B200GEMM_API gemm_status_t gemm_bf16_w4(const void *A, const uint8_t *B, const v
  * Products grouped by expert.  A's rows are sorted by expert; ends[e], on the
  * DEVICE, says where expert e's rows end: it has the rows [ends[e-1], ends[e])
  * (ends[-1] = 0), possibly none.  The host never learns the sizes, so a call
- * can be queued, or captured into a graph, before they are known.  ends must not
- * decrease and stay within [0, M]; where it does not, which rows are computed
- * is unspecified (nothing outside the operands is touched).
+ * can be queued, or captured into a graph, before they are known.  An end below
+ * an earlier one counts as that one (no rows), below 0 as 0, past M as M.
  * Like the products these use the device's status block (its first call on a
  * device may not be captured) and their waits are bounded by the watchdog; they
  * need no workspace, so calls on different streams are independent.

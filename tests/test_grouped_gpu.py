@@ -117,6 +117,26 @@ def test_rows_long_reduction_and_many_tiles():
     check(*run_rows([5, 0, 1, 64], 4096, 4096, G.KMAJOR, BF16, normal), 4096, BF16)
 
 
+@pytest.mark.parametrize("layout", [G.KMAJOR, G.MNMAJOR])
+@pytest.mark.parametrize("sizes", [[255, 256, 257, 0, 700], [300, 1, 0, 511, 513], [1500], [31, 33, 0, 1000, 97, 129]])
+def test_rows_of_many_tiles(sizes, layout):
+    """Sizes for which CTA pairs are chosen."""
+    check(*run_rows(sizes, 4196, 1000, layout, F32, normal, 3), 1000, F32)
+    check(*run_rows(sizes, 4101, 1090, layout, BF16, normal, 0, 4), 1090, BF16)
+    got, ref, _ = run_rows(sizes, 5000, 1064, layout, F32, ints, 1)
+    assert torch.equal(got, ref)
+
+
+@pytest.mark.parametrize("layout", [G.KMAJOR, G.MNMAJOR])
+@pytest.mark.parametrize("M", [1, 3, 16, 33, 64])
+@pytest.mark.parametrize("N,K", [(130, 8192), (257, 4100), (1000, 4096), (2049, 2050), (4100, 1030)])
+def test_few_rows_with_k_split_over_clusters(M, N, K, layout):
+    for c_type in (F32, BF16):
+        check(*run_rows([M], N, K, layout, c_type, normal, 1, M), K, c_type)
+    got, ref, _ = run_rows([0, M, 0, 0], N, K, layout, F32, ints)
+    assert torch.equal(got, ref)
+
+
 def test_rows_without_reduction():
     for sizes in ([3, 0, 70], [500, 1]):
         M, N = sum(sizes) + 4, 40
@@ -196,6 +216,18 @@ def test_gradient_long_reduction_and_many_tiles():
     check(*run_grad([77] * 30 + [0] * 5, 700, 520, G.MNMAJOR, BF16, normal), 77, BF16)
 
 
+@pytest.mark.parametrize("layout", [G.KMAJOR, G.MNMAJOR])
+@pytest.mark.parametrize("sizes", [[255, 256, 257, 0, 700], [300, 1, 0, 511, 513], [31, 33, 0, 1000, 97, 129]])
+def test_gradient_of_many_tiles(sizes, layout):
+    """Sizes for which CTA pairs are chosen."""
+    check(*run_grad(sizes, 4196, 2100, layout, F32, normal, 3), max(sizes), F32)
+    check(*run_grad(sizes, 3001, 4101, layout, BF16, normal, 0, 4), max(sizes), BF16)
+    old = ints(9, len(sizes) * 4000, 2500).view(len(sizes), 4000, 2500)
+    if layout == G.KMAJOR:
+        got, ref, _ = run_grad(sizes, 4000, 2500, layout, F32, ints, 1, 2, 1.0, old)
+        assert torch.equal(got, ref + old.double().cuda())
+
+
 @pytest.mark.parametrize("d_type", [F32, BF16])
 @pytest.mark.parametrize("beta", [1.0, 0.5])
 def test_gradient_is_added(d_type, beta):
@@ -218,8 +250,9 @@ def test_gradient_without_rows():
 
 
 @pytest.mark.parametrize("layout", [G.KMAJOR, G.MNMAJOR])
-def test_gradient_nan_stays_with_its_expert(layout):
-    sizes, N, K = [37, 0, 50, 13, 90], 72, 136
+@pytest.mark.parametrize("N,K", [(72, 136), (4200, 4200)])       # single CTAs, pairs
+def test_gradient_nan_stays_with_its_expert(N, K, layout):
+    sizes = [37, 0, 50, 13, 90]
     M = sum(sizes)
     a, d = normal(1, M, K), normal(2, M, N)
     a[87:100] = float("nan")            # all of expert 3's rows
@@ -233,17 +266,27 @@ def test_gradient_nan_stays_with_its_expert(layout):
     assert bool(bad[3].all()) and not bool(bad[[0, 1, 2, 4]].any())
 
 
-def test_ends_outside_the_buffer_are_cut():
-    """Ends past M, negative or falling: unspecified rows, but nothing outside C is written."""
-    M, N, K = 40, 24, 16
-    A, B, C = Buffer(M, K, torch.bfloat16, fill=normal(1, M, K)), Weights(3, N, K, torch.bfloat16), Buffer(M, N, torch.float32)
-    W = Weights(3, N, K, torch.float32)
-    for ends in ([1 << 30, 50, 60], [-5, 10, 1000], [30, 10, 40], [-(1 << 31), -1, 0]):
-        e = torch.tensor(ends, dtype=torch.int32, device="cuda")
-        G.gemm_bf16_grouped(A.ptr, B.ptr, e, C.ptr, 3, M, N, K, A.ld, B.ld, B.stride, C.ld)
-        G.gemm_bf16_grouped_wgrad(C.ptr, A.ptr, e, W.ptr, 3, M, N, K, 2 * C.ld, A.ld, W.ld, W.stride)
-        G.gemm_check_device_status()
-        assert C.guards_ok() and W.guards_ok()
+@pytest.mark.parametrize("ends", [[1 << 30, 50, 60], [-5, 10, 1000], [30, 10, 40], [-(1 << 31), -1, 0], [40, 0, 40],
+                                  [40, 0, 40] * 20, [5, 3, 9, 8, 8, 100, 7]])
+def test_ends_are_made_to_rise_within_the_buffer(ends):
+    """An end past M counts as M, below 0 as 0, below an earlier one as that one."""
+    M, N, K, E = 40, 24, 16, len(ends)
+    fixed = np.maximum.accumulate(np.clip(ends, 0, M))
+    sizes = np.diff(np.concatenate([[0], fixed])).tolist()
+    a, w, d = ints(1, M, K), ints(2, E * N, K), ints(3, M, N)
+    A, D = Buffer(M, K, torch.bfloat16, fill=a), Buffer(M, N, torch.bfloat16, fill=d)
+    B, C, W = Weights(E, N, K, torch.bfloat16, w.view(E, N, K)), Buffer(M, N, torch.float32), Weights(E, N, K, torch.float32)
+    e = torch.tensor(ends, dtype=torch.int32, device="cuda")
+    G.gemm_bf16_grouped(A.ptr, B.ptr, e, C.ptr, E, M, N, K, A.ld, B.ld, B.stride, C.ld)
+    G.gemm_bf16_grouped_wgrad(D.ptr, A.ptr, e, W.ptr, E, M, N, K, D.ld, A.ld, W.ld, W.stride)
+    G.gemm_check_device_status()
+    assert C.guards_ok() and W.guards_ok()
+    lo = 0
+    for i, n in enumerate(sizes):
+        assert torch.equal(C.get()[lo:lo + n], a[lo:lo + n] @ w.view(E, N, K)[i].t())
+        assert torch.equal(W.get()[i].cpu(), d[lo:lo + n].t() @ a[lo:lo + n])
+        lo += n
+    assert bool((C.t[lo:].contiguous().view(torch.uint8) == 0xFF).all())
 
 
 def test_same_bits_every_time():
