@@ -8,6 +8,7 @@
 #include <atomic>
 #include <cmath>
 #include <cstdint>
+#include <cstring>
 
 #include "b200gemm.h"
 #include "fp4_quantize_sm100.cuh"
@@ -515,6 +516,59 @@ gemm_status_t gemm_fp4(const uint8_t *A, const uint8_t *sfa, const float *scale_
     c.args.timeout_ns = b200::host::watchdog_ns(K);
     return format == GEMM_FP4_NV ? dispatch_fp4<true>(dev, sm_count, c, stream)
                                  : dispatch_fp4<false>(dev, sm_count, c, stream);
+}
+
+gemm_status_t gemm_call(gemm_call_t entry, const void *words) {
+    static const int kWords[4] = {15, 16, 12, 16};
+    if (!words || static_cast<int>(entry) < 0 || static_cast<int>(entry) > GEMM_CALL_FP4) return GEMM_ERR_INVALID_VALUE;
+    int64_t w[16];
+    std::memcpy(w, words, 8 * static_cast<size_t>(kWords[entry]));
+    bool fits = true;
+    const auto ptr = [&](int i) { return reinterpret_cast<void *>(static_cast<uintptr_t>(w[i])); };
+    const auto code = [&](int i) {
+        fits = fits && w[i] == static_cast<int>(w[i]);
+        return static_cast<int>(w[i]);
+    };
+    const auto type = [&](int i) { return static_cast<gemm_out_t>(code(i)); };
+    const auto layout = [&](int i) { return static_cast<gemm_layout_t>(code(i)); };
+    const auto format = [&](int i) { return static_cast<gemm_fp4_t>(code(i)); };
+    const auto stream = [&](int i) { return static_cast<cudaStream_t>(ptr(i)); };
+    switch (entry) {
+        case GEMM_CALL_BF16_GROUPED: {
+            const gemm_out_t c_type = type(12);
+            const gemm_layout_t b_layout = layout(13);
+            if (!fits) return GEMM_ERR_INVALID_VALUE;
+            return gemm_bf16_grouped(ptr(0), ptr(1), static_cast<const int32_t *>(ptr(2)), ptr(3), w[4], w[5], w[6], w[7],
+                                     w[8], w[9], w[10], w[11], c_type, b_layout, stream(14));
+        }
+        case GEMM_CALL_BF16_GROUPED_WGRAD: {
+            const gemm_out_t db_type = type(12);
+            const gemm_layout_t db_layout = layout(13);
+            if (!fits) return GEMM_ERR_INVALID_VALUE;
+            float beta;
+            std::memcpy(&beta, &w[14], 4);
+            return gemm_bf16_grouped_wgrad(ptr(0), ptr(1), static_cast<const int32_t *>(ptr(2)), ptr(3), w[4], w[5], w[6],
+                                           w[7], w[8], w[9], w[10], w[11], db_type, db_layout, beta, stream(15));
+        }
+        case GEMM_CALL_FP4_QUANTIZE: {
+            const gemm_fp4_t form = format(8);
+            const gemm_out_t x_type = type(9);
+            const gemm_layout_t x_layout = layout(10);
+            if (!fits) return GEMM_ERR_INVALID_VALUE;
+            return gemm_fp4_quantize(ptr(0), static_cast<const float *>(ptr(1)), static_cast<uint8_t *>(ptr(2)),
+                                     static_cast<uint8_t *>(ptr(3)), w[4], w[5], w[6], w[7], form, x_type, x_layout,
+                                     stream(11));
+        }
+        default: {
+            const gemm_fp4_t form = format(13);
+            const gemm_out_t c_type = type(14);
+            if (!fits) return GEMM_ERR_INVALID_VALUE;
+            return gemm_fp4(static_cast<const uint8_t *>(ptr(0)), static_cast<const uint8_t *>(ptr(1)),
+                            static_cast<const float *>(ptr(2)), static_cast<const uint8_t *>(ptr(3)),
+                            static_cast<const uint8_t *>(ptr(4)), static_cast<const float *>(ptr(5)), ptr(6), w[7], w[8],
+                            w[9], w[10], w[11], w[12], form, c_type, stream(15));
+        }
+    }
 }
 
 }  // extern "C"

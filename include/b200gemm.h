@@ -574,6 +574,21 @@ B200GEMM_API gemm_status_t gemm_fp4(const uint8_t *A, const uint8_t *sfa, const 
                                     int64_t lda, int64_t ldb, int64_t ldc, gemm_fp4_t format, gemm_out_t c_type,
                                     cudaStream_t stream);
 
+/*
+ * gemm_call: one of the entry points below with its arguments in a block of 64-bit
+ * words, in their order (pointers, sizes and enumerators as integers, a float's
+ * bits in the low half), for bindings in which a call costs by the argument.  A
+ * word that its argument's type does not hold, or an unknown entry point, is
+ * GEMM_ERR_INVALID_VALUE.
+ */
+typedef enum {
+    GEMM_CALL_BF16_GROUPED = 0,         /* 15 words */
+    GEMM_CALL_BF16_GROUPED_WGRAD = 1,   /* 16 */
+    GEMM_CALL_FP4_QUANTIZE = 2,         /* 12 */
+    GEMM_CALL_FP4 = 3                   /* 16 */
+} gemm_call_t;
+B200GEMM_API gemm_status_t gemm_call(gemm_call_t entry, const void *words);
+
 /* Synchronises `stream`, then reports and clears the device watchdog status
  * of the current device (the status blocks of every entry point, the static
  * one of gemm_bf16_noalloc included): GEMM_OK, or GEMM_ERR_TIMEOUT if a

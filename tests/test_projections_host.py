@@ -243,6 +243,42 @@ def test_binding_wants_operands_without_a_pitch_contiguous(name, what, host_is_t
 
 
 @no_gpu
+def test_binding_refuses_what_is_no_64_bit_number(host_is_the_device):
+    for name in CALLS:
+        for bad in (1 << 63, 2.5, "8"):
+            with pytest.raises(G.GemmError) as e:
+                CALLS[name](operands(), stream=bad) if bad == 1 << 63 else \
+                    G.gemm_fp4_quantize(None, None, None, None, bad, 32, 32, 16, stream=0)
+            assert e.value.status == INVALID
+
+
+def test_call_by_words():
+    """The words mean what the entry points' arguments mean, and nothing that a type does not hold passes."""
+    import struct
+    call = lambda entry, form, *w: G.lib.gemm_call(entry, struct.pack(form, *w))  # noqa: E731
+    assert call(0, "<15q", *P[:4], 4, 64, 128, 96, 96, 96, 128 * 96, 128, 0, 2, 0) == INVALID      # layout
+    assert call(0, "<15q", *P[:4], 4, 0, 128, 96, 96, 96, 128 * 96, 128, 0, 0, 0) == OK
+    assert call(0, "<15q", *P[:4], 4, 0, 128, 96, 96, 96, 128 * 96, 128, 1 << 32, 0, 0) == INVALID
+    assert call(0, "<15q", *P[:3], P[0], 4, 64, 128, 96, 96, 96, 128 * 96, 128, 0, 0, 0) == ALIAS
+    assert call(1, "<14qf4xq", *P[:4], 4, 64, 0, 96, 96, 96, 96, 128 * 96, 0, 0, 1.0, 0) == OK
+    assert call(1, "<14qf4xq", *P[:4], 4, 64, 128, 96, 128, 96, 98, 128 * 96, 0, 0, 1.0, 0) == MISALIGNED
+    assert call(1, "<14qf4xq", *P[:4], 4, 64, 128, 96, 128, 96, 96, 128 * 96, 0, (1 << 32) + 1, 1.0, 0) == INVALID
+    assert call(2, "<12q", P[0], 0, P[1], P[2], 64, 0, 128, 64, NV, BF16, KM, 0) == OK
+    assert call(2, "<12q", P[0], 0, P[1], P[0], 64, 128, 128, 64, NV, BF16, KM, 0) == ALIAS
+    assert call(2, "<12q", P[0], 0, P[1], P[2], 64, 128, 128, 64, NV - (1 << 32), BF16, KM, 0) == INVALID
+    assert call(3, "<16q", P[0], P[1], 0, P[2], P[3], 0, P[4], 0, 128, 256, 128, 128, 128, NV, F32, 0) == OK
+    assert call(3, "<16q", P[0], P[1], 0, P[2], P[3], 0, P[4], 64, 128, 256, 112, 128, 128, NV, F32, 0) == INVALID
+    assert call(3, "<16q", P[0], P[1], 0, P[2], P[3], 0, P[4], 64, 128, 256, 128, 128, 128, NV, 1 << 32, 0) == INVALID
+    assert call(4, "<16q", *[0] * 16) == INVALID and call(-1, "<16q", *[0] * 16) == INVALID
+    assert G.lib.gemm_call(0, None) == INVALID
+    if not torch.cuda.is_available():
+        assert call(0, "<15q", *P[:4], 4, 64, 128, 96, 96, 96, 128 * 96, 128, 0, 0, 0) == NO_DEVICE
+        assert call(1, "<14qf4xq", *P[:4], 4, 64, 128, 96, 128, 96, 96, 128 * 96, 0, 0, 1.0, 0) == NO_DEVICE
+        assert call(2, "<12q", P[0], P[5], P[1], P[2], 64, 128, 128, 64, NV, BF16, KM, 0) == NO_DEVICE
+        assert call(3, "<16q", P[0], P[1], 0, P[2], P[3], 0, P[4], 64, 128, 256, 128, 128, 128, NV, F32, 0) == NO_DEVICE
+
+
+@no_gpu
 def test_binding_refuses_formats_it_does_not_know(host_is_the_device):
     for name in ("quantize", "product"):
         with pytest.raises(G.GemmError) as e:
