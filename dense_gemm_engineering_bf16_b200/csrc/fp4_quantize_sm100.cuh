@@ -194,7 +194,10 @@ struct Fp4QuantizeArgs {
 // X stored K-major (M rows of K): VPT sixteens per thread, one NV block each or
 // half an MX block; 4 neighbouring threads (MX: 8) hold the blocks of a word of
 // scales.  A row takes blockDim.x threads in each of `parts` blocks; short rows
-// share a block (blockDim.y).
+// share a block (blockDim.y).  8192 x 8192 from bf16: 30 us, 88 % of the copy rate
+// (either format; 57 with eights of a warp's lanes, shuffles for the maxima and
+// scalar arithmetic: the instructions, not memory, were the time), from fp32 45 us,
+// 104 %; one row of 8192: 1.6 us.  32-byte loads where the rows' alignment allows.
 template <int XT, bool NV, int VPT, bool WIDE>
 __global__ void __launch_bounds__(256) fp4_quantize_kernel(Fp4QuantizeArgs a, unsigned parts) {
     wait_for_stream();
@@ -209,7 +212,7 @@ __global__ void __launch_bounds__(256) fp4_quantize_kernel(Fp4QuantizeArgs a, un
         const int64_t e = first + 16 * i * static_cast<int64_t>(blockDim.x);
         if (e < a.K) load_raw16<XT, WIDE>(p + e * elem_bytes<XT>, r[i]);
     }
-    const float g = NV && a.g ? __ldg(a.g) : 1.0f;
+    const float g = NV && a.g ? __ldcg(a.g) : 1.0f;
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
         const int64_t e = first + 16 * i * static_cast<int64_t>(blockDim.x);
@@ -235,6 +238,8 @@ __global__ void __launch_bounds__(256) fp4_quantize_kernel(Fp4QuantizeArgs a, un
 // holds whole blocks, without a shuffle.  The four warps of a block take 128
 // consecutive K; their codes and scales meet in shared memory, from where
 // each row i goes out as 64 bytes of codes and one (MX) or two words of scales.
+// 8192 x 8192 from bf16: MX 28.6 us, 91 % of the copy rate, NV 38.7 (a division per
+// 16 values on 89 registers); 4096 x 4096 NV 11.7; from fp32 45 to 46.
 template <int XT, bool NV>
 __global__ void __launch_bounds__(128) fp4_quantize_mn_kernel(Fp4QuantizeArgs a, unsigned i_tiles) {
     constexpr int kPitch = 64 + 16, B = kFp4Block<NV>, WORDS = NV ? 2 : 1;
@@ -275,7 +280,7 @@ __global__ void __launch_bounds__(128) fp4_quantize_mn_kernel(Fp4QuantizeArgs a,
                 }
             }
         }
-        const float g = NV && a.g ? __ldg(a.g) : 1.0f;
+        const float g = NV && a.g ? __ldcg(a.g) : 1.0f;
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
             if (k0 < a.K) {

@@ -20,9 +20,18 @@
 // r / 32, lane r % 32 of every quarter, four bytes).  E4M3: a tile is one
 // MMA's; E8M0: two MMAs', the second one takes bytes 2 and 3.
 //
-// SPLIT: a cluster of 2, 4 or 8 CTAs owns a tile, each over a share of K.  Each
-// member sums some of the tile's rows of C over all members' fp32 partials,
-// which cross through distributed shared memory, in member order.
+// SPLIT: a cluster of 2, 4 or 8 CTAs owns a tile, each over a share of K, and
+// their partials meet in distributed shared memory (cluster_sum).
+//
+// What bounds it: shared memory for pairs (per stage and SM the MMAs read 32 KB,
+// TMA writes 38 and the scale copies read 6, 600 cycles at 128 bytes each against
+// the MMAs' 512; 707 measured, 590 without the loads, 535 without the MMAs) and
+// the power limit: 8192^3 207 to 235 us (5.3 to 4.7 PFLOP/s, tensor pipe 73 %
+// busy), 4096 x 8192 x 4096 MX 57 us.  Single CTAs: the MMA of 128 x 128 x 64, 122
+// cycles instead of the 64 that its size would take: 512 x 4096 x 4096 8.8 us.
+// Few rows: memory and the start and end (3.6 us without any work): one row of
+// 8192 x 8192, 37.8 MB, 11.4 us; 64 rows 14.3.
+// Fewer scale slots cost time (two: 20 %), more than five gain nothing.
 #pragma once
 #include <cstdint>
 
@@ -297,7 +306,7 @@ gemm_fp4_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__
         const int part = static_cast<int>(warp - Cfg::EPI0) / 4;
         constexpr int PARTS = Cfg::EPI_WARPS / 4;               // fours of warps that share a tile's rows of C
         constexpr int CHUNKS = Cfg::BQ / 32 / PARTS;            // of 32 rows, for each of them
-        const float alpha = (a.ga ? __ldg(a.ga) : 1.0f) * (a.gb ? __ldg(a.gb) : 1.0f);
+        const float alpha = (a.ga ? __ldcg(a.ga) : 1.0f) * (a.gb ? __ldcg(a.gb) : 1.0f);
         const int64_t esize = a.f32 ? 4 : 2;
         ColumnsOut to(base + Cfg::OUT_OFF, part, sub, lane, a.ldc * esize);
         const int mine = static_cast<int>(sub * 32u + lane);   // this lane's column

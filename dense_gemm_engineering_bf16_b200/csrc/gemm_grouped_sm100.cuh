@@ -32,6 +32,22 @@
 // Every CTA works out the tiles from `ends` itself: the numbers of tiles up to
 // each expert in shared memory, a binary search per tile.  Rows outside every
 // expert are neither computed nor written.
+//
+// What bounds it (one B200, in bursts; runs of many seconds are held by the
+// power limit to 1.2 to 1.6 GHz of 1.97 and take up to a quarter longer):
+//   large experts  the tensor pipe and its power: 16384 x 4096 x 2048 in one group
+//                  185 to 194 us (1.4 to 1.5 PFLOP/s), in 32 of different sizes 218
+//                  to 232 (tensor pipe 80 % busy, every weight read once; narrower
+//                  tiles load P more often for the same work)
+//   few rows each  memory: 128 rows on 64 experts of 2048 x 4096, 740 MB in 125 us,
+//                  92 % of the copy rate
+//   one token      the start and the end (3.4 us without any work; a pair of CTAs 6)
+//                  and the ramp between: 2 of 8 experts of 4096 x 2048, 33.6 MB,
+//                  10.9 us
+//   gradient       of 32 experts, 512 rows each, 4096 x 2048, bf16: 273 us, the L2
+//                  bandwidth that operands (2.1 GB) and results share; with a few
+//                  rows each the write-back, 3.0 (bf16) to 4.3 TB/s (fp32).  8 experts,
+//                  1000 rows, 1024 x 512, fp32: 8.5 us
 #pragma once
 #include <cstdint>
 
@@ -225,7 +241,8 @@ gemm_grouped_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_consta
         tmem_relinquish<CG>();
     }
     wait_for_stream();
-    for (int e = threadIdx.x; e < a.groups; e += Cfg::THREADS) ends[e] = min(max(__ldg(a.ends + e), 0), a.M);
+    // from L2: the kernel before may have written them while this block was already here
+    for (int e = threadIdx.x; e < a.groups; e += Cfg::THREADS) ends[e] = min(max(__ldcg(a.ends + e), 0), a.M);
     tc_fence_before_sync();
     __syncthreads();
     if (warp == 0) {
