@@ -117,7 +117,10 @@ __device__ __forceinline__ uint32_t e2m1_codes8(const float (&q)[8]) {
 // iterative refinement (the residual is exact in an fma) gives the rounded
 // quotient (P. Markstein, "Computation of elementary functions on the IBM RISC
 // System/6000 processor", 1990).  Where the scale has saturated, quotients are
-// bounded first, so that the residual stays finite: all past 6 are a 6.
+// bounded first, so that the residual stays finite: all past 6 are a 6.  The
+// method's exception, a divisor b = 2^k (1 - 2^-24), moves no code: x / b is then
+// x 2^-k (1 + 2^-24 + ..), half a step beside a border only for x = 2^(k-2), whose
+// refined quotient is 1/4 (1 + 2^-23), as it has to be; dividing such blocks cost 4 %.
 template <bool NV>
 __device__ __forceinline__ uint32_t fp4_codes8(const float *v, const Fp4Scale &s) {
     float q[8];
@@ -238,10 +241,10 @@ __global__ void __launch_bounds__(256) fp4_quantize_kernel(Fp4QuantizeArgs a, un
 // holds whole blocks, without a shuffle.  The four warps of a block take 128
 // consecutive K; their codes and scales meet in shared memory, from where
 // each row i goes out as 64 bytes of codes and one (MX) or two words of scales.
-// 8192 x 8192 from bf16: MX 28.6 us, 91 % of the copy rate, NV 38.7 (a division per
-// 16 values on 89 registers); 4096 x 4096 NV 11.7; from fp32 45 to 46.
+// 8192 x 8192 from bf16: MX 28.1 us, 93 % of the copy rate, NV 36.9 with six blocks
+// per SM (40.5 with five, 41.1 with eight); 4096 x 4096 NV 11.7; from fp32 45 to 46.5.
 template <int XT, bool NV>
-__global__ void __launch_bounds__(128) fp4_quantize_mn_kernel(Fp4QuantizeArgs a, unsigned i_tiles) {
+__global__ void __launch_bounds__(128, XT == kF32 ? 5 : NV ? 6 : 7) fp4_quantize_mn_kernel(Fp4QuantizeArgs a, unsigned i_tiles) {
     constexpr int kPitch = 64 + 16, B = kFp4Block<NV>, WORDS = NV ? 2 : 1;
     __shared__ __align__(16) uint8_t tile[64 * kPitch];
     __shared__ __align__(8) uint8_t scales[64][4 * WORDS];

@@ -63,7 +63,10 @@ def reference_quantise(x, g, form):
     """x: fp64 of fp32 values, finite.  Codes [rows, K] and scale bytes [rows, blocks]."""
     b = x.reshape(x.shape[0], -1, BLOCK[form])
     top = np.abs(b).max(2)
-    f32 = lambda v: v.astype(np.float32).astype(np.float64)
+    def f32(v):
+        with np.errstate(over="ignore"):
+            return v.astype(np.float32).astype(np.float64)
+
     if form == MX:
         byte = np.searchsorted(6.0 * 2.0 ** np.arange(-127, 128, dtype=np.float64), top, side="left")
         q = b * 2.0 ** (127.0 - byte)[:, :, None]
@@ -128,9 +131,16 @@ def test_quantiser_at_ties_and_borders(form):
             rows.append(np.concatenate([part, part]))
     for top in (6.0, 6.03125, 5.96875, 6.375, 448 * 6, 500 * 6, 3e38, 1e-38, 1e-42, 0.0117, 0.005):
         rows.append(np.full(32, top) * np.linspace(-1, 1, 32))
+    for unit in (float(np.nextafter(np.float32(0.25), np.float32(0))), 1e-20, 1e20):      # ties of those g as well
+        for s in (1.0, 1.125, 1.875):
+            t = np.concatenate([border[:7], -border[:7], [6.0, 0.0]]) * unit * s
+            rows.append(np.concatenate([t, t]))
     x = torch.from_numpy(np.array(rows)).float()
+    ones = float(np.nextafter(np.float32(0.25), np.float32(0)))      # a mantissa of ones, as s g has it for s a power of two
+    sixth = float(np.float32(np.nextafter(np.float32(1), np.float32(0)) / 6))
+    assert np.float32(6) * np.float32(sixth) == np.nextafter(np.float32(1), np.float32(0))
     for x_type in (F32, BF16):
-        for g in ((None,) if form == MX else (None, 0.37)):
+        for g in ((None,) if form == MX else (None, 0.37, ones, sixth, 1e-20, 1e20)):
             codes, scales, _, stored = quantise(x, form, x_type, G.KMAJOR, g)
             want, byte = reference_quantise(stored, np.float64(np.float32(1.0 if g is None else g)), form)
             assert np.array_equal(scales, byte)
