@@ -143,15 +143,15 @@ gemm_fp4_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__
     wait_for_stream();
     const uint32_t tmem_base = static_cast<uint32_t>(uniform(static_cast<int>(*tmem_slot_ptr)));
 
-    const int tiles_p = (a.N + Cfg::BP - 1) / Cfg::BP, tiles_q = (a.M + Cfg::BQ - 1) / Cfg::BQ;
+    const int tiles_p = parts_of(a.N, Cfg::BP), tiles_q = parts_of(a.M, Cfg::BQ);
     const int num_tiles = tiles_p * tiles_q;
-    const int blocks = (a.K + Cfg::BK - 1) / Cfg::BK;
+    const int blocks = parts_of(a.K, Cfg::BK);
     const int kb0 = static_cast<int>(static_cast<int64_t>(blocks) * me / members);
     const int kb1 = static_cast<int>(static_cast<int64_t>(blocks) * (me + 1) / members);
     const int first = static_cast<int>(blockIdx.x) / cluster, step = static_cast<int>(gridDim.x) / cluster;
     auto mma_n = [&](int tq) {
         const int rows = min(Cfg::BQ, a.M - tq * Cfg::BQ);
-        return (rows + Cfg::N_STEP - 1) / Cfg::N_STEP * Cfg::N_STEP;
+        return parts_of(rows, Cfg::N_STEP) * Cfg::N_STEP;
     };
 
     if (warp == 0) {

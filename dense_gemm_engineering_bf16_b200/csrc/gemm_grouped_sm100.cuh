@@ -134,14 +134,13 @@ struct GroupedTiles {
     Divisor band, per;                  // tiles of eight Q tiles' band; of a group (gradient)
 
     __device__ __forceinline__ static int width_of(int extent) {
-        const int n = max((extent + Cfg::BQ - 1) / Cfg::BQ, 1);
-        return ((extent + n - 1) / n + Cfg::N_STEP - 1) / Cfg::N_STEP * Cfg::N_STEP;
+        return parts_of(parts_of(extent, max(parts_of(extent, Cfg::BQ), 1)), Cfg::N_STEP) * Cfg::N_STEP;
     }
 
     __device__ __forceinline__ GroupedTiles(const GroupedArgs &a, const int *ends_, const int *tiles_, const int *widths_,
                                             int members, int me)
         : ends(ends_), tiles(tiles_), widths(widths_), groups(a.groups), P(a.P), Q(a.Q), k0(0), k_len(a.K),
-          tiles_p((a.P + Cfg::BP - 1) / Cfg::BP), tiles_q((a.Q + Cfg::BQ - 1) / Cfg::BQ), width(width_of(a.Q)),
+          tiles_p(parts_of(a.P, Cfg::BP)), tiles_q(parts_of(a.Q, Cfg::BQ)), width(width_of(a.Q)),
           band(8 * static_cast<uint32_t>(tiles_p)), per(static_cast<uint32_t>(max(tiles_p * tiles_q, 1))) {
         if (members > 1) {
             const int64_t blocks = (int64_t(a.K) + Cfg::BK - 1) / Cfg::BK;
@@ -168,7 +167,7 @@ struct GroupedTiles {
             local = tile - (lo ? tiles[lo - 1] : 0);
             t.q0 = lo ? ends[lo - 1] : 0;
             extent = ends[lo] - t.q0;
-            n = (extent + Cfg::BQ - 1) / Cfg::BQ;
+            n = parts_of(extent, Cfg::BQ);
             wide = widths[lo];
             t.k0 = k0;
             t.k_len = k_len;
@@ -189,7 +188,7 @@ struct GroupedTiles {
         t.p0 = tp * Cfg::BP;
         t.q0 += tq * wide;
         t.count = min(wide, extent - tq * wide);
-        t.n = (t.count + Cfg::N_STEP - 1) / Cfg::N_STEP * Cfg::N_STEP;
+        t.n = parts_of(t.count, Cfg::N_STEP) * Cfg::N_STEP;
         return t;
     }
 };
@@ -248,7 +247,7 @@ gemm_grouped_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_consta
     if (warp == 0) {
         // An end below an earlier one counts as that one, so that the experts'
         // rows never overlap; then the tiles up to each expert's last.
-        const int tiles_p = (a.P + Cfg::BP - 1) / Cfg::BP;
+        const int tiles_p = parts_of(a.P, Cfg::BP);
         int top = 0, before = 0;
         for (int e0 = 0; e0 < a.groups; e0 += 32) {
             const int e = e0 + static_cast<int>(lane);
@@ -265,7 +264,7 @@ gemm_grouped_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_consta
             int n = 0;
             if (e < a.groups) {
                 ends[e] = end;
-                n = (end - start + Cfg::BQ - 1) / Cfg::BQ * tiles_p;
+                n = parts_of(end - start, Cfg::BQ) * tiles_p;
                 widths[e] = GroupedTiles<Cfg>::width_of(end - start);
             }
             if constexpr (!GRAD) {
@@ -298,8 +297,8 @@ gemm_grouped_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_consta
             const int q_cta = t.n / CG, q = t.q0 + static_cast<int>(rank) * q_cta;
             const int boxes = (q_cta + Cfg::QBOX - 1) / Cfg::QBOX;
             const uint32_t bytes = Cfg::P_BYTES + boxes * Cfg::QBOX * Cfg::BK * 2;
-            int k = t.k0;
-            for (int left = t.k_len; left > 0; left -= Cfg::BK, k += Cfg::BK) {
+            for (int left = t.k_len; left > 0; left -= Cfg::BK) {
+                const int k = t.k0 + (t.k_len - left);
                 if (!mbar_wait_warp(empty_bar(stage), phase ^ 1u, abort_flag, 2 * a.timeout_ns)) {
                     if (issue) record_timeout(a.status, abort_flag, abort_slot, cluster, kRoleProducer * 16 + kBarEmpty);
                     ok = false;
@@ -417,7 +416,7 @@ gemm_grouped_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_consta
         uint32_t blocks = 0, parity = 0;       // blocks so far; bit s: parity of fix[s]
         for (int tile = first; tile < num_tiles; tile += step) {
             const GroupedTile t = tile_at(tile);
-            blocks += (t.k_len + Cfg::BK - 1) / Cfg::BK;
+            blocks += parts_of(t.k_len, Cfg::BK);
             if (t.k_len % 16 == 0) continue;
             const uint32_t stage = (blocks - 1) % STAGES;
             uint32_t ready = 1;

@@ -177,6 +177,9 @@ struct Divisor {
     }
 };
 
+// Parts of at most d that x >= 0 takes; x + d - 1 might not be an int.
+__device__ __forceinline__ int parts_of(int x, int d) { return x > 0 ? (x - 1) / d + 1 : 0; }
+
 // x / d for 1 <= d <= 8.
 __device__ __forceinline__ uint32_t divide_small(uint32_t x, uint32_t d) {
     switch (d) {

@@ -349,3 +349,54 @@ def test_decoding_step_captured_into_a_graph(T):
         u = up.view(E, F, D).double()[choice.view(-1)[order].cuda()]
         check(out.double(), torch.einsum("md,mfd->mf", a.double(), u), torch.einsum("md,mfd->mf", a.double().abs(), u.abs()),
               D, F32)
+
+
+MOST = (1 << 31) - 1
+
+
+def test_as_many_rows_as_an_int_counts():
+    """2^31 - 1 rows of one column: tiles, rows and offsets at the ends of their types."""
+    a = torch.ones(MOST, 8, dtype=torch.bfloat16, device="cuda")
+    c = torch.zeros(MOST, 8, dtype=torch.bfloat16, device="cuda")
+    at = [0, 255, 256, 1 << 24, (1 << 30) + 5, MOST - 257, MOST - 1]
+    a[at, 0] = torch.arange(2.0, 2.0 + len(at), device="cuda").bfloat16()
+    w = torch.tensor([[3.0] + [float("nan")] * 7, [5.0] + [float("nan")] * 7], device="cuda").bfloat16()
+    ends = torch.tensor([MOST - 3, MOST], dtype=torch.int32, device="cuda")
+    G.gemm_bf16_grouped(a, w, ends, c, 2, MOST, 1, 1, 8, 8, 8, 8, BF16)
+    G.gemm_check_device_status()
+    want = [3.0 * (2 + i) for i in range(len(at) - 1)] + [5.0 * (1 + len(at))]
+    assert c[at, 0].tolist() == want
+    assert float(c[MOST - 4, 0]) == 3.0 and float(c[MOST - 3, 0]) == 5.0 and float(c[MOST - 2, 0]) == 5.0
+    c[at, 0] = 3.0
+    c[MOST - 3:, 0] = 3.0
+    assert bool((c[:, 0] == 3.0).all()) and not bool(c[:, 1:].any())
+
+
+def test_as_many_columns_as_an_int_counts():
+    w = torch.ones(MOST, 8, dtype=torch.bfloat16, device="cuda")
+    at = [0, 127, 128, 1 << 24, MOST - 129, MOST - 1]
+    w[at, 0] = torch.arange(2.0, 2.0 + len(at), device="cuda").bfloat16()
+    a = torch.full((1, 8), 3.0, device="cuda").bfloat16()
+    c = torch.zeros(1, MOST + 1, device="cuda")
+    ends = ends_of([1])
+    for layout, ldb in ((G.KMAJOR, 8), (G.MNMAJOR, MOST + 1)):
+        c.zero_()
+        b = w if layout == G.KMAJOR else torch.nn.functional.pad(w[:, 0], (0, 1))
+        G.gemm_bf16_grouped(a, b, ends, c, 1, 1, MOST, 1, 8, ldb, 0, MOST + 1, F32, layout)
+        G.gemm_check_device_status()
+        assert c[0, at].tolist() == [3.0 * (2 + i) for i in range(len(at))]
+        c[0, at] = 3.0
+        assert bool((c[0, :MOST] == 3.0).all()) and float(c[0, MOST]) == 0.0
+
+
+def test_as_long_a_4_bit_reduction_as_an_int_counts():
+    K, N = MOST - 31, 3
+    q, w = (torch.zeros(n, K // 2, dtype=torch.uint8, device="cuda") for n in (1, N))
+    sq, sw = (torch.full((G.gemm_fp4_scale_bytes(n, K, MX),), 127, dtype=torch.uint8, device="cuda") for n in (1, N))
+    for i, k in enumerate([0, 255, 256, 1 << 24, (1 << 30) + 7, K - 33, K - 1]):
+        q[0, k // 2] = 2 << 4 * (k & 1)                    # 1
+        w[:, k // 2] = (1 + i) % 8 << 4 * (k & 1)          # 0.5, 1, 1.5, 2, 3, 4, 6
+    c = torch.empty(1, 4, device="cuda")
+    G.gemm_fp4(q, sq, None, w, sw, None, c, 1, N, K, K // 2, K // 2, 4, MX)
+    G.gemm_check_device_status()
+    assert c[0, :N].tolist() == [18.0] * N
