@@ -56,14 +56,14 @@ bool overlap(const Mat &a, const Mat &b) {
     return overlaps(a.p, a.count, a.span(), a.stride, a.esize, b.p, b.count, b.span(), b.stride, b.esize);
 }
 
-// Clusters of `size` blocks of a kernel that a device holds at once.  Asked
-// once per kernel, device and size, before any capture.
+// Clusters of `size` blocks of a kernel that a device holds at once, possibly
+// none.  Asked once per kernel, device and size, before any capture.
 template <auto Kernel>
 gemm_status_t resident_clusters(int dev, int sm_count, int threads, int smem, int size, int &n, cudaStream_t stream) {
-    static std::atomic<int> known[b200::host::kMaxDevices][4];
+    static std::atomic<int> known[b200::host::kMaxDevices][4];      // one more than the answer
     const int slot = size >= 8 ? 3 : size >= 4 ? 2 : size >= 2 ? 1 : 0;
-    n = known[dev][slot].load(std::memory_order_relaxed);
-    if (n > 0) return GEMM_OK;
+    n = known[dev][slot].load(std::memory_order_relaxed) - 1;
+    if (n >= 0) return GEMM_OK;
     if (b200::host::capturing(stream)) return GEMM_ERR_CAPTURE;
     cudaLaunchConfig_t lc = {};
     cudaLaunchAttribute attr;
@@ -77,8 +77,7 @@ gemm_status_t resident_clusters(int dev, int sm_count, int threads, int smem, in
     lc.numAttrs = 1;
     const cudaError_t e = cudaOccupancyMaxActiveClusters(&n, Kernel, &lc);
     if (e != cudaSuccess) return b200::host::cuda_fail(e);
-    n = std::max(1, n);
-    known[dev][slot].store(n, std::memory_order_relaxed);
+    known[dev][slot].store(n + 1, std::memory_order_relaxed);
     return GEMM_OK;
 }
 
@@ -163,7 +162,7 @@ gemm_status_t launch_grouped(int dev, int sm_count, const CUtensorMap &tmP, cons
         }
     }
     if ((s = resident_clusters<kernel>(dev, sm_count, Cfg::THREADS, kMost, size, room, stream)) != GEMM_OK) return s;
-    return launch(kernel, static_cast<int>(std::min<int64_t>(room, tiles)), size, Cfg::THREADS,
+    return launch(kernel, static_cast<int>(std::min<int64_t>(std::max(room, 1), tiles)), size, Cfg::THREADS,
                   Cfg::smem_bytes(a.groups), stream, tmP, tmQ, a);
 }
 
@@ -291,7 +290,7 @@ gemm_status_t launch_fp4(int dev, int sm_count, const Fp4Call &c, cudaStream_t s
         (s = map_scales(&tmSP, c.sfb, scale_tiles(c.args.N, c.args.K, c.format), Cfg::CHUNKS)) != GEMM_OK ||
         (s = map_scales(&tmSQ, c.sfa, scale_tiles(c.args.M, c.args.K, c.format), Cfg::CHUNKS)) != GEMM_OK)
         return s;
-    return launch(kernel, static_cast<int>(std::min<int64_t>(room, tiles)), size, Cfg::THREADS, Cfg::SMEM_BYTES, stream,
+    return launch(kernel, static_cast<int>(std::min<int64_t>(std::max(room, 1), tiles)), size, Cfg::THREADS, Cfg::SMEM_BYTES, stream,
                   tmP, tmQ, tmSP, tmSQ, c.args);
 }
 

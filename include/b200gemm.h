@@ -575,7 +575,7 @@ B200GEMM_API gemm_status_t gemm_fp4(const uint8_t *A, const uint8_t *sfa, const 
                                     cudaStream_t stream);
 
 /*
- * gemm_call: one of the entry points below with its arguments in a block of 64-bit
+ * gemm_call: one of four entry points above with its arguments in a block of 64-bit
  * words, in their order (pointers, sizes and enumerators as integers, a float's
  * bits in the low half), for bindings in which a call costs by the argument.  A
  * word that its argument's type does not hold, or an unknown entry point, is
