@@ -74,8 +74,7 @@ struct GemmFp4Cfg {
     static constexpr int SMEM_BYTES = 1024 + PART_OFF + (SPLIT ? BQ * 128 * 4 : 0);
     static_assert(TMEM_COLS <= 512 && STAGE_BYTES % 1024 == 0 && SMEM_BYTES <= 232448, "it fits");
     static_assert(!SPLIT || (CG == 1 && EPI_WARPS == 4), "split: one-CTA tiles");
-    // a tile's scales start at a tile of scales, or in its middle (64); 32: one tile
-    static_assert(BQ == 32 || BQ == 64 || BQ % 128 == 0, "rows of A per tile");
+    static_assert(BQ == 64 || BQ % 128 == 0, "a tile's scales start at a tile of scales, or in its middle");
 };
 
 struct GemmFp4Args {
