@@ -49,6 +49,7 @@
 //                  rows each the write-back, 3.0 (bf16) to 4.3 TB/s (fp32).  8 experts,
 //                  1000 rows, 1024 x 512, fp32: 8.5 us
 #pragma once
+#include <climits>
 #include <cstdint>
 
 #include "columns_out.cuh"
@@ -107,7 +108,7 @@ struct GroupedArgs {
     int P, Q, K;                // P's extent (columns of the output); gradient: Q's (its rows); rows: K
     float beta;                 // gradient
     bool f32;                   // type of the output
-    int segment;                // blocks of the reduction that the tensor core sums by itself
+    int segment;                // blocks of the reduction that the tensor core sums by itself (a split's share: all)
     DeviceStatus *status;
     uint64_t timeout_ns;
 };
@@ -377,7 +378,7 @@ gemm_grouped_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_consta
                         }
                         acc = tmem_base + buf * Cfg::BQ;
                         more = 0;
-                        until = a.segment;
+                        until = members > 1 ? INT_MAX : a.segment;
                     }
                     if (!mbar_wait_warp(full_bar(stage), phase, abort_flag, a.timeout_ns)) {
                         if (issue) record_timeout(a.status, abort_flag, abort_slot, cluster, kRoleMma * 16 + kBarFull);
@@ -449,7 +450,6 @@ gemm_grouped_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_consta
         constexpr int PARTS = Cfg::EPI_WARPS / 4;               // fours of warps that share a tile's rows of the output
         constexpr int CHUNKS = Cfg::BQ / 32 / PARTS;            // of 32 rows, for each of them
         const int64_t esize = a.f32 ? 4 : 2;
-        const bool whole = a.f32 || (GRAD && a.beta != 0.0f);   // sums go through registers in fp32
         ColumnsOut to(base + Cfg::OUT_OFF, part, sub, lane, a.ld * esize);
         uint32_t done = 0;
         // the accumulator of a tile's next segment is complete
@@ -497,7 +497,9 @@ gemm_grouped_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_consta
                 release();
                 continue;
             }
-            if (!whole) {
+            // one segment whose sum is only rounded; else the sums go through registers in fp32
+            const bool packed = !a.f32 && (!GRAD || a.beta == 0.0f) && t.k_len <= a.segment * Cfg::BK;
+            if (packed) {
                 if (!to.agree(t.k_len == 0 || wait_full())) break;
                 uint32_t w[CHUNKS][16] = {};
                 if (t.k_len > 0) {
@@ -511,9 +513,9 @@ gemm_grouped_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_consta
                 }
                 continue;
             }
-            // fp32: the tensor core cuts what its sums do not hold, always towards
-            // zero, so the error grows with the length (4.5e-6 of the result at
-            // 4096); segments are added here, to nearest (5e-7)
+            // The tensor core cuts what its sums do not hold, always towards zero, so
+            // the error grows with the length (4.5e-6 of an fp32 result at 4096);
+            // segments are added here, to nearest (5e-7)
             float v[CHUNKS][32] = {};
             bool ok = true;
             for (int left = t.k_len; left > 0 && ok; left -= a.segment * Cfg::BK) {

@@ -137,9 +137,10 @@ gemm_status_t map_experts(CUtensorMap *map, const Mat &m, uint32_t box) {
                                   CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
-// Blocks of 64 that a tensor core sums by itself: all for a bf16 result, 512
-// elements for an fp32 one (gemm_grouped_kernel's epilogue).
-int segment_blocks(bool f32) { return f32 ? 8 : 1 << 24; }
+// Blocks of 64 that a tensor core sums by itself (gemm_grouped_kernel's epilogue):
+// 512 elements for an fp32 result; 2^20 for a bf16 one, whose 2^16 MMAs take off
+// 2^15 last places of the sum, 2^-8 of it, at the very most: half a step of bf16.
+int segment_blocks(bool f32) { return f32 ? 8 : 1 << 14; }
 
 constexpr int64_t kMaxTiles = int64_t(1) << 30;     // tile numbers are 32-bit, one grid's step on top
 
@@ -158,7 +159,7 @@ gemm_status_t launch_grouped(int dev, int sm_count, const CUtensorMap &tmP, cons
         const int64_t blocks = (int64_t(a.K) + Cfg::BK - 1) / Cfg::BK;
         for (size = 8; size > 1; size /= 2) {
             if ((s = resident_clusters<kernel>(dev, sm_count, Cfg::THREADS, kMost, size, room, stream)) != GEMM_OK) return s;
-            if (tiles <= room && blocks >= 8 * size && (blocks + size - 1) / size <= a.segment) break;
+            if (tiles <= room && blocks >= 8 * size && (!a.f32 || (blocks + size - 1) / size <= a.segment)) break;
         }
     }
     if ((s = resident_clusters<kernel>(dev, sm_count, Cfg::THREADS, kMost, size, room, stream)) != GEMM_OK) return s;
