@@ -145,8 +145,9 @@ struct GroupedTiles {
           band(8 * static_cast<uint32_t>(tiles_p)), per(static_cast<uint32_t>(max(tiles_p * tiles_q, 1))) {
         if (members > 1) {
             const int64_t blocks = (int64_t(a.K) + Cfg::BK - 1) / Cfg::BK;
-            k0 = static_cast<int>(blocks * me / members) * Cfg::BK;
-            k_len = min(static_cast<int>(blocks * (me + 1) / members) * Cfg::BK, a.K) - k0;
+            k0 = static_cast<int>(blocks * me / members * Cfg::BK);
+            // the last share's end may be 2^31
+            k_len = static_cast<int>(min(blocks * (me + 1) / members * Cfg::BK, static_cast<int64_t>(a.K)) - k0);
         }
     }
 

@@ -9,6 +9,7 @@ from dense_gemm_engineering_bf16_b200 import gemm as G
 from operator_refs import BF16, F32, TORCH
 
 pytestmark = pytest.mark.gpu
+MOST = (1 << 31) - 1
 
 
 def ends_of(sizes):
@@ -43,6 +44,21 @@ def test_rows_past_a_million_products(c_type):
     want = torch.full((3, N), K + 3.0, device="cuda")
     want[:, 5] += 8
     assert torch.equal(c, want.to(TORCH[c_type]))
+
+
+def test_rows_of_the_longest_reduction():
+    """K = 2^31 - 1, split over a cluster: shares end at the ends of their type."""
+    a = torch.zeros(1, MOST + 1, dtype=torch.bfloat16, device="cuda")
+    b = torch.zeros(2, MOST + 1, dtype=torch.bfloat16, device="cuda")
+    at = [0, 63, 64, (1 << 28) - 1, 1 << 28, (1 << 30) + 5, 7 * (1 << 28), MOST - 64, MOST - 1]
+    a[0, at] = torch.arange(1.0, 1.0 + len(at), device="cuda").bfloat16()
+    b[0, at], b[1, at[-1]] = 1.0, 3.0
+    a[0, MOST] = b[:, MOST] = float("nan")            # of the pitch
+    for c_type in (BF16, F32):
+        c = torch.empty(1, 8, dtype=TORCH[c_type], device="cuda")
+        G.gemm_bf16_grouped(a, b, ends_of([1]), c, 1, 1, 2, MOST, MOST + 1, MOST + 1, 0, 8, c_type)
+        G.gemm_check_device_status()
+        assert c[0, :2].tolist() == [45.0, 27.0]
 
 
 @pytest.mark.parametrize("d_type", [BF16, F32])
