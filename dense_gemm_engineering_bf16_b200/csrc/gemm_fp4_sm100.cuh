@@ -342,7 +342,9 @@ gemm_fp4_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__
                         record_timeout(a.status, abort_flag, abort_slot, cluster, kRoleEpilogue * 16 + kBarRxFull);
                         got = 0;
                     }
-                    return __shfl_sync(0xFFFFFFFFu, got, 0) != 0;
+                    got = __shfl_sync(0xFFFFFFFFu, got, 0);
+                    __syncwarp();   // the other members' stores are visible to every lane
+                    return got != 0;
                 };
                 if (!cluster_sum(acc, mma_n(tq) / 4, static_cast<int>(members), static_cast<int>(me), sub * 32u + lane,
                                  base + Cfg::PART_OFF, received_bar, wait, out + mine * esize, to.ld_bytes, count,

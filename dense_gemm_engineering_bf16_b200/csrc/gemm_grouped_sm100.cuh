@@ -427,6 +427,7 @@ gemm_grouped_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_consta
                 ready = 0;
             }
             ready = __shfl_sync(0xFFFFFFFFu, ready, 0);
+            __syncwarp();       // the copies' bytes are visible to every lane
             if (!ready) break;
             parity ^= 1u << stage;
             // a row of a box is 128 bytes, swizzled within itself
@@ -461,6 +462,7 @@ gemm_grouped_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_consta
                 ready = 0;
             }
             ready = __shfl_sync(0xFFFFFFFFu, ready, 0);
+            __syncwarp();       // the MMAs' completion holds for every lane
             tc_fence_after_sync();
             return ready != 0;
         };
@@ -489,7 +491,9 @@ gemm_grouped_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_consta
                         record_timeout(a.status, abort_flag, abort_slot, cluster, kRoleEpilogue * 16 + kBarRxFull);
                         got = 0;
                     }
-                    return __shfl_sync(0xFFFFFFFFu, got, 0) != 0;
+                    got = __shfl_sync(0xFFFFFFFFu, got, 0);
+                    __syncwarp();   // the other members' stores are visible to every lane
+                    return got != 0;
                 };
                 const int c = static_cast<int>(sub * 32u + lane);
                 if (!wait_full() || !cluster_sum(from(0), t.n / 4, members, me, c, base + Cfg::PART_OFF, received_bar, wait,
