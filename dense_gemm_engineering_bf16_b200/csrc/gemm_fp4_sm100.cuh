@@ -337,14 +337,9 @@ gemm_fp4_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__
             };
             if (Cfg::SPLIT && members > 1) {
                 auto wait = [&]() {
-                    uint32_t got = 1;
-                    if (lane == 0 && !mbar_wait(received_bar, 0, abort_flag, 3 * a.timeout_ns)) {
-                        record_timeout(a.status, abort_flag, abort_slot, cluster, kRoleEpilogue * 16 + kBarRxFull);
-                        got = 0;
-                    }
-                    got = __shfl_sync(0xFFFFFFFFu, got, 0);
-                    __syncwarp();   // the other members' stores are visible to every lane
-                    return got != 0;
+                    if (mbar_wait_warp(received_bar, 0, abort_flag, 3 * a.timeout_ns)) return true;
+                    if (lane == 0) record_timeout(a.status, abort_flag, abort_slot, cluster, kRoleEpilogue * 16 + kBarRxFull);
+                    return false;
                 };
                 if (!cluster_sum(acc, mma_n(tq) / 4, static_cast<int>(members), static_cast<int>(me), sub * 32u + lane,
                                  base + Cfg::PART_OFF, received_bar, wait, out + mine * esize, to.ld_bytes, count,

@@ -421,14 +421,10 @@ gemm_grouped_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_consta
             blocks += parts_of(t.k_len, Cfg::BK);
             if (t.k_len % 16 == 0) continue;
             const uint32_t stage = (blocks - 1) % STAGES;
-            uint32_t ready = 1;
-            if (lane == 0 && !mbar_wait(fix_bar(stage), (parity >> stage) & 1u, abort_flag, 3 * a.timeout_ns)) {
-                record_timeout(a.status, abort_flag, abort_slot, cluster, kRoleFix * 16 + kBarFix);
-                ready = 0;
+            if (!mbar_wait_warp(fix_bar(stage), (parity >> stage) & 1u, abort_flag, 3 * a.timeout_ns)) {
+                if (lane == 0) record_timeout(a.status, abort_flag, abort_slot, cluster, kRoleFix * 16 + kBarFix);
+                break;
             }
-            ready = __shfl_sync(0xFFFFFFFFu, ready, 0);
-            __syncwarp();       // the copies' bytes are visible to every lane
-            if (!ready) break;
             parity ^= 1u << stage;
             // a row of a box is 128 bytes, swizzled within itself
             const int used = t.k_len % Cfg::BK, clear = (16 - used % 16) * 128;
@@ -456,15 +452,10 @@ gemm_grouped_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_consta
         uint32_t done = 0;
         // the accumulator of a tile's next segment is complete
         auto wait_full = [&]() {
-            uint32_t ready = 1;
-            if (lane == 0 && !mbar_wait(tfull_bar(done & 1u), (done >> 1) & 1u, abort_flag, 3 * a.timeout_ns)) {
-                record_timeout(a.status, abort_flag, abort_slot, cluster, kRoleEpilogue * 16 + kBarTmemFull);
-                ready = 0;
-            }
-            ready = __shfl_sync(0xFFFFFFFFu, ready, 0);
-            __syncwarp();       // the MMAs' completion holds for every lane
+            const bool ready = mbar_wait_warp(tfull_bar(done & 1u), (done >> 1) & 1u, abort_flag, 3 * a.timeout_ns);
+            if (!ready && lane == 0) record_timeout(a.status, abort_flag, abort_slot, cluster, kRoleEpilogue * 16 + kBarTmemFull);
             tc_fence_after_sync();
-            return ready != 0;
+            return ready;
         };
         auto release = [&]() {
             tc_fence_before_sync();
@@ -486,14 +477,9 @@ gemm_grouped_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_consta
             };
             if (Cfg::SPLIT && members > 1) {
                 auto wait = [&]() {
-                    uint32_t got = 1;
-                    if (lane == 0 && !mbar_wait(received_bar, 0, abort_flag, 3 * a.timeout_ns)) {
-                        record_timeout(a.status, abort_flag, abort_slot, cluster, kRoleEpilogue * 16 + kBarRxFull);
-                        got = 0;
-                    }
-                    got = __shfl_sync(0xFFFFFFFFu, got, 0);
-                    __syncwarp();   // the other members' stores are visible to every lane
-                    return got != 0;
+                    if (mbar_wait_warp(received_bar, 0, abort_flag, 3 * a.timeout_ns)) return true;
+                    if (lane == 0) record_timeout(a.status, abort_flag, abort_slot, cluster, kRoleEpilogue * 16 + kBarRxFull);
+                    return false;
                 };
                 const int c = static_cast<int>(sub * 32u + lane);
                 if (!wait_full() || !cluster_sum(from(0), t.n / 4, members, me, c, base + Cfg::PART_OFF, received_bar, wait,

@@ -121,7 +121,8 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity,
     return true;
 }
 
-// The same by all lanes of a warp, which get one answer.  A loop that issues
+// The same by all lanes of a warp, which get one answer; each has acquired what
+// the barrier's arrivals released, so each may read it.  A loop that issues
 // TMA copies or MMAs keeps its operands in uniform registers only where the
 // whole warp runs it, with elect_one around the instructions themselves: inside a
 // branch of one lane they are moved there one by one, about 200 cycles an MMA.
