@@ -159,6 +159,25 @@ __device__ __forceinline__ void store_columns(uint8_t *c, int64_t ld_bytes, int 
     }
 }
 
+// What sums are multiplied with: ga gb in fp32, except where fp32 would not hold
+// that as a normal number (scales are from 2^-100 to 2^100).  Then 2^-100 or
+// 2^100 of it come second, so that a sum of zero stays zero and one that brings
+// the result back into range is not lost.
+struct Factor {
+    float first, second;    // second: else 1
+
+    __device__ __forceinline__ Factor(float ga, float gb) : first(ga * gb), second(1.0f) {
+        if (fabsf(first) < 0x1p-126f) {
+            first = ga * 0x1p100f * gb;
+            second = 0x1p-100f;
+        } else if (fabsf(first) > 0x1.fffffep127f) {
+            first = ga * 0x1p-100f * gb;
+            second = 0x1p100f;
+        }
+    }
+    __device__ __forceinline__ float operator()(float sum) const { return sum * first * second; }
+};
+
 // Sum over a cluster's members, each of which has the same rows x 128 of C over
 // its share of the reduction in TMEM at `acc` (the warp's quarter): `fours` times
 // four rows, the first `count` rows are C's.  Member o sums the fours [o share,
@@ -169,7 +188,7 @@ __device__ __forceinline__ void store_columns(uint8_t *c, int64_t ld_bytes, int 
 template <class Wait>
 __device__ __forceinline__ bool cluster_sum(uint32_t acc, int fours, int members, int me, uint32_t column, uint32_t parts,
                                             uint32_t received, Wait wait, uint8_t *c, int64_t ld_bytes, int count,
-                                            bool mine, bool f32, float alpha) {
+                                            bool mine, bool f32, Factor scale) {
     const int share = (fours + members - 1) / members;
     for (int f = 0; f < fours; f += 8) {
         uint32_t r[32];
@@ -199,7 +218,7 @@ __device__ __forceinline__ bool cluster_sum(uint32_t acc, int fours, int members
             for (int i = 0; i < 4; ++i) sum[i] += __uint_as_float(x[i]);
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) sum[i] *= alpha;
+        for (int i = 0; i < 4; ++i) sum[i] = scale(sum[i]);
         store_columns<4>(c + 4 * f * ld_bytes, ld_bytes, count - 4 * f, mine, f32, 0.0f, sum);
     }
     return true;

@@ -78,7 +78,7 @@ struct GemmFp4Cfg {
 };
 
 struct GemmFp4Args {
-    const float *ga, *gb;       // null: 1
+    const float *ga, *gb;       // NV; null: 1
     void *c;
     int64_t ldc;
     int M, N, K;
@@ -87,6 +87,48 @@ struct GemmFp4Args {
     DeviceStatus *status;
     uint64_t timeout_ns;
 };
+
+// The epilogue of scales whose product needs a second factor.  Apart from the
+// ordinary one, which a branch or that factor slowed down by 1 to 1.5 %.
+template <class Cfg>
+__device__ __noinline__ void fp4_far_tiles(GemmFp4Args a, Factor scale, uint32_t tmem_base, uint32_t tfull, uint32_t tempty,
+                                           volatile uint32_t *abort_flag, uint32_t abort_slot, int first, int step,
+                                           uint32_t rank) {
+    constexpr int FOURS = Cfg::EPI_WARPS / 4;
+    const uint32_t warp = threadIdx.x / 32, lane = threadIdx.x % 32, sub = warp & 3u;
+    const int part = static_cast<int>(warp - Cfg::EPI0) / 4;
+    const int tiles_p = parts_of(a.N, Cfg::BP), tiles_q = parts_of(a.M, Cfg::BQ);
+    const int64_t esize = a.f32 ? 4 : 2, ld_bytes = a.ldc * esize;
+    uint32_t done = 0;
+    for (int tile = first; tile < tiles_p * tiles_q; tile += step, ++done) {
+        int tq, tp;
+        raster_tile(tile, tiles_q, tiles_p, 8, tq, tp);
+        const uint32_t buf = done % Cfg::ACC_BUFS;
+        if (!mbar_wait_warp(tfull + 8u * buf, (done / Cfg::ACC_BUFS) & 1u, abort_flag, 3 * a.timeout_ns)) {
+            if (lane == 0) record_timeout(a.status, abort_flag, abort_slot, Cfg::CG, kRoleEpilogue * 16 + kBarTmemFull);
+            break;
+        }
+        tc_fence_after_sync();
+        const int64_t col = int64_t(tp) * Cfg::BP + rank * Cfg::BP_CTA + sub * 32u + lane;
+        uint8_t *out = static_cast<uint8_t *>(a.c) + (static_cast<int64_t>(tq) * Cfg::BQ * a.ldc + col) * esize;
+#pragma unroll 1
+        for (int j = 32 * part; j < Cfg::BQ; j += 32 * FOURS) {
+            uint32_t r[32];
+            float v[32];
+            tmem_ld_32x32b_x32(tmem_base + ((sub * 32u) << 16) + buf * Cfg::BQ + j, r);
+            tmem_ld_wait();
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = scale(__uint_as_float(r[i]));
+            store_columns<32>(out + j * ld_bytes, ld_bytes, min(Cfg::BQ, a.M - tq * Cfg::BQ) - j, col < a.N, a.f32, 0.0f, v);
+        }
+        tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) {
+            if (Cfg::CG == 1) mbar_arrive_local(tempty + 8u * buf);
+            else mbar_arrive_cluster(map_to_cta(tempty + 8u * buf, 0));
+        }
+    }
+}
 
 template <class Cfg>
 __global__ void __launch_bounds__(Cfg::THREADS, 1)
@@ -305,12 +347,16 @@ gemm_fp4_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__
         const int part = static_cast<int>(warp - Cfg::EPI0) / 4;
         constexpr int PARTS = Cfg::EPI_WARPS / 4;               // fours of warps that share a tile's rows of C
         constexpr int CHUNKS = Cfg::BQ / 32 / PARTS;            // of 32 rows, for each of them
-        const float alpha = (a.ga ? __ldcg(a.ga) : 1.0f) * (a.gb ? __ldcg(a.gb) : 1.0f);
+        const Factor scale(Cfg::NV && a.ga ? __ldcg(a.ga) : 1.0f, Cfg::NV && a.gb ? __ldcg(a.gb) : 1.0f);
+        const float alpha = scale.first;
         const int64_t esize = a.f32 ? 4 : 2;
         ColumnsOut to(base + Cfg::OUT_OFF, part, sub, lane, a.ldc * esize);
         const int mine = static_cast<int>(sub * 32u + lane);   // this lane's column
         uint32_t done = 0;
-        for (int tile = first; tile < num_tiles; tile += step, ++done) {
+        const bool far = Cfg::NV && scale.second != 1.0f && members == 1;
+        if (far)
+            fp4_far_tiles<Cfg>(a, scale, tmem_base, tfull_bar(0), tempty_bar(0), abort_flag, abort_slot, first, step, rank);
+        for (int tile = far ? num_tiles : first; tile < num_tiles; tile += step, ++done) {
             int tq, tp;
             raster_tile(tile, tiles_q, tiles_p, 8, tq, tp);
             const uint32_t buf = done % Cfg::ACC_BUFS;
@@ -343,7 +389,7 @@ gemm_fp4_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__
                 };
                 if (!cluster_sum(acc, mma_n(tq) / 4, static_cast<int>(members), static_cast<int>(me), sub * 32u + lane,
                                  base + Cfg::PART_OFF, received_bar, wait, out + mine * esize, to.ld_bytes, count,
-                                 mine < to.cols, a.f32, alpha))
+                                 mine < to.cols, a.f32, scale))
                     break;
                 release();
                 continue;

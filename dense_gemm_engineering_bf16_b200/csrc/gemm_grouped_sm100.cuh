@@ -483,7 +483,7 @@ gemm_grouped_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_consta
                 };
                 const int c = static_cast<int>(sub * 32u + lane);
                 if (!wait_full() || !cluster_sum(from(0), t.n / 4, members, me, c, base + Cfg::PART_OFF, received_bar, wait,
-                                                 out + c * esize, to.ld_bytes, t.count, c < to.cols, a.f32, 1.0f))
+                                                 out + c * esize, to.ld_bytes, t.count, c < to.cols, a.f32, Factor(1.0f, 1.0f)))
                     break;
                 release();
                 continue;

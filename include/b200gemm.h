@@ -560,13 +560,14 @@ B200GEMM_API gemm_status_t gemm_fp4_quantize(const void *X, const float *scale, 
  *   C[i][j] = ga gb sum_k (a_ik sa_i,k/block) (b_jk sb_j,k/block)
  *
  *   A, sfa, scale_a   M x lda bytes of codes, their scales, NV: the matrix's
- *                     scale (on the device; NULL: 1.  MX: NULL)
+ *                     scale (one float on the device, as in gemm_fp4_quantize;
+ *                     NULL: 1.  MX: NULL)
  *   B, sfb, scale_b   the same, N x ldb (stored K-major)
  *   C                 M x N of c_type
  * Both operands have the same format.  K must be a multiple of 32, lda and ldb
  * of 16, all pointers to codes, scales and C 16-byte aligned.  Products are exact,
- * sums fp32 in a fixed order, times ga gb in fp32, rounded once.  C overlaps no
- * input.  M == 0 or N == 0: nothing to do; K == 0: C = 0.  One kernel, no
+ * sums fp32 in a fixed order, times ga gb in fp32, rounded once (ga gb may be
+ * beyond fp32's range as long as C is not).  C overlaps no input.  M == 0 or N == 0: nothing to do; K == 0: C = 0.  One kernel, no
  * workspace; the status block and the watchdog as for the products.
  */
 B200GEMM_API gemm_status_t gemm_fp4(const uint8_t *A, const uint8_t *sfa, const float *scale_a, const uint8_t *B,
