@@ -371,7 +371,7 @@ _GROUPED, _WGRAD, _QUANTIZE, _FP4 = (struct.Struct(f).pack for f in ("<15q", "<1
 def _call(entry: int, pack, *words) -> int:
     try:
         return lib.gemm_call(entry, pack(*words))
-    except struct.error as e:       # no number, or none that a word holds
+    except (struct.error, OverflowError, TypeError) as e:       # no number, or none that a word or an fp32 holds
         raise GemmError(1, str(e)) from e
 
 

@@ -567,8 +567,9 @@ B200GEMM_API gemm_status_t gemm_fp4_quantize(const void *X, const float *scale, 
  * Both operands have the same format.  K must be a multiple of 32, lda and ldb
  * of 16, all pointers to codes, scales and C 16-byte aligned.  Products are exact,
  * sums fp32 in a fixed order, times ga gb in fp32, rounded once (ga gb may be
- * beyond fp32's range as long as C is not).  C overlaps no input.  M == 0 or N == 0: nothing to do; K == 0: C = 0.  One kernel, no
- * workspace; the status block and the watchdog as for the products.
+ * beyond fp32's range as long as C is not).  C overlaps no input.  M == 0 or N
+ * == 0: nothing to do; K == 0: C = 0.  One kernel, no workspace; the status block
+ * and the watchdog as for the products.
  */
 B200GEMM_API gemm_status_t gemm_fp4(const uint8_t *A, const uint8_t *sfa, const float *scale_a, const uint8_t *B,
                                     const uint8_t *sfb, const float *scale_b, void *C, int64_t M, int64_t N, int64_t K,
