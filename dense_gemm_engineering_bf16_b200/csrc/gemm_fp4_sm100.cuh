@@ -12,8 +12,8 @@
 //          the scale tiles of both
 //   1      MMA issuer (of the pair's leader), owner of TMEM: four MMAs of K = 64
 //          a stage
-//   2      scale copier: a stage's scale tiles into one of four TMEM slots,
-//          ahead of the MMAs and ordered with them by barriers only
+//   2      scale copier: a stage's scale tiles into one of four to eight TMEM
+//          slots, ahead of the MMAs and ordered with them by barriers only
 //   3 on   epilogue (columns_out.cuh)
 //
 // Scales in TMEM: a tile of 128 rows x 4 scales becomes four columns (column
@@ -31,7 +31,8 @@
 // cycles instead of the 64 that its size would take: 512 x 4096 x 4096 8.8 us.
 // Few rows: memory and the start and end (3.6 us without any work): one row of
 // 8192 x 8192, 37.8 MB, 11.4 us; 64 rows 14.3.
-// Fewer scale slots cost time (two: 20 %), more than five gain nothing.
+// Fewer scale slots cost time (two: 20 %); beyond five nothing changes, and pairs
+// take what TMEM has left, five (NV) or eight (MX).
 #pragma once
 #include <cstdint>
 
@@ -74,7 +75,8 @@ struct GemmFp4Cfg {
     static constexpr int SMEM_BYTES = 1024 + PART_OFF + (SPLIT ? BQ * 128 * 4 : 0);
     static_assert(TMEM_COLS <= 512 && STAGE_BYTES % 1024 == 0 && SMEM_BYTES <= 232448, "it fits");
     static_assert(!SPLIT || (CG == 1 && EPI_WARPS == 4), "split: one-CTA tiles");
-    static_assert(BQ == 64 || BQ % 128 == 0, "a tile's scales start at a tile of scales, or in its middle");
+    static constexpr bool ONE_TILE_M = BQ == 64;            // at most BQ rows of A: one tile along M
+    static_assert(ONE_TILE_M || BQ % 128 == 0, "a tile's scales start at a tile of scales");
 };
 
 struct GemmFp4Args {
@@ -261,8 +263,6 @@ gemm_fp4_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__
                     break;
                 }
                 const uint32_t acc = tmem_base + buf * Cfg::BQ;
-                // a tile of 64 rows of A may be the second half of its scales' 128
-                const uint32_t q_col = Cfg::BQ == 64 ? 2u * (tq & 1) : 0u;
                 for (int kb = kb0; kb < kb1; ++kb) {
                     const uint32_t slot = n % Cfg::SF_SLOTS;
                     // the copier waited for the stage's bytes before it copied them
@@ -277,7 +277,7 @@ gemm_fp4_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__
                         const uint64_t p_desc = p_desc0 + (stage * Cfg::STAGE_BYTES >> 4);
                         const uint64_t q_desc = q_desc0 + (stage * Cfg::STAGE_BYTES >> 4);
                         const uint32_t sp = tmem_base + Cfg::SF_COL0 + slot * Cfg::SLOT_COLS;
-                        const uint32_t sq = sp + 4 * Cfg::CHUNKS + q_col;
+                        const uint32_t sq = sp + 4 * Cfg::CHUNKS;
                         const int left = a.K - kb * Cfg::BK;
 #pragma unroll
                         for (int j = 0; j < Cfg::MMAS; ++j) {

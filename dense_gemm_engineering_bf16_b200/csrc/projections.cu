@@ -271,7 +271,7 @@ template <class Cfg>
 gemm_status_t launch_fp4(int dev, int sm_count, const Fp4Call &c, cudaStream_t stream) {
     constexpr auto kernel = b200::gemm_fp4_kernel<Cfg>;
     const int64_t tiles = ((int64_t(c.args.N) + Cfg::BP - 1) / Cfg::BP) * ((int64_t(c.args.M) + Cfg::BQ - 1) / Cfg::BQ);
-    if (tiles > kMaxTiles) return GEMM_ERR_TOO_LARGE;
+    if (tiles > kMaxTiles || (Cfg::ONE_TILE_M && c.args.M > Cfg::BQ)) return GEMM_ERR_TOO_LARGE;
     gemm_status_t s;
     if ((s = b200::host::prepare<kernel>(dev, Cfg::SMEM_BYTES, stream)) != GEMM_OK) return s;
     int size = Cfg::CG, room;
