@@ -27,7 +27,8 @@
 //
 // SPLIT, for the few rows of a token: a cluster of 2, 4 or 8 CTAs owns a tile,
 // each over a share of K, and their partials meet in distributed shared memory
-// (cluster_sum).  One tile per cluster.
+// (cluster_sum).  One tile per cluster.  A share is one accumulator's sum, so
+// with an fp32 result no longer than a segment: K of about 1024, 2048 or 4096.
 //
 // Every CTA works out the tiles from `ends` itself: the numbers of tiles up to
 // each expert in shared memory, a binary search per tile.  Rows outside every
@@ -44,10 +45,14 @@
 //   one token      the start and the end (3.4 us without any work; a pair of CTAs 6)
 //                  and the ramp between: 2 of 8 experts of 4096 x 2048, 33.6 MB,
 //                  10.9 us
-//   gradient       of 32 experts, 512 rows each, 4096 x 2048, bf16: 273 us, the L2
-//                  bandwidth that operands (2.1 GB) and results share; with a few
-//                  rows each the write-back, 3.0 (bf16) to 4.3 TB/s (fp32).  8 experts,
-//                  1000 rows, 1024 x 512, fp32: 8.5 us
+//   gradient       the write-back, of 256 x 256 values for each few blocks of MMAs:
+//                  32 experts, 512 rows each, 4096 x 2048, bf16 261 us, of which the
+//                  stores are 41 and taking the accumulators out 44 (218 without the
+//                  operands' loads); 64 experts, 256 rows each 401 us, stores 74,
+//                  accumulators 129 (371 without loads).  8 experts, 1000 rows, 1024 x
+//                  512, fp32: 8.2 us
+// The pairs' rows kernels spill 44 bytes a thread, at the 168 registers that 320
+// threads leave.
 #pragma once
 #include <climits>
 #include <cstdint>
@@ -488,7 +493,7 @@ gemm_grouped_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_consta
                 release();
                 continue;
             }
-            // one segment whose sum is only rounded; else the sums go through registers in fp32
+            // one segment whose sum is only rounded; otherwise sums go through registers in fp32
             const bool packed = !a.f32 && (!GRAD || a.beta == 0.0f) && t.k_len <= a.segment * Cfg::BK;
             if (packed) {
                 if (!to.agree(t.k_len == 0 || wait_full())) break;

@@ -194,7 +194,7 @@ template <bool PMN>
 gemm_status_t dispatch_rows(int dev, int sm_count, const Mat &A, const Mat &B, const b200::GroupedArgs &a,
                             cudaStream_t stream) {
     // Tiles of 64 rows for few rows an expert, or for tiles so few that K is
-    // split.  Then single CTAs of 128 x 128 or pairs of 256 x 256, whichever is
+    // split (for an fp32 result where launch_grouped can).  Then single CTAs of 128 x 128 or pairs of 256 x 256, whichever is
     // predicted faster: a fixed cost, and per wave one of its own and one per 64
     // of K, in us (K = 2048, N = 2048, skewed, 64-row tiles, single, pair: 8 experts,
     // 64 rows 15.1 15.1 16.6; 512 rows 21.0 16.5 18.0; 4000 rows 60 40 37; 64 experts,
