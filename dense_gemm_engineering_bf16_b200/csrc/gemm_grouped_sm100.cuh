@@ -103,6 +103,9 @@ struct GroupedCfg {
     static_assert(BQ >= 32 && BQ <= 256, "the epilogue reads 32 columns at a time");
     static_assert(!SPLIT || (CG == 1 && EPI_WARPS == 4 && MODE == kGroupedRows), "split: one-CTA tiles of rows");
     static_assert(smem_bytes(kMaxGroups) <= 232448, "dynamic shared memory per CTA on sm_100");
+    // wait_for_stream lets the next kernel's blocks come while TMEM is still being
+    // allocated here: one that allocates as well may not fit beside this one
+    static_assert(smem_bytes(0) > 233472 / 2, "more than half of an SM's shared memory");
 };
 
 struct GroupedArgs {
